@@ -28,8 +28,11 @@ MOE_DEV_OK, MOE_DEV_WAIT_TIMEOUT = 0, 1
 EXPORTS = ("moe_status_string", "moe_abi_version", "moe_validate_cfg", "moe_query_sizes",
            "moe_prepare_weights", "moe_route", "moe_dispatch_layout", "moe_layer_fwd",
            "moe_layer_bwd", "moe_read_device_status", "moe_mx_quantize", "moe_timing_enable",
-           "moe_timing_read", "moe_diag_mfma_loop", "moe_layer_fwd_static")
+           "moe_timing_read", "moe_diag_mfma_loop", "moe_layer_fwd_static", "moe_mx_dequantize",
+           "moe_add_rmsnorm_fwd", "moe_add_rmsnorm_bwd", "moe_query_add_rmsnorm_bwd", "moe_layer_fwd_few",
+           "moe_query_few")
 MOE_STATIC_WORKSPACE_BYTES = 256 << 20
+MOE_FEW_MAX_TOKENS = 64
 KERNEL_KINDS = ("route", "layout", "gemm_gate_up", "gemm_down", "combine", "gather", "other", "wgrad",
                 "dgrad_down", "dgrad_gate_up", "shared_gemm", "layer")
 
@@ -93,6 +96,13 @@ def _load():
             "moe_timing_read": (ctypes.c_int, [ctypes.POINTER(moe_kernel_times)]),
             "moe_diag_mfma_loop": (ctypes.c_int, [I32, P, ctypes.c_int64, I32, I32, P, P, P]),
             "moe_layer_fwd_static": (ctypes.c_int, [cfgp, ctypes.POINTER(moe_weights), P, P, P, P]),
+            "moe_mx_dequantize": (ctypes.c_int, [P, P, ctypes.c_int64, I32, I32, P, P]),
+            "moe_add_rmsnorm_fwd": (ctypes.c_int, [ctypes.c_int64, I32, P, P, P, ctypes.c_float, P, P, P, P, P, P, P,
+                                                   P]),
+            "moe_query_add_rmsnorm_bwd": (ctypes.c_int, [ctypes.c_int64, I32, ctypes.POINTER(SZ)]),
+            "moe_add_rmsnorm_bwd": (ctypes.c_int, [ctypes.c_int64, I32, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "moe_layer_fwd_few": (ctypes.c_int, [cfgp, ctypes.POINTER(moe_weights), P, P, P, P, P, SZ, P]),
+            "moe_query_few": (ctypes.c_int, [cfgp, ctypes.POINTER(SZ)]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -200,6 +210,117 @@ def moe_mx_quantize(src, codes, scales, stream=None):
     rows, cols = src.shape
     _check("moe_mx_quantize", _load().moe_mx_quantize(_ptr(src), rows, cols, _ptr(codes), _ptr(scales),
                                                       _stream(stream)))
+
+
+def _dense(fn, like, **tensors):
+    """The pointers of dense tensors on one device, by (tensor, dtype, elements); None stays None.
+
+    The kernels see pointers only, so a tensor of another type, with strides,
+    too small or on another device is refused here."""
+    device = like.device
+    out = []
+    for t, dtype, n in tensors.values():
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.device != device:
+            raise MoeError(fn, MOE_E_INVALID)
+        out.append(t.data_ptr())
+    return out
+
+
+class _On:
+    """The device of `t` as the current one (a launch goes to the current
+    device's queues), and the stream as an integer: the given one, or that
+    device's current stream."""
+
+    def __init__(self, t, stream):
+        import torch
+        self.guard = None
+        if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(t.device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def moe_mx_dequantize(codes, scales, dst, operand_scales=False, stream=None):
+    """dst (bf16) = the values of codes [rows, cols] and their scales: [rows, cols/32], or with
+    operand_scales the GEMM operand layout [ceil(cols/128), rows, 4]."""
+    import torch
+    rows, cols = codes.shape
+    u8 = torch.uint8
+    n_scales = (cols + 127) // 128 * rows * 4 if operand_scales else rows * (cols // 32)
+    p = _dense("moe_mx_dequantize", codes, codes=(codes, u8, 0), scales=(scales, u8, n_scales),
+               dst=(dst, torch.bfloat16, rows * cols))
+    with _On(codes, stream) as s:
+        _check("moe_mx_dequantize", _load().moe_mx_dequantize(p[0], p[1], rows, cols, 1 if operand_scales else 0, p[2],
+                                                              s))
+
+
+def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd=None, y_codes=None, y_scales=None,
+                        ck_codes=None, ck_scales=None, stream=None):
+    """y = rmsnorm(x + residual) * weight over the rows of x [rows, cols]; see include/moe.h for the
+    optional outputs (the sum, 1/rms, the MXFP8 form of y, the 8-bit checkpoint of the sum)."""
+    import torch
+    fn = "moe_add_rmsnorm_fwd"
+    rows, cols = x.shape
+    n, b16, f32, u8 = rows * cols, torch.bfloat16, torch.float32, torch.uint8
+    p = _dense(fn, x, x=(x, b16, n), residual=(residual, b16, n), weight=(weight, f32, cols),
+               summed=(summed, b16, n), y=(y, b16, n), rstd=(rstd, f32, rows), yc=(y_codes, u8, n),
+               ys=(y_scales, u8, (cols + 127) // 128 * rows * 4), cc=(ck_codes, u8, n),
+               cs=(ck_scales, u8, rows * (cols // 32)))
+    with _On(x, stream) as s:
+        _check(fn, _load().moe_add_rmsnorm_fwd(rows, cols, p[0], p[1], p[2], eps, *p[3:], s))
+
+
+def moe_query_add_rmsnorm_bwd(rows, cols) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_query_add_rmsnorm_bwd", _load().moe_query_add_rmsnorm_bwd(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def moe_add_rmsnorm_bwd(dy, weight, rstd, dx, dweight, ws, summed=None, ck_codes=None, ck_scales=None, dsum=None,
+                        stream=None):
+    """dx and dweight of moe_add_rmsnorm_fwd, from the sum or from its 8-bit checkpoint."""
+    import torch
+    fn = "moe_add_rmsnorm_bwd"
+    rows, cols = dy.shape
+    n, b16, f32, u8 = rows * cols, torch.bfloat16, torch.float32, torch.uint8
+    p = _dense(fn, dy, dy=(dy, b16, n), dsum=(dsum, b16, n), summed=(summed, b16, n),
+               cc=(ck_codes, u8, n), cs=(ck_scales, u8, rows * (cols // 32)), weight=(weight, f32, cols),
+               rstd=(rstd, f32, rows), dx=(dx, b16, n), dw=(dweight, f32, cols), ws=(ws, u8, 0))
+    with _On(dy, stream) as s:
+        _check(fn, _load().moe_add_rmsnorm_bwd(rows, cols, *p, ws.numel(), s))
+
+
+def moe_query_few(cfg: moe_cfg) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_query_few", _load().moe_query_few(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=None, stream=None):
+    """Layer forward for cfg.T <= MOE_FEW_MAX_TOKENS tokens; ws: moe_query_few bytes, its first 256 zeroed
+    once."""
+    import torch
+    fn = "moe_layer_fwd_few"
+    T, H, E = cfg.T, cfg.H, cfg.E
+    b16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    p = _dense(fn, x, Wr=(Wr, f32, H * E), bias=(bias, f32, E), packed=(packed, u8, 0), x=(x, b16, T * H),
+               xc=(x_codes, u8, T * H), xs=(x_scales, u8, (H + 127) // 128 * T * 4), out=(out, b16, T * H),
+               ws=(ws, u8, 0))
+    w = moe_weights(p[0], p[1], p[2], packed.numel())
+    with _On(x, stream) as s:
+        _check(fn, _load().moe_layer_fwd_few(ctypes.byref(cfg), ctypes.byref(w), p[3], p[4], p[5], p[6], p[7],
+                                             ws.numel(), s))
 
 
 def moe_diag_mfma_loop(kind, operands, blocks, iters, clocks, sink, stream=None):

@@ -930,6 +930,157 @@ moe_status moe_mx_quantize(const uint16_t* src, int64_t rows, int32_t cols, uint
     return check_launch();
 }
 
+moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                             int32_t operand_scales, uint16_t* dst, void* stream) {
+    if (!codes || !scales || !dst || rows < 1 || cols < 32 || cols % 32) return MOE_E_INVALID;
+    if (operand_scales != 0 && operand_scales != 1) return MOE_E_INVALID;
+    if (!aligned(codes, 16) || !aligned(dst, 16)) return MOE_E_INVALID;
+    if (rows >= (1ll << 35) / cols) return MOE_E_UNSUPPORTED;  // one thread per 16 codes, a 32-bit grid
+    launch_mx_dequant(codes, scales, rows, cols, operand_scales, dst, (hipStream_t)stream);
+    return check_launch();
+}
+
+// Limits of the norm's sizes (a row in a workgroup's registers, a 32-bit grid).
+static moe_status check_norm(int64_t rows, int32_t cols) {
+    if (rows < 1 || cols < 32 || cols % 32) return MOE_E_INVALID;
+    if (cols > kNormMaxCols || rows > (1 << 21)) return MOE_E_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status moe_add_rmsnorm_fwd(int64_t rows, int32_t cols, const uint16_t* x, const uint16_t* residual,
+                               const float* weight, float eps, uint16_t* summed, uint16_t* y, float* rstd,
+                               uint8_t* y_codes, uint8_t* y_scales, uint8_t* ck_codes, uint8_t* ck_scales,
+                               void* stream) {
+    moe_status st = check_norm(rows, cols);
+    if (st != MOE_OK) return st;
+    if (!x || !weight || !y || !(eps >= 0.0f) || summed == y) return MOE_E_INVALID;
+    if (!y_codes != !y_scales || !ck_codes != !ck_scales) return MOE_E_INVALID;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(summed, 16) || !aligned(y, 16) ||
+        !aligned(rstd, 4) || !aligned(y_codes, 16) || !aligned(y_scales, 4) || !aligned(ck_codes, 16) ||
+        !aligned(ck_scales, 4))
+        return MOE_E_INVALID;
+    NormFwd a{};
+    a.rows = rows; a.cols = cols; a.x = x; a.residual = residual; a.weight = weight; a.eps = eps;
+    a.summed = summed; a.y = y; a.rstd = rstd; a.yq = y_codes; a.ys = y_scales; a.ckq = ck_codes; a.cks = ck_scales;
+    TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_norm_fwd(a, (hipStream_t)stream));
+    return check_launch();
+}
+
+moe_status moe_query_add_rmsnorm_bwd(int64_t rows, int32_t cols, size_t* workspace) {
+    if (!workspace) return MOE_E_INVALID;
+    moe_status st = check_norm(rows, cols);
+    if (st != MOE_OK) return st;
+    *workspace = align_up((size_t)norm_bwd_parts(rows, cols) * cols * 4);
+    return MOE_OK;
+}
+
+moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t* dy, const uint16_t* dsum,
+                               const uint16_t* summed, const uint8_t* ck_codes, const uint8_t* ck_scales,
+                               const float* weight, const float* rstd, uint16_t* dx, float* dweight, void* ws,
+                               size_t ws_bytes, void* stream) {
+    size_t need = 0;
+    moe_status st = moe_query_add_rmsnorm_bwd(rows, cols, &need);
+    if (st != MOE_OK) return st;
+    if (!dy || !weight || !rstd || !dx || !dweight || !ws) return MOE_E_INVALID;
+    if (!ck_codes != !ck_scales || !summed == !ck_codes) return MOE_E_INVALID;  // one form of s
+    if (!aligned(dy, 16) || !aligned(dsum, 16) || !aligned(summed, 16) || !aligned(ck_codes, 16) ||
+        !aligned(ck_scales, 4) || !aligned(weight, 16) || !aligned(rstd, 4) || !aligned(dx, 16) ||
+        !aligned(dweight, 16) || !aligned(ws, 16))
+        return MOE_E_INVALID;
+    if (ws_bytes < need) return MOE_E_WORKSPACE;
+    NormBwd a{};
+    a.rows = rows; a.cols = cols; a.dy = dy; a.dsum = dsum; a.summed = summed; a.ckq = ck_codes; a.cks = ck_scales;
+    a.weight = weight; a.rstd = rstd; a.dx = dx; a.dw = dweight; a.partial = (float*)ws;
+    TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_norm_bwd(a, (hipStream_t)stream));
+    return check_launch();
+}
+
+// Workspace of moe_layer_fwd_few (byte offsets).
+struct FewPlan {
+    size_t counter, n_act, act_e, act_off, row_token, row_w, slot_row, logits, xq, xs, h, hq, hs, y, total;
+    int max_act;  // experts that T * k choices can reach, and the shared one
+};
+
+static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
+    moe_status st = make_plan(c, p);
+    if (st != MOE_OK) return st;
+    if (p->T > kFewTokens || p->identity) return MOE_E_UNSUPPORTED;
+    const size_t T = p->T, H = p->H, I = p->I, Tk = T * p->k, rows = Tk + (p->shared ? T : 0);
+    size_t o = kAlign;  // the counters, zero between calls
+    f->counter = 0;
+    auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
+    f->n_act = take(4);
+    f->act_e = take((size_t)p->Et * 4);
+    f->act_off = take(((size_t)p->Et + 1) * 4);
+    f->row_token = take(rows * 4);
+    f->row_w = take(rows * 4);
+    f->slot_row = take(Tk * 4);
+    f->logits = take(T * p->E * 4);
+    f->h = take(rows * I * 2);
+    f->y = take(rows * H * 4);
+    if (p->mx) {
+        f->xq = take(T * H);
+        f->xs = take((size_t)mx_groups(H) * T * 4);
+        f->hq = take(Tk * I);
+        f->hs = take(Tk * (size_t)mx_groups(I) * 4);
+    }
+    f->total = o;
+    f->max_act = std::min(p->E, (int)Tk) + (p->shared ? 1 : 0);
+    return MOE_OK;
+}
+
+moe_status moe_query_few(const moe_cfg* cfg, size_t* workspace) {
+    if (!workspace) return MOE_E_INVALID;
+    Plan p;
+    FewPlan f{};
+    moe_status st = make_few_plan(cfg, &p, &f);
+    if (st != MOE_OK) return st;
+    *workspace = f.total;
+    return MOE_OK;
+}
+
+moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uint16_t* x, const uint8_t* x_codes,
+                             const uint8_t* x_scales, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+    Plan p;
+    FewPlan f{};
+    moe_status st = make_few_plan(cfg, &p, &f);
+    if (st != MOE_OK) return st;
+    if (!w || !w->Wr || !w->packed || !x || !out || !ws) return MOE_E_INVALID;
+    if (!x_codes != !x_scales || (x_codes && !p.mx)) return MOE_E_INVALID;
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(ws, kAlign) || !aligned(w->packed, kAlign) ||
+        !aligned(w->Wr, 4) || !aligned(w->bias, 4) || !aligned(x_codes, 16) || !aligned(x_scales, 4))
+        return MOE_E_INVALID;
+    if (w->packed_bytes < p.packed || ws_bytes < f.total) return MOE_E_WORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    uint8_t* b = (uint8_t*)ws;
+    const uint8_t* pk = (const uint8_t*)w->packed;
+    FewRoute r{};
+    r.x = x; r.Wr = w->Wr; r.bias = w->bias; r.T = p.T; r.H = p.H; r.E = p.E; r.k = p.k; r.shared = p.shared;
+    r.logits = (float*)(b + f.logits);
+    r.xq = p.mx && !x_codes ? b + f.xq : nullptr;
+    r.xs = p.mx && !x_codes ? b + f.xs : nullptr;
+    r.counter = (int*)(b + f.counter);
+    r.n_act = (int*)(b + f.n_act); r.act_e = (int*)(b + f.act_e); r.act_off = (int*)(b + f.act_off);
+    r.row_token = (int*)(b + f.row_token); r.row_w = (float*)(b + f.row_w); r.slot_row = (int*)(b + f.slot_row);
+    TIMED(MOE_K_ROUTE, s, launch_few_route(r, s));
+    FewGemm g{};
+    g.T = p.T; g.H = p.H; g.I = p.I; g.E = p.E;
+    g.n_act = r.n_act; g.act_e = r.act_e; g.act_off = r.act_off; g.row_token = r.row_token; g.row_w = r.row_w;
+    g.slot_row = r.slot_row;
+    g.x = x; g.w1 = (const uint16_t*)(pk + p.pk_w1t); g.w2 = (const uint16_t*)(pk + p.pk_w2t);
+    g.h = (uint16_t*)(b + f.h); g.y = (float*)(b + f.y);
+    if (p.mx) {
+        g.xq = x_codes ? x_codes : b + f.xq;
+        g.xs = x_codes ? x_scales : b + f.xs;
+        g.w1q = pk + p.pk_w1q; g.s1 = pk + p.pk_s1; g.w2q = pk + p.pk_w2q; g.s2 = pk + p.pk_s2;
+        g.hq = b + f.hq; g.hs = b + f.hs;
+    }
+    TIMED(MOE_K_GEMM_GATE_UP, s, launch_few_gate_up(g, f.max_act, s));
+    TIMED(MOE_K_GEMM_DOWN, s, launch_few_down(g, f.max_act, s));
+    TIMED(MOE_K_COMBINE, s, launch_few_combine(g, p.k, p.shared, out, s));
+    return check_launch();
+}
+
 // Destroys every timing event (they must not outlive the runtime's own
 // teardown at process exit, which runs after profiling tools have finalised).
 static moe_status release_timing_events() {

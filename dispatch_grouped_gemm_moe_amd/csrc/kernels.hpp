@@ -331,4 +331,93 @@ void launch_pack_gate_up(const uint16_t* Wg, const uint16_t* Wu, int E, int H, i
 void launch_transpose(const uint16_t* src, int batches, int rows, int cols, uint16_t* dst,
                       hipStream_t stream);
 
+// ---- the layer for a few tokens (few.hip) ----
+
+constexpr int kFewTokens = 64;  // most tokens of one call: an expert's tokens are one 64-bit mask
+
+// Router of a few tokens: logits, top-k, softmax weights and the experts' row
+// lists.  Rows are grouped by expert in ascending order, by token within an
+// expert; the shared expert's T rows come last.
+struct FewRoute {
+    const uint16_t* x;   // [T][H]
+    const float* Wr;     // [H][E]
+    const float* bias;   // [E] or NULL
+    int T, H, E, k, shared;
+    float* logits;       // [T][E]
+    uint8_t* xq;         // MXFP8: codes [T][H] to write, or NULL
+    uint8_t* xs;         // their scales, operand layout
+    int* counter;        // zero between calls
+    int* n_act;          // active experts
+    int* act_e;          // [n_act] expert, E for the shared one
+    int* act_off;        // [n_act + 1] first row
+    int* row_token;      // [rows]
+    float* row_w;        // [rows] weight, 1 for the shared expert
+    int* slot_row;       // [T][k] row of each selection
+};
+void launch_few_route(const FewRoute& a, hipStream_t stream);
+
+struct FewGemm {
+    int T, H, I, E;
+    const int* n_act;
+    const int* act_e;
+    const int* act_off;
+    const int* row_token;
+    const float* row_w;
+    const int* slot_row;
+    const uint16_t* x;                 // [T][H]
+    const uint16_t *w1, *w2;           // packed bf16 weights [Et][2I][H], [Et][H][I]
+    uint16_t* h;                       // [rows][I]
+    // MXFP8 (xq NULL: bf16)
+    const uint8_t *xq, *xs;            // [T][H], operand-layout scales
+    const uint8_t *w1q, *s1, *w2q, *s2;
+    uint8_t* hq;                       // [rows][I]
+    uint8_t* hs;                       // [rows][mx_groups(I)][4]
+    float* y;                          // [rows][H] weighted expert outputs
+};
+void launch_few_gate_up(const FewGemm& a, int max_act, hipStream_t stream);
+void launch_few_down(const FewGemm& a, int max_act, hipStream_t stream);
+void launch_few_combine(const FewGemm& a, int k, int shared, uint16_t* out, hipStream_t stream);
+
+// ---- residual addition and root-mean-square norm (norm.hip) ----
+
+constexpr int kNormMaxCols = 32768;  // a row stays in a workgroup's registers
+
+struct NormFwd {
+    int64_t rows;
+    int cols;
+    const uint16_t* x;
+    const uint16_t* residual;  // or NULL
+    const float* weight;
+    float eps;
+    uint16_t* summed;          // or NULL
+    uint16_t* y;
+    uint8_t* yq;               // y's codes and operand-layout scales, or NULL
+    uint8_t* ys;
+    uint8_t* ckq;              // the sum's codes and row scales [rows][cols / 32], or NULL
+    uint8_t* cks;
+    float* rstd;               // or NULL
+};
+void launch_norm_fwd(const NormFwd& a, hipStream_t stream);
+
+struct NormBwd {
+    int64_t rows;
+    int cols;
+    const uint16_t* dy;
+    const uint16_t* dsum;      // or NULL
+    const uint16_t* summed;    // or NULL: the 8-bit checkpoint
+    const uint8_t* ckq;
+    const uint8_t* cks;
+    const float* weight;
+    const float* rstd;
+    uint16_t* dx;
+    float* dw;
+    float* partial;            // [norm_bwd_parts][cols]
+};
+int norm_bwd_parts(int64_t rows, int cols);
+void launch_norm_bwd(const NormBwd& a, hipStream_t stream);
+
+// codes [rows][cols] and scales (layout 0: [rows][cols / 32], 1: operand layout) -> bf16
+void launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int layout, uint16_t* dst,
+                       hipStream_t stream);
+
 }  // namespace moe

@@ -55,6 +55,48 @@ void launch_mx_quant(const uint16_t* src, int64_t rows, int cols, int layout, ui
 }
 
 // ---------------------------------------------------------------------------
+// dequantiser: codes and scales of either layout back to bf16.  A product of an
+// E4M3 value (four significand bits) and a power of two is exact in bf16 down
+// to its smallest subnormal, 2^-133, and rounded to nearest even below; scale
+// byte 255 is NaN, as the format has it.  One thread per 16 codes.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int64_t rows, int cols,
+                                                         int layout, uint16_t* __restrict__ dst) {
+    const int np = cols / 16;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= rows * np) return;
+    const int64_t r = i / np;
+    const int p = (int)(i - r * np), b = p >> 1;
+    const int sc = layout == 0 ? scales[r * (cols / 32) + b] : scales[((int64_t)(b >> 2) * rows + r) * 4 + (b & 3)];
+    const int e = sc - 127;
+    const intx4 q = *(const intx4*)(codes + i * 16);
+    intx4 o[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float v[4] = {__builtin_amdgcn_cvt_f32_fp8(q[j], 0), __builtin_amdgcn_cvt_f32_fp8(q[j], 1),
+                      __builtin_amdgcn_cvt_f32_fp8(q[j], 2), __builtin_amdgcn_cvt_f32_fp8(q[j], 3)};
+        uint32_t h[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float f = ldexpf(v[c], e);
+            h[c] = (sc == 255 || f != f) ? 0x7FC0u : f32_to_bf16_rne(f);
+        }
+        o[j >> 1][2 * (j & 1)] = (int)(h[0] | (h[1] << 16));
+        o[j >> 1][2 * (j & 1) + 1] = (int)(h[2] | (h[3] << 16));
+    }
+    *(intx4*)(dst + i * 16) = o[0];
+    *(intx4*)(dst + i * 16 + 8) = o[1];
+}
+
+void launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int layout, uint16_t* dst,
+                       hipStream_t stream) {
+    const int64_t n = rows * (cols / 16);
+    hipLaunchKernelGGL(mx_dequant_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, codes, scales, rows,
+                       cols, layout, dst);
+}
+
+// ---------------------------------------------------------------------------
 // scaled-MFMA grouped GEMM
 // ---------------------------------------------------------------------------
 

@@ -1,0 +1,273 @@
+// Residual addition with root-mean-square norm, forward and backward (gfx950).
+//
+//   s = bf16(x + residual),  rstd = 1 / sqrt(mean(s^2) + eps),  y = bf16(s * rstd * w)
+//   dx = dsum + rstd * (dy w - xhat mean(dy w xhat)),  xhat = s * rstd
+//   dw = sum over rows of dy * xhat
+//
+// All of it is bound by memory: a few operations per value.  A row is read
+// once and kept in registers between its sum and its output.  A thread holds
+// vectors of eight consecutive values (16 bytes of bf16), so an MXFP8 block of
+// 32 is four neighbouring lanes.
+#include "common.hpp"
+#include "kernels.hpp"
+#include "mxfp8.hpp"
+
+namespace moe {
+
+#pragma clang fp contract(off)
+
+constexpr int kNormVec = 8;
+
+__device__ __forceinline__ void unpack8(intx4 raw, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __builtin_bit_cast(float, (uint32_t)raw[q] << 16);
+        v[2 * q + 1] = __builtin_bit_cast(float, (uint32_t)raw[q] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
+}
+
+__device__ __forceinline__ intx4 pack8(const float (&v)[8]) {
+    intx4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = (int)pack2(v[2 * q], v[2 * q + 1]);
+    return o;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+    return v;
+}
+
+// Sum over the workgroup (kWaves waves), the same in every thread and in the
+// same order on every call.  s_sum alternates between two halves, so a call
+// needs one barrier.
+template <int kWaves>
+__device__ __forceinline__ float group_sum(float v, float* s_sum) {
+    v = wave_sum(v);
+    if constexpr (kWaves == 1) return v;
+    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float r = s_sum[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) r += s_sum[w];
+    return r;
+}
+
+// The eight values of a lane as part of the 32-value block of its four lanes:
+// the codes, and the scale byte (the same in all four).
+__device__ __forceinline__ uint64_t block_codes(const float (&v)[8], uint8_t& scale) {
+    float m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) m = fmaxf(m, fabsf(v[c]));
+    m = fmaxf(m, __shfl_xor(m, 1, kWave));
+    m = fmaxf(m, __shfl_xor(m, 2, kWave));
+    const int e = mx_scale_exp(m);
+    scale = (uint8_t)(e + 127);
+    const uint32_t lo = fp8x4(ldexpf(v[0], -e), ldexpf(v[1], -e), ldexpf(v[2], -e), ldexpf(v[3], -e));
+    const uint32_t hi = fp8x4(ldexpf(v[4], -e), ldexpf(v[5], -e), ldexpf(v[6], -e), ldexpf(v[7], -e));
+    return (uint64_t)lo | ((uint64_t)hi << 32);
+}
+
+// A row per group of kWaves waves, kNV vectors per thread; kPer rows of a
+// workgroup side by side (kWaves = 1).
+template <int kWaves, int kNV, int kPer>
+__global__ __launch_bounds__(kWaves * kWave * kPer) void norm_fwd_kernel(NormFwd a) {
+    __shared__ float s_sum[kWaves];
+    const int lid = kPer == 1 ? threadIdx.x : threadIdx.x & 63;
+    const int64_t r = kPer == 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kPer + (threadIdx.x >> 6);
+    if (kPer > 1 && r >= a.rows) return;  // whole waves; no barrier follows
+    const int nv = a.cols / kNormVec;
+    const int64_t base = r * a.cols;
+    float v[kNV][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        const int p = lid + i * kWaves * kWave;
+        intx4 raw = {0, 0, 0, 0};
+        if (p < nv) raw = *(const intx4*)(a.x + base + p * kNormVec);
+        if (a.residual) {
+            intx4 rr = {0, 0, 0, 0};
+            if (p < nv) rr = *(const intx4*)(a.residual + base + p * kNormVec);
+            float xv[8], rv[8];
+            unpack8(raw, xv);
+            unpack8(rr, rv);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) xv[c] += rv[c];
+            raw = pack8(xv);
+        }
+        if (a.summed && p < nv) *(intx4*)(a.summed + base + p * kNormVec) = raw;
+        unpack8(raw, v[i]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ss = __builtin_fmaf(v[i][c], v[i][c], ss);
+    }
+    const float rstd = 1.0f / sqrtf(group_sum<kWaves>(ss, s_sum) / (float)a.cols + a.eps);
+    if (a.rstd && lid == 0) a.rstd[r] = rstd;
+    const int nb = a.cols / 32;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        const int p = lid + i * kWaves * kWave;
+        if (p >= nv) break;  // in fours: cols is a multiple of 32
+        uint8_t sc;
+        if (a.ckq) {
+            *(uint64_t*)(a.ckq + base + p * kNormVec) = block_codes(v[i], sc);
+            if ((p & 3) == 0) a.cks[r * nb + (p >> 2)] = sc;
+        }
+        const floatx4 w0 = *(const floatx4*)(a.weight + p * kNormVec), w1 = *(const floatx4*)(a.weight + p * kNormVec + 4);
+        float y[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] = v[i][c] * rstd * (c < 4 ? w0[c] : w1[c - 4]);
+        const intx4 out = pack8(y);
+        *(intx4*)(a.y + base + p * kNormVec) = out;
+        if (a.yq) {  // the codes of the rounded y, as the layer's own quantisation of y gives
+            unpack8(out, y);
+            *(uint64_t*)(a.yq + base + p * kNormVec) = block_codes(y, sc);
+            if ((p & 3) == 0) mx_store_scale_byte(a.ys, a.rows, r, p >> 2, nb, sc);
+        }
+    }
+}
+
+void launch_norm_fwd(const NormFwd& a, hipStream_t stream) {
+    const int nv = a.cols / kNormVec;
+#define NORM_FWD(W, NV, PER)                                                                                       \
+    hipLaunchKernelGGL((norm_fwd_kernel<W, NV, PER>), dim3((unsigned)((a.rows + PER - 1) / PER)), dim3(W * kWave * PER), \
+                       0, stream, a)
+    if (nv <= 64) NORM_FWD(1, 1, 4);
+    else if (nv <= 128) NORM_FWD(1, 2, 4);
+    else if (nv <= 256) NORM_FWD(2, 2, 1);
+    else if (nv <= 512) NORM_FWD(4, 2, 1);
+    else if (nv <= 1024) NORM_FWD(8, 2, 1);
+    else if (nv <= 2048) NORM_FWD(16, 2, 1);
+    else NORM_FWD(16, 4, 1);
+#undef NORM_FWD
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+constexpr int kNormParts = 512;  // most partial sums of dw
+
+int norm_bwd_parts(int64_t rows, int cols) {
+    (void)cols;
+    return (int)(rows < kNormParts ? rows : kNormParts);
+}
+
+// Workgroup b takes rows b, b + parts, ...; dw's partial sums stay in
+// registers over them.
+template <int kWaves, int kNV, bool kCk>
+__global__ __launch_bounds__(kWaves * kWave) void norm_bwd_kernel(NormBwd a) {
+    __shared__ float s_sum[2][kWaves];
+    const int lid = threadIdx.x;
+    const int nv = a.cols / kNormVec, nb = a.cols / 32;
+    float dw[kNV][8];
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dw[i][c] = 0.0f;
+    int half = 0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, half ^= 1) {
+        const int64_t base = r * a.cols;
+        const float rstd = a.rstd[r];
+        float xh[kNV][8], gy[kNV][8];
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const int p = lid + i * kWaves * kWave;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) xh[i][c] = gy[i][c] = 0.0f;
+            if (p >= nv) continue;
+            if constexpr (kCk) {
+                const uint64_t q = *(const uint64_t*)(a.ckq + base + p * kNormVec);
+                const int e = (int)a.cks[r * nb + (p >> 2)] - 127;
+                const uint32_t lo = (uint32_t)q, hi = (uint32_t)(q >> 32);
+                xh[i][0] = __builtin_amdgcn_cvt_f32_fp8(lo, 0); xh[i][1] = __builtin_amdgcn_cvt_f32_fp8(lo, 1);
+                xh[i][2] = __builtin_amdgcn_cvt_f32_fp8(lo, 2); xh[i][3] = __builtin_amdgcn_cvt_f32_fp8(lo, 3);
+                xh[i][4] = __builtin_amdgcn_cvt_f32_fp8(hi, 0); xh[i][5] = __builtin_amdgcn_cvt_f32_fp8(hi, 1);
+                xh[i][6] = __builtin_amdgcn_cvt_f32_fp8(hi, 2); xh[i][7] = __builtin_amdgcn_cvt_f32_fp8(hi, 3);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) xh[i][c] = ldexpf(xh[i][c], e);
+            } else {
+                unpack8(*(const intx4*)(a.summed + base + p * kNormVec), xh[i]);
+            }
+            unpack8(*(const intx4*)(a.dy + base + p * kNormVec), gy[i]);
+            const floatx4 w0 = *(const floatx4*)(a.weight + p * kNormVec);
+            const floatx4 w1 = *(const floatx4*)(a.weight + p * kNormVec + 4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                xh[i][c] *= rstd;
+                dw[i][c] = __builtin_fmaf(gy[i][c], xh[i][c], dw[i][c]);
+                gy[i][c] *= c < 4 ? w0[c] : w1[c - 4];
+                dot = __builtin_fmaf(gy[i][c], xh[i][c], dot);
+            }
+        }
+        const float mean = group_sum<kWaves>(dot, s_sum[half]) / (float)a.cols;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const int p = lid + i * kWaves * kWave;
+            if (p >= nv) continue;
+            float d[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d[c] = rstd * (gy[i][c] - xh[i][c] * mean);
+            if (a.dsum) {
+                float ds[8];
+                unpack8(*(const intx4*)(a.dsum + base + p * kNormVec), ds);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] += ds[c];
+            }
+            *(intx4*)(a.dx + base + p * kNormVec) = pack8(d);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        const int p = lid + i * kWaves * kWave;
+        if (p >= nv) continue;
+        float* d = a.partial + (int64_t)blockIdx.x * a.cols + p * kNormVec;
+        *(floatx4*)d = floatx4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        *(floatx4*)(d + 4) = floatx4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+}
+
+// dw[c] = the partial sums in a fixed order: 32 columns per workgroup, thread
+// (group, column quad) sums every 128th part, then a tree over the groups.
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* partial, int parts, int cols, float* dw) {
+    __shared__ __attribute__((aligned(16))) floatx4 s[128][8];
+    const int q = threadIdx.x & 7, g = threadIdx.x >> 3;
+    const int c = blockIdx.x * 32 + q * 4;
+    floatx4 v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int p = g; p < parts; p += 128) v += *(const floatx4*)(partial + (int64_t)p * cols + c);
+    s[g][q] = v;
+    for (int n = 64; n >= 1; n >>= 1) {
+        __syncthreads();
+        if (g < n) s[g][q] += s[g + n][q];
+    }
+    if (g == 0) *(floatx4*)(dw + c) = s[0][q];
+}
+
+void launch_norm_bwd(const NormBwd& a, hipStream_t stream) {
+    const int nv = a.cols / kNormVec;
+    const int parts = norm_bwd_parts(a.rows, a.cols);
+#define NORM_BWD(W, NV)                                                                                          \
+    do {                                                                                                         \
+        if (a.ckq)                                                                                               \
+            hipLaunchKernelGGL((norm_bwd_kernel<W, NV, true>), dim3(parts), dim3(W * kWave), 0, stream, a);      \
+        else                                                                                                     \
+            hipLaunchKernelGGL((norm_bwd_kernel<W, NV, false>), dim3(parts), dim3(W * kWave), 0, stream, a);     \
+    } while (0)
+    if (nv <= 64) NORM_BWD(1, 1);
+    else if (nv <= 128) NORM_BWD(1, 2);
+    else if (nv <= 256) NORM_BWD(2, 2);
+    else if (nv <= 512) NORM_BWD(4, 2);
+    else if (nv <= 1024) NORM_BWD(8, 2);
+    else if (nv <= 2048) NORM_BWD(16, 2);
+    else NORM_BWD(16, 4);
+#undef NORM_BWD
+    hipLaunchKernelGGL(norm_dw_kernel, dim3(a.cols / 32), dim3(1024), 0, stream, a.partial, parts, a.cols, a.dw);
+}
+
+}  // namespace moe

@@ -314,6 +314,105 @@ moe_status moe_mx_quantize(const uint16_t *src, int64_t rows, int32_t cols, uint
                            uint8_t *scales, void *stream);
 
 /*
+ * The inverse of the quantiser: bf16 values of E4M3 codes and E8M0 scales,
+ * code * 2^(scale - 127).
+ *   codes [rows, cols] uint8 (16-byte aligned), cols a multiple of 32;
+ *   operand_scales = 0: scales [rows, cols/32], as moe_mx_quantize writes them
+ *       (and the checkpoint of moe_add_rmsnorm_fwd);
+ *   operand_scales = 1: scales [ceil(cols/128)][rows][4], the GEMM operand
+ *       layout that moe_route and moe_add_rmsnorm_fwd write;
+ *   dst [rows, cols] bf16 (16-byte aligned).
+ * Exact wherever bf16 holds the value (all that moe_mx_quantize writes of
+ * magnitudes from 2^-133 on); below, rounded to nearest even.  A NaN code or
+ * the scale 255 gives NaN.  MOE_E_INVALID for null or misaligned pointers,
+ * rows < 1, cols not a positive multiple of 32 or an unknown operand_scales;
+ * MOE_E_UNSUPPORTED for 2^35 codes or more.
+ */
+moe_status moe_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols,
+                             int32_t operand_scales, uint16_t *dst, void *stream);
+
+/*
+ * Residual addition with root-mean-square norm: what stands in front of the
+ * layer in a transformer block.  For each of `rows` rows:
+ *   s    = bf16(x + residual)                 (s = x without a residual)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)          (fp32)
+ *   y    = bf16(s * rstd * weight)
+ * and optionally, in the same pass,
+ *   y_codes, y_scales: y in MXFP8 as moe_route would quantise it: E4M3 codes
+ *       [rows, cols] and scales in the GEMM operand layout
+ *       [ceil(cols/128)][rows][4] (spare bytes zero), which
+ *       moe_layer_fwd_few takes;
+ *   ck_codes, ck_scales: an 8-bit checkpoint of s for moe_add_rmsnorm_bwd:
+ *       E4M3 codes [rows, cols] and scales [rows, cols/32], as moe_mx_quantize
+ *       of s.  1.03 bytes a value are kept for the backward instead of 2.
+ *   x, residual (NULL: none) bf16 [rows, cols]; weight fp32 [cols];
+ *   summed: s, bf16 [rows, cols], or NULL; y bf16 [rows, cols];
+ *   rstd: fp32 [rows], or NULL (moe_add_rmsnorm_bwd needs it).
+ * summed may be x or residual itself, and y may be whichever of x and
+ * residual summed is not; buffers overlap in no other way.
+ * All pointers 16-byte aligned (rstd and the scales 4).  MOE_E_INVALID for
+ * null x, weight or y, misaligned pointers, rows < 1, cols not a positive
+ * multiple of 32, eps negative or NaN, one of a codes / scales pair without
+ * the other, or summed == y; MOE_E_UNSUPPORTED for cols > 32768 or
+ * rows > 2^21.  Rows are independent: a NaN or infinity reaches its own row's
+ * outputs only (codes of such a row are unspecified).
+ */
+moe_status moe_add_rmsnorm_fwd(int64_t rows, int32_t cols, const uint16_t *x, const uint16_t *residual,
+                               const float *weight, float eps, uint16_t *summed, uint16_t *y, float *rstd,
+                               uint8_t *y_codes, uint8_t *y_scales, uint8_t *ck_codes, uint8_t *ck_scales,
+                               void *stream);
+
+/* Host-only: bytes of moe_add_rmsnorm_bwd's workspace (its refusals of rows and cols). */
+moe_status moe_query_add_rmsnorm_bwd(int64_t rows, int32_t cols, size_t *workspace);
+
+/*
+ * Backward of moe_add_rmsnorm_fwd.  With xhat = s * rstd and g = dy * weight:
+ *   dx      = bf16(dsum + rstd * (g - xhat * mean(g * xhat)))
+ *   dweight = sum over rows of dy * xhat          (fp32, overwritten)
+ * dx is the gradient of x and of the residual alike.
+ *   dy bf16 [rows, cols]: gradient of y;
+ *   dsum bf16 [rows, cols]: gradient that reaches s past the norm, or NULL;
+ *   s either as summed (bf16; x where there was no residual) or as its 8-bit
+ *   checkpoint ck_codes, ck_scales: exactly one of the two, the other NULL;
+ *   rstd fp32 [rows], weight fp32 [cols]: the forward's;
+ *   dx bf16 [rows, cols], which may be dy or dsum itself;
+ *   ws: at least moe_query_add_rmsnorm_bwd bytes, 16-byte aligned, of any content.
+ * Sums have a fixed order, so results are bitwise repeatable.  Refusals as
+ * moe_add_rmsnorm_fwd's, and MOE_E_WORKSPACE for a smaller workspace.
+ */
+moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t *dy, const uint16_t *dsum,
+                               const uint16_t *summed, const uint8_t *ck_codes, const uint8_t *ck_scales,
+                               const float *weight, const float *rstd, uint16_t *dx, float *dweight, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/*
+ * Layer forward for a few tokens (decoding): moe_layer_fwd for
+ * cfg->T <= MOE_FEW_MAX_TOKENS, bound by reading the chosen experts' weights
+ * once instead of by tiles of 128 rows.  Same cfg, weights (one
+ * moe_prepare_weights buffer serves both) and formula, the same expert choice
+ * and weights bit for bit; the outputs differ from moe_layer_fwd's by the
+ * rounding of sums taken in another order (here the expert outputs stay fp32
+ * until the weighted sum).  Runs of one call are bitwise repeatable.
+ *   x, out [T,H] bf16, 16-byte aligned; they may not overlap;
+ *   x_codes, x_scales: MOE_PREC_MXFP8, optional: the MXFP8 form of x as
+ *       moe_route or moe_add_rmsnorm_fwd wrote it (codes 16-byte aligned,
+ *       scales 4); both or neither.  Without them the call quantises x itself.
+ *   ws: at least moe_query_few bytes, 256-byte aligned; zero its first 256
+ *       bytes once when it is allocated (every call leaves them zero).
+ * cfg->minibatch, ring_slots, comm_cus and the flags other than
+ * MOE_F_SHARED_EXPERT have no effect.  MOE_E_UNSUPPORTED for more tokens and
+ * in identity-expert mode; MOE_E_INVALID for x_codes with MOE_PREC_BF16.
+ * Inputs must be finite: a NaN reaches its own token's output only.
+ */
+#define MOE_FEW_MAX_TOKENS 64
+moe_status moe_layer_fwd_few(const moe_cfg *cfg, const moe_weights *w, const uint16_t *x,
+                             const uint8_t *x_codes, const uint8_t *x_scales, uint16_t *out, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/* Host-only: bytes of moe_layer_fwd_few's workspace (its refusals of a cfg). */
+moe_status moe_query_few(const moe_cfg *cfg, size_t *workspace);
+
+/*
  * Kernel timing (diagnostics, for benchmarks).  While enabled, every kernel
  * the library launches is bracketed by a pair of HIP events recorded on the
  * stream it is launched on; moe_timing_read waits for those events and

@@ -1,0 +1,270 @@
+"""The layer for a few tokens (moe_layer_fwd_few): its refusals on the CPU, and on
+the GPU its outputs against the layer in 64 bits within a derived bound."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import dispatch_grouped_gemm_moe_amd as moe
+from few_reference import few_layer
+from moe_inputs import Workload, make_inputs
+
+FAKE = 1 << 20  # aligned and never dereferenced: the checks fail first
+
+
+def _cfg(T=8, H=128, I=64, E=8, k=2, **kw):
+    return moe.make_cfg(T, H, I, E, k, **kw)
+
+
+# ------------------------------------------------------------------ refusals (no GPU)
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=0), moe.MOE_E_INVALID), (dict(k=9), moe.MOE_E_INVALID), (dict(H=96), moe.MOE_E_UNSUPPORTED),
+    (dict(T=65), moe.MOE_E_UNSUPPORTED), (dict(flags=moe.MOE_F_IDENTITY_EXPERTS), moe.MOE_E_UNSUPPORTED)])
+def test_few_refuses_configurations(kw, want):
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_query_few(_cfg(**kw))
+    assert e.value.status == want
+
+
+def test_few_workspace_depends_on_the_layer_only():
+    base = moe.moe_query_few(_cfg())
+    assert base % 256 == 0 and base >= 8 * 2 * 128 * 4
+    assert moe.moe_query_few(_cfg(minibatch=4, ring_slots=2, comm_cus=8)) == base
+    assert moe.moe_query_few(_cfg(T=64)) > base
+    assert moe.moe_query_few(_cfg(flags=moe.MOE_F_SHARED_EXPERT)) > base
+    assert moe.lib().moe_query_few(ctypes.byref(_cfg()), None) == moe.MOE_E_INVALID
+
+
+def _call(cfg, ws_bytes=None, packed_bytes=None, **over):
+    a = dict(x=FAKE, xc=None, xs=None, out=FAKE, ws=FAKE, Wr=FAKE, packed=FAKE, bias=None)
+    a.update(over)
+    s = moe.moe_query_sizes(_cfg(prec=cfg.prec, flags=cfg.flags))
+    w = moe.moe_weights(a["Wr"], a["bias"], a["packed"], s.packed_weights if packed_bytes is None else packed_bytes)
+    return moe.lib().moe_layer_fwd_few(ctypes.byref(cfg), ctypes.byref(w), a["x"], a["xc"], a["xs"], a["out"], a["ws"],
+                                       1 << 40 if ws_bytes is None else ws_bytes, None)
+
+
+@pytest.mark.parametrize("over", [dict(x=None), dict(out=None), dict(ws=None), dict(Wr=None), dict(packed=None),
+                                  dict(x=FAKE + 8), dict(out=FAKE + 2), dict(ws=FAKE + 128), dict(packed=FAKE + 16),
+                                  dict(Wr=FAKE + 2), dict(bias=FAKE + 1), dict(xc=FAKE), dict(xs=FAKE),
+                                  dict(xc=FAKE, xs=FAKE)])
+def test_few_refuses_pointers(over):
+    assert _call(_cfg(), **over) == moe.MOE_E_INVALID
+
+
+def test_few_refuses_small_buffers_and_misaligned_codes():
+    cfg = _cfg(prec=moe.MOE_PREC_MXFP8)
+    assert _call(cfg, xc=FAKE + 8, xs=FAKE) == moe.MOE_E_INVALID
+    assert _call(cfg, xc=FAKE, xs=FAKE + 2) == moe.MOE_E_INVALID
+    assert _call(cfg, ws_bytes=moe.moe_query_few(cfg) - 1) == moe.MOE_E_WORKSPACE
+    s = moe.moe_query_sizes(cfg)
+    assert _call(cfg, packed_bytes=s.packed_weights - 1) == moe.MOE_E_WORKSPACE
+
+
+def test_few_binding_refuses_tensors_the_kernels_cannot_read():
+    cfg = _cfg()
+    ok = dict(Wr=torch.zeros(128, 8), bias=None, packed=torch.zeros(16, dtype=torch.uint8),
+              x=torch.zeros(8, 128, dtype=torch.bfloat16), out=torch.zeros(8, 128, dtype=torch.bfloat16),
+              ws=torch.zeros(16, dtype=torch.uint8))
+    bad = [dict(x=torch.zeros(8, 128)), dict(x=torch.zeros(128, 8, dtype=torch.bfloat16).t()),
+           dict(out=torch.zeros(7, 128, dtype=torch.bfloat16)), dict(Wr=torch.zeros(127, 8)),
+           dict(bias=torch.zeros(8, dtype=torch.float64)), dict(x_codes=torch.zeros(8, 64, dtype=torch.uint8)),
+           dict(x=torch.zeros(8, 128, dtype=torch.bfloat16, device="meta"))]
+    for b in bad:
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_layer_fwd_few(cfg, stream=0, **{**ok, **b})
+        assert e.value.status == moe.MOE_E_INVALID, b
+
+
+# ------------------------------------------------------------------ GPU
+
+class Few:
+    """One layer on the GPU, with a workspace whose contents past the counters are noise."""
+
+    def __init__(self, w, inp=None):
+        self.w, self.inp = w, inp or make_inputs(w)
+        self.cfg = moe.make_cfg(w.T, w.H, w.I, w.E, w.k, prec=moe.MOE_PREC_MXFP8 if w.prec == "mxfp8" else 0,
+                                flags=moe.MOE_F_SHARED_EXPERT if w.shared_expert else 0)
+        d = lambda t: None if t is None else t.cuda().contiguous()
+        i = self.inp
+        self.Wr, self.bias, self.x = d(i.Wr), d(i.bias), d(i.x)
+        self.packed = torch.empty(moe.moe_query_sizes(self.cfg).packed_weights, dtype=torch.uint8, device="cuda")
+        moe.moe_prepare_weights(self.cfg, d(i.Wg), d(i.Wu), d(i.Wd), self.packed, d(i.Wsg), d(i.Wsu), d(i.Wsd))
+        self.ws = torch.randint(0, 256, (moe.moe_query_few(self.cfg),), dtype=torch.uint8, device="cuda")
+        self.ws[:256] = 0
+        torch.cuda.synchronize()
+
+    def __call__(self, x=None, **kw):
+        x = self.x if x is None else x
+        out = torch.full((x.shape[0] + 1, x.shape[1]), 7.0, dtype=torch.bfloat16, device="cuda")
+        moe.moe_layer_fwd_few(self.cfg, self.Wr, self.bias, self.packed, x, out, self.ws, **kw)
+        torch.cuda.synchronize()
+        assert not self.ws[:256].any(), "the counters are not back at zero"
+        assert (out[-1] == 7).all(), "a row past the last token was written"
+        return out[:-1]
+
+
+def _wl(T, H, I, E, k, prec="bf16", shared=False, bias="none", **kw):
+    name = "few_%d_%d_%d_%d_%d_%s_%d" % (T, H, I, E, k, prec, shared)
+    return Workload(name, T=T, H=H, I=I, E=E, k=k, prec=prec, shared_expert=shared, router_bias=bias,
+                    stream=9000 + sum(map(ord, name)) % 997, **kw)
+
+
+SHAPES = [(1, 64, 64, 1, 1), (1, 128, 64, 8, 2), (2, 2112, 128, 5, 3), (5, 192, 320, 6, 3), (7, 448, 64, 256, 16),
+          (16, 320, 192, 4, 4), (17, 256, 128, 8, 2), (31, 128, 192, 7, 1), (33, 448, 320, 16, 5), (48, 64, 128, 2, 1),
+          (64, 128, 64, 1, 1), (64, 4160, 64, 3, 2), (64, 192, 64, 200, 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+def test_few_matches_the_layer_in_64_bits(gpu_lib, shape, prec):
+    w = _wl(*shape, prec=prec, shared=sum(shape) % 2 == 0, bias="normal" if shape[0] % 3 else "none")
+    few = Few(w)
+    got = few().double().cpu().numpy()
+    ref, bound = few_layer(few.inp, w.T)
+    worst = (np.abs(got - ref) / bound).max()
+    print("%s: largest error %.3f of its bound" % (w.name, worst))
+    assert worst <= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+def test_few_wide_magnitudes_and_skewed_routing(gpu_lib, prec):
+    w = _wl(40, 256, 128, 12, 4, prec=prec, bias="zipf", wide_range=True)
+    few = Few(w)
+    ref, bound = few_layer(few.inp, w.T)
+    assert (np.abs(few().double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.gpu
+def test_few_router_weight_off_16_bytes(gpu_lib):
+    w = _wl(9, 192, 64, 8, 2)
+    few = Few(w)
+    want = few()
+    shifted = torch.empty(few.Wr.numel() + 1, device="cuda")[1:].view(few.Wr.shape)
+    shifted.copy_(few.Wr)
+    few.Wr = shifted
+    assert torch.equal(few(), want)
+
+
+@pytest.mark.gpu
+def test_few_ties_go_to_the_lower_expert(gpu_lib):
+    w = _wl(6, 128, 64, 8, 2)
+    inp = make_inputs(w)
+    inp.Wr[:] = inp.Wr[:, :1]  # every logit of a token is the same: experts 0 and 1
+    few = Few(w, inp)
+    ref, bound = few_layer(inp, w.T)
+    assert (np.abs(few().double().cpu().numpy() - ref) <= bound).all()
+    inp.bias = torch.zeros(8)
+    inp.bias[7] = 1.0
+    few = Few(w, inp)
+    ref, bound = few_layer(inp, w.T)
+    assert (np.abs(few().double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+def test_few_reads_nothing_of_an_expert_that_no_token_chose(gpu_lib, prec):
+    w = _wl(4, 128, 64, 6, 2, prec=prec)
+    inp = make_inputs(w)
+    inp.bias = torch.tensor([0.0, -1e4, 0.0, 0.0, -1e4, 0.0])
+    clean = Few(w, inp)()
+    for m in (inp.Wg, inp.Wu, inp.Wd):
+        m[1], m[4] = 3e38, -3e38
+    assert torch.equal(Few(w, inp)(), clean) and torch.isfinite(clean).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_few_a_token_that_is_not_finite_spoils_only_itself(gpu_lib, bad):
+    w = _wl(20, 256, 64, 8, 3)
+    few = Few(w)
+    want = few()
+    x = few.x.clone()
+    x[3, 17] = bad
+    got = few(x)
+    keep = torch.arange(20, device="cuda") != 3
+    assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[3]).all()
+
+
+@pytest.mark.gpu
+def test_few_codes_given_equal_codes_made(gpu_lib):
+    for H in (320, 512):
+        w = _wl(11, H, 128, 8, 2, prec="mxfp8", shared=True)
+        few = Few(w)
+        want = few()
+        idx = torch.empty(w.T, w.k, dtype=torch.int32, device="cuda")
+        gw = torch.empty(w.T, w.k, device="cuda")
+        codes = torch.empty(w.T, H, dtype=torch.uint8, device="cuda")
+        scales = torch.empty((H + 127) // 128, w.T, 4, dtype=torch.uint8, device="cuda")
+        moe.moe_route(few.cfg, few.x, few.Wr, None, idx, gw, x_codes=codes, x_scales=scales)
+        assert torch.equal(few(x_codes=codes, x_scales=scales), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+def test_few_agrees_with_the_layer_forward(gpu_lib, prec):
+    # both are within the bound of the 64-bit layer; the layer forward also
+    # rounds every expert's output to bf16 before the weighted sum
+    w = _wl(33, 256, 192, 8, 4, prec=prec, shared=True)
+    few = Few(w)
+    ref, bound = few_layer(few.inp, w.T)
+    ws = torch.zeros(moe.moe_query_sizes(few.cfg).workspace_fwd, dtype=torch.uint8, device="cuda")
+    full = torch.empty_like(few.x)
+    moe.moe_layer_fwd(few.cfg, few.Wr, few.bias, few.packed, few.x, full, ws)
+    got = few().double().cpu().numpy()
+    assert (np.abs(got - ref) <= bound).all()
+    gap = np.abs(got - full.double().cpu().numpy()).max() / np.abs(ref).max()
+    assert gap <= 2 * 2.0 ** -6, gap
+
+
+@pytest.mark.gpu
+def test_few_one_workspace_serves_calls_of_other_sizes(gpu_lib):
+    a, b = Few(_wl(64, 256, 128, 16, 4, shared=True)), Few(_wl(3, 128, 64, 8, 2, prec="mxfp8"))
+    want = a().clone(), b().clone()
+    a.ws = b.ws = max(a.ws, b.ws, key=lambda t: t.numel())
+    for _ in range(3):
+        assert torch.equal(a(), want[0]) and torch.equal(b(), want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+def test_few_captured_twice_on_one_workspace(gpu_lib, prec):
+    few = Few(_wl(10, 256, 128, 8, 2, prec=prec, shared=True))
+    x1, x2 = few.x.clone(), few.x.flip(0).contiguous()
+    want = [few(x1).clone(), few(x2).clone()]
+    outs = [torch.empty_like(few.x) for _ in want]
+    graphs = []
+    for x, o in zip((x1, x2), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_layer_fwd_few(few.cfg, few.Wr, few.bias, few.packed, x, o, few.ws)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        few(x2)  # the program's own call between replays
+        assert torch.equal(outs[i], want[i])
+    x1.copy_(x2)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[1])
+
+
+@pytest.mark.gpu
+def test_few_on_another_stream(gpu_lib):
+    few = Few(_wl(12, 512, 256, 8, 2))
+    want = few()
+    s = torch.cuda.Stream()
+    x = torch.zeros_like(few.x)
+    torch.cuda.synchronize()
+    out = torch.empty_like(x)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1000000)
+        x.copy_(few.x)
+        moe.moe_layer_fwd_few(few.cfg, few.Wr, few.bias, few.packed, x, out, few.ws)
+    s.synchronize()
+    assert torch.equal(out, want)
