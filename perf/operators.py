@@ -276,8 +276,10 @@ def _own(st):
         return out
     if st["op"] == "norm_bwd":
         dx, dgain = torch.empty_like(st["dy"]), torch.empty_like(st["gain"])
-        moe.moe_add_rmsnorm_bwd(st["dy"], st["gain"], st["rstd"], dx, dgain, st["ws"], summed=st.get("s"),
-                                ck_codes=st.get("codes"), ck_scales=st.get("scales"), dsum=st["dsum"])
+        ck = st["checkpoint"]
+        moe.moe_add_rmsnorm_bwd(st["dy"], st["gain"], st["rstd"], dx, dgain, st["ws"], summed=None if ck else st["s"],
+                                ck_codes=st["codes"] if ck else None, ck_scales=st["scales"] if ck else None,
+                                dsum=st["dsum"])
         return {"dx": dx, "dgain": dgain}
     x, r = st["x"], st["residual"]
     rows, cols = x.shape
