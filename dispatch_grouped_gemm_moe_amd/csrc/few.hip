@@ -275,94 +275,99 @@ __device__ __forceinline__ intx8 cat8(intx4 a, intx4 b) {
 // 16 bytes at 16 (l / 16) of each half line: for bf16 the operands of two
 // 16x16x32 MFMAs, for MXFP8 those of one scaled 16x16x128 MFMA, whose scale of
 // (row m, block b) comes from lane m + 16 b.
-template <bool MX, int MT>
-struct FewStep {
-    intx4 w[4][2];
-    intx4 x[MT][2];
-    uint32_t ws[MX ? 4 : 1];
-    uint32_t xs[MX ? MT : 1];
+template <bool MX, int N>
+struct FewFrag {
+    intx4 v[N][2];
+    uint32_t s[MX ? N : 1];
 };
 
-struct FewTile {
-    const uint8_t* w;       // the tile's first weight row
-    uint32_t w_row;         // bytes per weight row
-    const uint8_t* w_scale; // MX: operand-layout scales of the tile's first row
-    uint32_t w_group;       // MX: bytes between the scale dwords of consecutive 128 columns
-    const uint8_t* x;       // token rows
-    const uint8_t* x_scale; // MX
-    uint32_t x_group;       // MX: as w_group (or 4 where a row's dwords are adjacent)
-    int kb;                 // bytes of a row
+// One operand of a tile: rows of data and, for MXFP8, their scale dwords
+// (`group` bytes from one 128-column group to the next).  Buffer loads: a
+// lane's offset stays, the step is the scalar offset, and a buffer of no bytes
+// gives zeros without touching memory.
+struct FewOperand {
+    const void* data;
+    const void* scale;
+    uint32_t bytes, scale_bytes, group;
 };
 
-template <bool MX, int MT>
-__device__ __forceinline__ void few_load(const FewTile& f, int nmt, int c, uint32_t woff, const uint32_t* xoff,
-                                         uint32_t wsoff, const uint32_t* xsoff, FewStep<MX, MT>& s) {
-    const uint32_t at = (uint32_t)c * kFgChunk;
-    const bool whole = !MX || (int)at + kFgChunk <= f.kb;  // an MXFP8 row may end in half a line
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+}
+
+// Fragments of step c of rows of kb bytes: zeros past the row's end, which for
+// MXFP8 rows of an odd multiple of 64 columns is in the middle of a line.  (The
+// scalar offset counts against the buffer's size, so it is zero there too.)
+template <bool MX, int N>
+__device__ __forceinline__ void few_load(const FewOperand& o, int kb, int c, const uint32_t (&off)[N],
+                                         const uint32_t (&soff)[N], FewFrag<MX, N>& f) {
+    const int at = c * kFgChunk;
+    const bool in = at < kb, whole = MX ? at + kFgChunk / 2 < kb : in;
+    const __amdgpu_buffer_rsrc_t lo = few_rsrc(o.data, in ? o.bytes : 0), hi = few_rsrc(o.data, whole ? o.bytes : 0);
+    const __amdgpu_buffer_rsrc_t sc = few_rsrc(o.scale, in ? o.scale_bytes : 0);
+    const int lo_at = in ? at : 0, hi_at = whole ? at : 0, sc_at = in ? c * (int)o.group : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t o = woff + (uint32_t)i * 16 * f.w_row + at;
-        s.w[i][0] = *(const intx4*)(f.w + o);
-        s.w[i][1] = whole ? *(const intx4*)(f.w + (o + 64)) : intx4{0, 0, 0, 0};
-        if (MX) s.ws[i] = *(const uint32_t*)(f.w_scale + (wsoff + (uint32_t)i * 64 + (uint32_t)c * f.w_group));
+    for (int i = 0; i < N; ++i) {
+        f.v[i][0] = __builtin_amdgcn_raw_buffer_load_b128(lo, off[i], lo_at, 0);
+        f.v[i][1] = __builtin_amdgcn_raw_buffer_load_b128(hi, off[i] + kFgChunk / 2, hi_at, 0);
+        if (MX) f.s[i] = __builtin_amdgcn_raw_buffer_load_b32(sc, soff[i], sc_at, 0);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        if (m < nmt) {
-            s.x[m][0] = *(const intx4*)(f.x + (xoff[m] + at));
-            s.x[m][1] = whole ? *(const intx4*)(f.x + (xoff[m] + at + 64)) : intx4{0, 0, 0, 0};
-            if (MX) s.xs[m] = *(const uint32_t*)(f.x_scale + (xsoff[m] + (uint32_t)c * f.x_group));
-        }
 }
 
 template <bool MX, int MT>
-__device__ __forceinline__ void few_mfma(const FewStep<MX, MT>& s, int nmt, int shift, floatx4 (&acc)[4][MT]) {
+__device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<MX, MT>& x, int shift,
+                                         floatx4 (&acc)[4][MT]) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-        if (m < nmt) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (MX) {
-                    acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        cat8(s.w[i][0], s.w[i][1]), cat8(s.x[m][0], s.x[m][1]), acc[i][m], 0, 0, 0,
-                        (int)(s.ws[i] >> shift), 0, (int)(s.xs[m] >> shift));
-                } else {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (MX) {
+                acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    cat8(w.v[i][0], w.v[i][1]), cat8(x.v[m][0], x.v[m][1]), acc[i][m], 0, 0, 0, (int)(w.s[i] >> shift),
+                    0, (int)(x.s[m] >> shift));
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, s.w[i][j]), __builtin_bit_cast(bf16x8, s.x[m][j]), acc[i][m], 0,
-                            0, 0);
-                }
+                for (int j = 0; j < 2; ++j)
+                    acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[i][j]),
+                                                                        __builtin_bit_cast(bf16x8, x.v[m][j]),
+                                                                        acc[i][m], 0, 0, 0);
             }
         }
 }
 
 // acc[i][m] (+)= weight rows 16 i .. of the tile times token rows 16 m .., over
-// the steps wave, wave + 8, ... of the row.
+// the steps wave, wave + 8, ... of the rows' kb bytes.  The weights of one step
+// are in flight while the step before is multiplied; the tokens, which come
+// from the L2, are loaded in their own step, ahead of the next weights, so that
+// waiting for them (loads return in order) leaves those in flight.  Steps past
+// the end load zeros, so the loop has one exit and keeps its registers.
 template <bool MX, int MT>
-__device__ __forceinline__ void few_stream(const FewTile& f, int nmt, int wave, int lane, const uint32_t* xrow,
-                                           const uint32_t* xsrow, floatx4 (&acc)[4][MT]) {
-    const int nc = (f.kb + kFgChunk - 1) / kFgChunk;
+__device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperand& xo, int kb, int wave, int lane,
+                                           const uint32_t (&xrow)[MT], const uint32_t (&xsoff)[MT],
+                                           floatx4 (&acc)[4][MT]) {
     const uint32_t lo = (uint32_t)(lane >> 4) * 16;
-    const uint32_t woff = (uint32_t)(lane & 15) * f.w_row + lo;
-    const uint32_t wsoff = (uint32_t)(lane & 15) * 4;
-    uint32_t xoff[MT];
+    uint32_t woff[4], wsoff[4], xoff[MT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        woff[i] = (uint32_t)(i * 16 + (lane & 15)) * (uint32_t)kb + lo;
+        wsoff[i] = (uint32_t)(i * 16 + (lane & 15)) * 4;
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m) xoff[m] = xrow[m] + lo;
     const int shift = 8 * (lane >> 4);
-    int c = wave;
-    if (c >= nc) return;
-    FewStep<MX, MT> s0, s1;
-    few_load<MX, MT>(f, nmt, c, woff, xoff, wsoff, xsrow, s0);
-    for (;;) {
-        if (c + kFgWaves >= nc) { few_mfma<MX, MT>(s0, nmt, shift, acc); break; }
-        c += kFgWaves;
-        few_load<MX, MT>(f, nmt, c, woff, xoff, wsoff, xsrow, s1);
-        few_mfma<MX, MT>(s0, nmt, shift, acc);
-        if (c + kFgWaves >= nc) { few_mfma<MX, MT>(s1, nmt, shift, acc); break; }
-        c += kFgWaves;
-        few_load<MX, MT>(f, nmt, c, woff, xoff, wsoff, xsrow, s0);
-        few_mfma<MX, MT>(s1, nmt, shift, acc);
+    FewFrag<MX, 4> w0, w1;
+    FewFrag<MX, MT> x;
+    auto step = [&](int c, const FewFrag<MX, 4>& w, FewFrag<MX, 4>& next) {
+        few_load<MX, MT>(xo, kb, c, xoff, xsoff, x);
+        few_load<MX, 4>(wo, kb, c + kFgWaves, woff, wsoff, next);
+        __builtin_amdgcn_sched_barrier(0);
+        few_mfma<MX, MT>(w, x, shift, acc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    few_load<MX, 4>(wo, kb, wave, woff, wsoff, w0);
+    for (int c = wave; c * kFgChunk < kb; c += 2 * kFgWaves) {
+        step(c, w0, w1);
+        step(c + kFgWaves, w1, w0);
     }
 }
 
@@ -379,29 +384,29 @@ template <bool MX, int MT>
 __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int H = a.H, I = a.I, nmt = ceil_div(rows, 16);
-    FewTile f;
-    if (MX) {
-        f.w = a.w1q + ((size_t)e * 2 * I + (size_t)n * kFgRows) * H;
-        f.w_row = H;
-        f.w_scale = a.s1 + (size_t)e * mx_groups(H) * 2 * I * 4 + (size_t)n * kFgRows * 4;
-        f.w_group = (uint32_t)2 * I * 4;
-        f.x = a.xq;
-        f.x_scale = a.xs;
-        f.x_group = (uint32_t)a.T * 4;
-        f.kb = H;
+    const int H = a.H, I = a.I;
+    const uint32_t kb = (uint32_t)H * (MX ? 1 : 2);
+    FewOperand wo{}, xo{};
+    wo.bytes = kFgRows * kb;
+    xo.bytes = (uint32_t)a.T * kb;
+    if constexpr (MX) {
+        wo.data = a.w1q + ((int64_t)e * 2 * I + (int64_t)n * kFgRows) * H;
+        wo.scale = a.s1 + ((int64_t)e * mx_groups(H) * 2 * I + (int64_t)n * kFgRows) * 4;
+        wo.group = (uint32_t)2 * I * 4;
+        wo.scale_bytes = ((uint32_t)mx_groups(H) - 1) * wo.group + kFgRows * 4;
+        xo.data = a.xq;
+        xo.scale = a.xs;
+        xo.group = (uint32_t)a.T * 4;
+        xo.scale_bytes = (uint32_t)mx_groups(H) * xo.group;
     } else {
-        f.w = (const uint8_t*)(a.w1 + ((size_t)e * 2 * I + (size_t)n * kFgRows) * H);
-        f.w_row = (uint32_t)H * 2;
-        f.w_scale = nullptr; f.w_group = 0; f.x_scale = nullptr; f.x_group = 0;
-        f.x = (const uint8_t*)a.x;
-        f.kb = H * 2;
+        wo.data = a.w1 + ((int64_t)e * 2 * I + (int64_t)n * kFgRows) * H;
+        xo.data = a.x;
     }
     uint32_t xrow[MT], xsrow[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int t = a.row_token[row0 + min(m * 16 + (lane & 15), rows - 1)];
-        xrow[m] = (uint32_t)t * (uint32_t)f.kb;
+        xrow[m] = (uint32_t)t * kb;
         xsrow[m] = (uint32_t)t * 4;
     }
     floatx4 acc[4][MT];
@@ -409,13 +414,13 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT>(f, nmt, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
     // thread (token tid / 32, column tid % 32): the tile's rows are 32 gate
     // columns and the 32 up columns of the same indices
     const int tt = tid >> 5, col = tid & 31;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        if (m >= nmt) break;
+        if (m * 16 >= rows) break;
         __syncthreads();
         few_stage<MT>(acc, m, wave, lane, s_part);
         __syncthreads();
@@ -452,29 +457,29 @@ template <bool MX, int MT>
 __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int H = a.H, I = a.I, nmt = ceil_div(rows, 16);
-    FewTile f;
-    if (MX) {
-        f.w = a.w2q + ((size_t)e * H + (size_t)n * kFgRows) * I;
-        f.w_row = I;
-        f.w_scale = a.s2 + (size_t)e * mx_groups(I) * H * 4 + (size_t)n * kFgRows * 4;
-        f.w_group = (uint32_t)H * 4;
-        f.x = a.hq + (size_t)row0 * I;
-        f.x_scale = a.hs + (size_t)row0 * mx_groups(I) * 4;
-        f.x_group = 4;
-        f.kb = I;
+    const int H = a.H, I = a.I;
+    const uint32_t kb = (uint32_t)I * (MX ? 1 : 2);
+    FewOperand wo{}, xo{};
+    wo.bytes = kFgRows * kb;
+    xo.bytes = (uint32_t)rows * kb;
+    if constexpr (MX) {
+        wo.data = a.w2q + ((int64_t)e * H + (int64_t)n * kFgRows) * I;
+        wo.scale = a.s2 + ((int64_t)e * mx_groups(I) * H + (int64_t)n * kFgRows) * 4;
+        wo.group = (uint32_t)H * 4;
+        wo.scale_bytes = ((uint32_t)mx_groups(I) - 1) * wo.group + kFgRows * 4;
+        xo.data = a.hq + (int64_t)row0 * I;
+        xo.scale = a.hs + (int64_t)row0 * mx_groups(I) * 4;
+        xo.group = 4;
+        xo.scale_bytes = (uint32_t)rows * (uint32_t)mx_groups(I) * 4;
     } else {
-        f.w = (const uint8_t*)(a.w2 + ((size_t)e * H + (size_t)n * kFgRows) * I);
-        f.w_row = (uint32_t)I * 2;
-        f.w_scale = nullptr; f.w_group = 0; f.x_scale = nullptr; f.x_group = 0;
-        f.x = (const uint8_t*)(a.h + (size_t)row0 * I);
-        f.kb = I * 2;
+        wo.data = a.w2 + ((int64_t)e * H + (int64_t)n * kFgRows) * I;
+        xo.data = a.h + (int64_t)row0 * I;
     }
     uint32_t xrow[MT], xsrow[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const uint32_t r = (uint32_t)min(m * 16 + (lane & 15), rows - 1);
-        xrow[m] = r * (uint32_t)f.kb;
+        xrow[m] = r * kb;
         xsrow[m] = r * (uint32_t)mx_groups(I) * 4;
     }
     floatx4 acc[4][MT];
@@ -482,11 +487,11 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT>(f, nmt, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
     const int tt = tid >> 5, col = (tid & 31) * 2;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        if (m >= nmt) break;
+        if (m * 16 >= rows) break;
         __syncthreads();
         few_stage<MT>(acc, m, wave, lane, s_part);
         __syncthreads();
@@ -506,23 +511,33 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
     }
 }
 
+template <bool kDown, bool MX, int MT>
+__device__ __forceinline__ void few_tile(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
+    if constexpr (kDown) few_down<MX, MT>(a, e, n, row0, rows, s_part);
+    else few_gate_up<MX, MT>(a, e, n, row0, rows, s_part);
+}
+
+// The tile's code by the 16-row fragments that the expert's rows fill (three
+// run as four, the rows past the last repeating it).
+template <bool kDown, bool MX, int kMost>
+__device__ __forceinline__ void few_tile_rows(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
+    if (kMost == 1 || rows <= 16) few_tile<kDown, MX, 1>(a, e, n, row0, rows, s_part);
+    else if (kMost == 2 || rows <= 32) few_tile<kDown, MX, 2>(a, e, n, row0, rows, s_part);
+    else few_tile<kDown, MX, 4>(a, e, n, row0, rows, s_part);
+}
+
 // Workgroup b: active expert b / n_tiles, weight rows 64 (b % n_tiles) .. + 63.
 // The host sizes the grid for every expert that T * k choices can reach; the
-// workgroups past the active ones end at once.
-template <bool kDown, bool kMx, int MT>
+// workgroups past the active ones end at once.  kMost: 16-row fragments of T.
+template <bool kDown, bool kMx, int kMost>
 __global__ __launch_bounds__(kFgThreads) void few_gemm_kernel(FewGemm a) {
     __shared__ __attribute__((aligned(16))) float s_part[kFgWaves * 16 * kFgLd];
     const int nt = kDown ? a.H / kFgRows : a.I / 32;
     const int i = blockIdx.x / nt, n = blockIdx.x - i * nt;
     if (i >= ld_layout(a.n_act)) return;
     const int e = ld_layout(a.act_e + i), row0 = ld_layout(a.act_off + i), rows = ld_layout(a.act_off + i + 1) - row0;
-    if (kMx && e < a.E) {
-        if constexpr (kDown) few_down<true, MT>(a, e, n, row0, rows, s_part);
-        else few_gate_up<true, MT>(a, e, n, row0, rows, s_part);
-    } else {
-        if constexpr (kDown) few_down<false, MT>(a, e, n, row0, rows, s_part);
-        else few_gate_up<false, MT>(a, e, n, row0, rows, s_part);
-    }
+    if (kMx && e < a.E) few_tile_rows<kDown, true, kMost>(a, e, n, row0, rows, s_part);
+    else few_tile_rows<kDown, false, kMost>(a, e, n, row0, rows, s_part);
 }
 
 template <bool kDown>
