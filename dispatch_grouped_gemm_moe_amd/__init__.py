@@ -32,7 +32,7 @@ EXPORTS = ("moe_status_string", "moe_abi_version", "moe_validate_cfg", "moe_quer
            "moe_add_rmsnorm_fwd", "moe_add_rmsnorm_bwd", "moe_query_add_rmsnorm_bwd", "moe_layer_fwd_few",
            "moe_query_few")
 MOE_STATIC_WORKSPACE_BYTES = 256 << 20
-MOE_FEW_MAX_TOKENS = 64
+MOE_FEW_MAX_TOKENS, MOE_FEW_COUNTER_BYTES = 64, 512
 KERNEL_KINDS = ("route", "layout", "gemm_gate_up", "gemm_down", "combine", "gather", "other", "wgrad",
                 "dgrad_down", "dgrad_gate_up", "shared_gemm", "layer")
 
@@ -308,8 +308,8 @@ def moe_query_few(cfg: moe_cfg) -> int:
 
 
 def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=None, stream=None):
-    """Layer forward for cfg.T <= MOE_FEW_MAX_TOKENS tokens; ws: moe_query_few bytes, its first 256 zeroed
-    once."""
+    """Layer forward for cfg.T <= MOE_FEW_MAX_TOKENS tokens; ws: moe_query_few bytes, the first
+    MOE_FEW_COUNTER_BYTES of them zeroed once."""
     import torch
     fn = "moe_layer_fwd_few"
     T, H, E = cfg.T, cfg.H, cfg.E

@@ -997,7 +997,7 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t* dy, c
 
 // Workspace of moe_layer_fwd_few (byte offsets).
 struct FewPlan {
-    size_t counter, n_act, act_e, act_off, row_token, row_w, slot_row, logits, xq, xs, h, hq, hs, y, total;
+    size_t counter, partial, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row, logits, xq, xs, h, hq, hs, y, total;
     int max_act;  // experts that T * k choices can reach, and the shared one
 };
 
@@ -1006,15 +1006,19 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
     if (st != MOE_OK) return st;
     if (p->T > kFewTokens || p->identity) return MOE_E_UNSUPPORTED;
     const size_t T = p->T, H = p->H, I = p->I, Tk = T * p->k, rows = Tk + (p->shared ? T : 0);
-    size_t o = kAlign;  // the counters, zero between calls
+    static_assert(kFewCounters * 4 <= MOE_FEW_COUNTER_BYTES, "the counters fit their block");
+    size_t o = MOE_FEW_COUNTER_BYTES;  // the counters, zero between calls
     f->counter = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
+    f->sel_e = take(Tk * 4);
+    f->sel_w = take(Tk * 4);
     f->n_act = take(4);
     f->act_e = take((size_t)p->Et * 4);
     f->act_off = take(((size_t)p->Et + 1) * 4);
     f->row_token = take(rows * 4);
     f->row_w = take(rows * 4);
     f->slot_row = take(Tk * 4);
+    f->partial = take(T * p->E * 16 * 4);
     f->logits = take(T * p->E * 4);
     f->h = take(rows * I * 2);
     f->y = take(rows * H * 4);
@@ -1056,10 +1060,12 @@ moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uin
     const uint8_t* pk = (const uint8_t*)w->packed;
     FewRoute r{};
     r.x = x; r.Wr = w->Wr; r.bias = w->bias; r.T = p.T; r.H = p.H; r.E = p.E; r.k = p.k; r.shared = p.shared;
+    r.partial = (float*)(b + f.partial);
     r.logits = (float*)(b + f.logits);
     r.xq = p.mx && !x_codes ? b + f.xq : nullptr;
     r.xs = p.mx && !x_codes ? b + f.xs : nullptr;
     r.counter = (int*)(b + f.counter);
+    r.sel_e = (int*)(b + f.sel_e); r.sel_w = (float*)(b + f.sel_w);
     r.n_act = (int*)(b + f.n_act); r.act_e = (int*)(b + f.act_e); r.act_off = (int*)(b + f.act_off);
     r.row_token = (int*)(b + f.row_token); r.row_w = (float*)(b + f.row_w); r.slot_row = (int*)(b + f.slot_row);
     TIMED(MOE_K_ROUTE, s, launch_few_route(r, s));

@@ -26,230 +26,320 @@ namespace moe {
 // ---------------------------------------------------------------------------
 
 constexpr int kFrThreads = 512;
-constexpr int kFrEC = 4;         // experts per workgroup
-constexpr int kFrTok = 16;       // tokens per workgroup, two per wave
-constexpr int kFrSlab = 2048;    // h per LDS slab
-constexpr int kFrWL = kFrSlab / kFrThreads;                   // weight rows (16 bytes) per thread and slab
-constexpr int kFrXL = kFrTok * kFrSlab / 8 / kFrThreads;      // 16-byte pieces of x per thread and slab
+constexpr int kFrWaves = kFrThreads / kWave;
+constexpr int kFrTok = kFrWaves;  // tokens per workgroup, one per wave
+constexpr int kFrEC = 32;         // experts per workgroup: a cache line of a router weight row
+constexpr int kFrRes = 16;        // residue groups: group l takes h mod 64 in {l, l + 16, l + 32, l + 48}
+constexpr int kFrSlab = 128;      // 64-wide chunks of h per LDS slab
 
-__device__ __forceinline__ float tree64(float v) {
-    // halving tree p[l] += p[l+s], s = 32, 16, ..., 1 (the result is lane 0's)
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v = v + __shfl_xor(v, s, kWave);
-    return v;
+template <int kCtrl>
+__device__ __forceinline__ float dpp_max(float v) {
+    const int o = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, v), __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF,
+                                              false);
+    return fmaxf(v, __builtin_bit_cast(float, o));
 }
 
-// Top-k of every token and the experts' row lists, by the workgroup that
-// finishes the logits last.  At most 64 tokens: an expert's tokens are one
-// 64-bit mask, a row's rank within its expert a population count.
-__device__ void few_layout(const FewRoute& a, uint64_t* s_mask, int* s_idx, float* s_w, int* s_off) {
+// Largest value of the wave, uniform (no NaN among them).
+__device__ __forceinline__ float wave_max(float v) {
+    v = dpp_max<0x111>(v);  // row_shr:1, 2, 4, 8: lane 15 of a row has the row's
+    v = dpp_max<0x112>(v);
+    v = dpp_max<0x114>(v);
+    v = dpp_max<0x118>(v);
+    v = dpp_max<0x142>(v);  // row_bcast:15, 31: lane 63 has the wave's
+    v = dpp_max<0x143>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), kWave - 1));
+}
+
+__device__ __forceinline__ int agent_load(const int* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void agent_store(int* p, int v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Whether this workgroup is the last of n to count in; what the others stored
+// with agent_store before is then readable with agent_load (both go past the
+// XCD's cache, so no cache is written back or dropped).  The last one leaves
+// the counter at zero for the next call.
+__device__ __forceinline__ bool counts_in_last(int* counter, int n, int* s_flag) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores have reached memory
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (before == n - 1) agent_store(counter, 0);
+        *s_flag = before == n - 1;
+    }
+    __syncthreads();
+    const bool last = *s_flag != 0;
+    __syncthreads();
+    return last;
+}
+
+// Top-k of one token by one wave: its selections and their softmax weights,
+// selection j in lane j.
+__device__ __forceinline__ void few_topk(const float* logits, int E, int k, int lane, int& sel, float& weight) {
+    constexpr int kQ = kMaxExperts / kWave;
+    float v[kQ];
+    unsigned open = 0;  // bit q: expert lane + 64 q may still be chosen
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        const int e = lane + q * kWave;
+        v[q] = -INFINITY;
+        if (e < E) {
+            const float z = logits[e];
+            // a NaN compares with nothing: as the lowest value the order stays total
+            if (z == z) v[q] = z;
+            open |= 1u << q;
+        }
+    }
+    int mine = 0;
+    float mv = 0.0f, first = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) m = fmaxf(m, (open >> q & 1) ? v[q] : -INFINITY);
+        m = wave_max(m);
+        int best = 0;  // the lowest index among the open experts of that value: k <= E leaves one
+#pragma unroll
+        for (int q = kQ - 1; q >= 0; --q) {
+            const uint64_t at = __ballot((open >> q & 1) && v[q] == m);
+            if (at) best = q * kWave + __builtin_ctzll(at);
+        }
+        if ((best & (kWave - 1)) == lane) open &= ~(1u << (best / kWave));
+        if (j == 0) first = m;
+        if (lane == j) { mine = best; mv = m; }
+    }
+    const float z = expf(mv - first);
+    float den = 0.0f;  // summed in slot order
+    for (int j = 0; j < k; ++j)
+        den = den + __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, z), j));
+    sel = mine;
+    weight = z / den;
+}
+
+// LDS of the row lists.
+struct FewLists {
+    uint64_t mask[kMaxExperts];  // tokens of each expert
+    int off[kMaxExperts];        // its first row
+    int wave_rows[kMaxExperts / kWave], wave_act[kMaxExperts / kWave];
+    int sel_e[kFewTokens * kMaxTopK];  // every token's selections
+    float sel_w[kFewTokens * kMaxTopK];
+};
+
+// The experts' row lists.  At most 64 tokens: an expert's tokens are one 64-bit
+// mask, and a row's rank within its expert a population count.
+__device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int T = a.T, E = a.E, k = a.k;
-    for (int e = tid; e < kMaxExperts; e += kFrThreads) s_mask[e] = 0;
+    const int n = a.T * a.k;
+    static_assert(kFewTokens * kMaxTopK == 2 * kFrThreads && kMaxExperts <= kFrThreads, "selections and experts per thread");
+    if (tid < kMaxExperts) s.mask[tid] = 0;
     __syncthreads();
-    for (int t = wave; t < T; t += kFrThreads / kWave) {
-        float v[kMaxExperts / kWave];
-        unsigned taken = 0;
 #pragma unroll
-        for (int q = 0; q < kMaxExperts / kWave; ++q) {
-            const int e = lane + q * kWave;
-            // written by other workgroups of this launch: read past this XCD's cache
-            v[q] = e < E ? __hip_atomic_load(a.logits + (size_t)t * E + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                         : 0.0f;
-            // a NaN compares with nothing: as the lowest value the order stays
-            // total, so every lane picks the same k distinct experts
-            if (v[q] != v[q]) v[q] = -INFINITY;
-            if (e >= E) taken |= 1u << q;
+    for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * kFrThreads;
+        if (i < n) atomicOr((unsigned long long*)&s.mask[s.sel_e[i]], 1ull << (i / a.k));
+    }
+    __syncthreads();
+    // exclusive prefixes over the experts, of rows and of experts that have any
+    int c = 0, inc = 0;
+    uint64_t on = 0;
+    if (tid < kMaxExperts) {
+        c = __popcll(s.mask[tid]);
+        inc = c;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int o = __shfl_up(inc, d, kWave);
+            if (lane >= d) inc += o;
         }
-        float first = 0.0f, den = 0.0f, ez = 0.0f;
-        int mine = -1;  // lane j keeps selection j
-        for (int j = 0; j < k; ++j) {
-            float bv = 0.0f;
-            int bi = 0x7fffffff;
-#pragma unroll
-            for (int q = 0; q < kMaxExperts / kWave; ++q)
-                if (!(taken & (1u << q)) && (bi == 0x7fffffff || v[q] > bv)) { bv = v[q]; bi = lane + q * kWave; }
-#pragma unroll
-            for (int s = 32; s >= 1; s >>= 1) {
-                const float ov = __shfl_xor(bv, s, kWave);
-                const int oi = __shfl_xor(bi, s, kWave);
-                if (oi != 0x7fffffff && (bi == 0x7fffffff || ov > bv || (ov == bv && oi < bi))) { bv = ov; bi = oi; }
-            }
-            if (j == 0) first = bv;
-            const float z = expf(bv - first);
-            den = den + z;
-            if (lane == j) { mine = bi; ez = z; }
-            if ((bi & (kWave - 1)) == lane) taken |= 1u << (bi / kWave);
-        }
-        if (lane < k) {
-            s_idx[t * k + lane] = mine;
-            s_w[t * k + lane] = ez / den;
-            atomicOr((unsigned long long*)&s_mask[mine], 1ull << t);
+        on = __ballot(c > 0);
+        if (lane == kWave - 1) {
+            s.wave_rows[wave] = inc;
+            s.wave_act[wave] = __popcll(on);
         }
     }
     __syncthreads();
-    // exclusive prefix of rows and of active experts over the experts (wave 0)
-    if (wave == 0) {
-        int rows = 0, act = 0;
-        for (int e0 = 0; e0 < E; e0 += kWave) {
-            const int e = e0 + lane;
-            const int c = e < E ? __popcll(s_mask[e]) : 0;
-            int inc = c;
-#pragma unroll
-            for (int s = 1; s < kWave; s <<= 1) {
-                const int o = __shfl_up(inc, s, kWave);
-                if (lane >= s) inc += o;
-            }
-            const uint64_t on = __ballot(c > 0);
-            const int at = act + __popcll(on & ((1ull << lane) - 1ull));
-            if (e < E) s_off[e] = rows + inc - c;
+    int rows = 0, act = 0;
+    for (int w = 0; w < kMaxExperts / kWave; ++w) {
+        if (w == wave && tid < kMaxExperts) {
+            const int off = rows + inc - c;
+            s.off[tid] = off;
             if (c > 0) {
-                a.act_e[at] = e;
-                a.act_off[at] = rows + inc - c;
+                const int at = act + __popcll(on & ((1ull << lane) - 1ull));
+                a.act_e[at] = tid;
+                a.act_off[at] = off;
             }
-            rows += __shfl(inc, kWave - 1, kWave);
-            act += __popcll(on);
         }
-        if (lane == 0) {
-            if (a.shared) {  // the shared expert takes every token, after the routed rows
-                a.act_e[act] = E;
-                a.act_off[act] = rows;
-                ++act;
-                rows += T;
-            }
+        rows += s.wave_rows[w];
+        act += s.wave_act[w];
+    }
+    if (tid == 0) {
+        if (a.shared) {  // the shared expert takes every token, after the routed rows
+            a.act_e[act] = a.E;
             a.act_off[act] = rows;
-            *a.n_act = act;
+            ++act;
+            rows += a.T;
         }
+        a.act_off[act] = rows;
+        *a.n_act = act;
     }
     __syncthreads();
-    for (int i = tid; i < T * k; i += kFrThreads) {
-        const int t = i / k, e = s_idx[i];
-        const int row = s_off[e] + __popcll(s_mask[e] & ((1ull << t) - 1ull));
-        a.row_token[row] = t;
-        a.row_w[row] = s_w[i];
-        a.slot_row[i] = row;
-    }
-    if (a.shared)
-        for (int t = tid; t < T; t += kFrThreads) {
-            a.row_token[T * k + t] = t;
-            a.row_w[T * k + t] = 1.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * kFrThreads;
+        if (i < n) {
+            const int t = i / a.k, e = s.sel_e[i];
+            const int row = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1ull));
+            a.row_token[row] = t;
+            a.row_w[row] = s.sel_w[i];
+            a.slot_row[i] = row;
         }
+    }
+    if (a.shared && tid < a.T) {
+        a.row_token[n + tid] = tid;
+        a.row_w[n + tid] = 1.0f;
+    }
 }
 
-// Workgroup (x, y): experts 4x .. 4x+3 for tokens 16y .. 16y+15.  The logits'
-// order is moe_route's: lane l sums h = l, l + 64, ... with fused
-// multiply-adds, then the halving tree, then the bias.  Slabs of kFrSlab rows
-// of the router weight and of the tokens go through LDS, the next slab's loads
-// in flight while one is summed.
+// Workgroup (l, x, y): residues l, l + 16, l + 32, l + 48 of h mod 64, experts
+// 32 x .. 32 x + 31, tokens 8 y .. 8 y + 7, a wave per token.
+//
+// The logits' order is moe_route's: p[r] sums h = r, r + 64, ... with fused
+// multiply-adds, a halving tree joins the 64 p[r], the bias comes last.  The
+// sums over h are chains, but the 64 residues are independent, so they are what
+// is spread over workgroups: each asks for its rows of the router weight (whole
+// cache lines) and its tokens' values at once and waits for memory once.  What
+// this costs is latency and cache lines per workgroup (about 350 lines a
+// microsecond), not bytes.  Splitting the experts alone instead (every
+// workgroup all of h, 16 bytes of each line) took 26 us for one token of H 7168
+// and 32 experts, and 27 us for 64 tokens.
+//
+// A lane holds expert lane % 32; its half of the wave residues l + 16 half and
+// l + 16 half + 32: the first two tree levels stay in the wave.  The workgroup
+// of an (x, y) that counts in last joins the 16 groups' sums to logits, the
+// last of a y picks its tokens' experts, the last y builds the row lists.
 template <bool kVec4>
 __global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
-    __shared__ __attribute__((aligned(16))) float s_wr[kFrSlab][kFrEC];
-    __shared__ __attribute__((aligned(16))) uint16_t s_x[kFrTok][kFrSlab];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int e0 = blockIdx.x * kFrEC, t0 = blockIdx.y * kFrTok;
-    const int T = a.T, H = a.H, E = a.E;
-    const int nt = min(kFrTok, T - t0);
-    floatx4 wn[kFrWL];
-    intx4 xn[kFrXL];
-    auto load = [&](int h0) {
-#pragma unroll
-        for (int i = 0; i < kFrWL; ++i) {
-            const int h = h0 + i * kFrThreads + tid;
-            floatx4 v = {0, 0, 0, 0};
-            if (h < H) {
-                const float* p = a.Wr + (size_t)h * E + e0;
-                if (kVec4) {
-                    v = *(const floatx4*)p;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < kFrEC; ++q) v[q] = e0 + q < E ? p[q] : 0.0f;
-                }
+    __shared__ __attribute__((aligned(1024))) float s_wr[kFrSlab * 4][kFrEC];
+    __shared__ __attribute__((aligned(16))) float s_x[kFrTok][2][kFrSlab][2];
+    __shared__ float s_logit[kFrTok][kMaxExperts];
+    __shared__ FewLists s_lists;
+    __shared__ int s_flag;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l = blockIdx.x, e0 = blockIdx.y * kFrEC, t0 = blockIdx.z * kFrTok;
+    const int ng = gridDim.y, nz = gridDim.z;
+    const int T = a.T, H = a.H, E = a.E, k = a.k;
+    const int nt = min(kFrTok, T - t0), ne = min(kFrEC, E - e0);
+    const int half = lane >> 5, el = lane & 31;
+    float p0 = 0.0f, p1 = 0.0f;
+    for (int c0 = 0; c0 < H / kWave; c0 += kFrSlab) {
+        const int nc = min(kFrSlab, H / kWave - c0);
+        if (c0) __syncthreads();  // the previous slab is summed
+        // LDS row 4 c + j: h = 64 (c0 + c) + l + 16 j
+        auto h_of = [&](int r) { return (c0 + (r >> 2)) * kWave + l + 16 * (r & 3); };
+        if (kVec4 && ne == kFrEC) {
+            // eight rows per load; a slab's rows are a multiple of four
+            for (int r = wave * 8; r < nc * 4; r += kFrWaves * 8)
+                __builtin_amdgcn_global_load_lds(
+                    (gbl_cvoid*)(a.Wr + (size_t)h_of(min(r + (lane >> 3), nc * 4 - 1)) * E + e0 + (lane & 7) * 4),
+                    (lds_void*)s_wr[r], 16, 0, 0);
+        } else {
+            for (int i = tid; i < nc * 4 * kFrEC; i += kFrThreads) {
+                const int r = i / kFrEC, q = i % kFrEC;
+                s_wr[r][q] = q < ne ? a.Wr[(size_t)h_of(r) * E + e0 + q] : 0.0f;
             }
-            wn[i] = v;
         }
+        if (wave < nt) {
+            const uint16_t* xr = a.x + (size_t)(t0 + wave) * H + (size_t)c0 * kWave + l;
+            uint16_t v[kFrSlab / kWave][4];
 #pragma unroll
-        for (int i = 0; i < kFrXL; ++i) {
-            const int p = i * kFrThreads + tid;  // 16-byte piece of the slab: token p / 256
-            const int t = p / (kFrSlab / 8), h = h0 + (p % (kFrSlab / 8)) * 8;
-            intx4 v = {0, 0, 0, 0};
-            if (t < nt && h < H) v = *(const intx4*)(a.x + (size_t)(t0 + t) * H + h);
-            xn[i] = v;
+            for (int i = 0; i < kFrSlab / kWave; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = xr[(size_t)min(i * kWave + lane, nc - 1) * kWave + 16 * j];
+#pragma unroll
+            for (int i = 0; i < kFrSlab / kWave; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s_x[wave][j & 1][i * kWave + lane][j >> 1] = bf16_to_f32(v[i][j]);
         }
-    };
-    float acc[2][kFrEC] = {};
-    load(0);
-    for (int h0 = 0; h0 < H; h0 += kFrSlab) {
-        __syncthreads();  // the previous slab is summed
-#pragma unroll
-        for (int i = 0; i < kFrWL; ++i) *(floatx4*)s_wr[i * kFrThreads + tid] = wn[i];
-#pragma unroll
-        for (int i = 0; i < kFrXL; ++i) {
-            const int p = i * kFrThreads + tid;
-            *(intx4*)&s_x[p / (kFrSlab / 8)][(p % (kFrSlab / 8)) * 8] = xn[i];
-        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads into LDS too
         __syncthreads();
-        if (h0 + kFrSlab < H) load(h0 + kFrSlab);
-        if (wave * 2 < nt) {
-            const int nc = min(kFrSlab, H - h0) / kWave;
-#pragma unroll 4
+        if (wave < nt) {
+            const float* wr = &s_wr[half][el];
+#pragma unroll 8
             for (int c = 0; c < nc; ++c) {
-                const floatx4 w4 = *(const floatx4*)s_wr[c * kWave + lane];
-                const float x0 = bf16_to_f32(s_x[wave * 2][c * kWave + lane]);
-                const float x1 = bf16_to_f32(s_x[wave * 2 + 1][c * kWave + lane]);
-#pragma unroll
-                for (int q = 0; q < kFrEC; ++q) {
-                    acc[0][q] = __builtin_fmaf(x0, w4[q], acc[0][q]);
-                    acc[1][q] = __builtin_fmaf(x1, w4[q], acc[1][q]);
-                }
+                p0 = __builtin_fmaf(s_x[wave][half][c][0], wr[c * 4 * kFrEC], p0);
+                p1 = __builtin_fmaf(s_x[wave][half][c][1], wr[(c * 4 + 2) * kFrEC], p1);
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = t0 + wave * 2 + i;
-        if (wave * 2 + i >= nt) break;
-#pragma unroll
-        for (int q = 0; q < kFrEC; ++q) {
-            float v = tree64(acc[i][q]);
-            if (lane == 0 && e0 + q < E) {
-                if (a.bias) v = v + a.bias[e0 + q];
-                __hip_atomic_store(a.logits + (size_t)t * E + e0 + q, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-        }
+    {
+        float v = p0 + p1;             // p[r] + p[r + 32]
+        v = v + __shfl_xor(v, 32, kWave);  // + 16
+        if (wave < nt && half == 0 && el < ne)
+            agent_store((int*)a.partial + ((size_t)(t0 + wave) * E + e0 + el) * kFrRes + l, __builtin_bit_cast(int, v));
     }
     // MXFP8: the tokens' codes and operand-layout scales, a block of 32 per thread
     if (a.xq) {
-        const int nb = H / 32, ng = gridDim.x * gridDim.y;
-        for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kFrThreads + tid; i < T * nb; i += ng * kFrThreads) {
-            const int t = i / nb, b = i - t * nb;
-            const uint8_t sc = mx_quant_block32(a.x + (size_t)t * H + b * 32, a.xq + (size_t)t * H + b * 32);
-            mx_store_scale_byte(a.xs, T, t, b, nb, sc);
+        const int nb = H / 32, n = gridDim.x * ng * nz;
+        for (int i = ((blockIdx.z * ng + blockIdx.y) * gridDim.x + l) * kFrThreads + tid; i < T * nb;
+             i += n * kFrThreads) {
+            const int ti = i / nb, b = i - ti * nb;
+            const uint8_t sc = mx_quant_block32(a.x + (size_t)ti * H + b * 32, a.xq + (size_t)ti * H + b * 32);
+            mx_store_scale_byte(a.xs, T, ti, b, nb, sc);
         }
     }
-    // The workgroup that counts in last lays the rows out; it leaves the
-    // counter at zero for the next call.
-    __syncthreads();
-    if (tid == 0) {
-        __atomic_thread_fence(__ATOMIC_RELEASE);
-        const int n = gridDim.x * gridDim.y;
-        const int before = __hip_atomic_fetch_add(a.counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = before == n - 1;
-        if (s_last) __hip_atomic_store(a.counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (!counts_in_last(a.counter + 16 + blockIdx.z * ng + blockIdx.y, kFrRes, &s_flag)) return;
+    for (int i = tid; i < nt * ne; i += kFrThreads) {
+        const int ti = i / ne, ei = i - ti * ne;
+        const uint64_t* q = (const uint64_t*)(a.partial + ((size_t)(t0 + ti) * E + e0 + ei) * kFrRes);
+        float v[kFrRes];
+#pragma unroll
+        for (int j = 0; j < kFrRes / 2; ++j) {
+            const uint64_t two = __hip_atomic_load(q + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v[2 * j] = __builtin_bit_cast(float, (uint32_t)two);
+            v[2 * j + 1] = __builtin_bit_cast(float, (uint32_t)(two >> 32));
+        }
+#pragma unroll
+        for (int d = kFrRes / 2; d >= 1; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < d; ++j) v[j] = v[j] + v[j + d];
+        float z = v[0];
+        if (a.bias) z = z + a.bias[e0 + ei];
+        s_logit[ti][e0 + ei] = z;
+        if (ng > 1) agent_store((int*)a.logits + (size_t)(t0 + ti) * E + e0 + ei, __builtin_bit_cast(int, z));
+    }
+    if (ng > 1) {
+        if (!counts_in_last(a.counter + 8 + blockIdx.z, ng, &s_flag)) return;
+        for (int i = tid; i < nt * E; i += kFrThreads)
+            s_logit[i / E][i % E] = __builtin_bit_cast(float, agent_load((const int*)a.logits + (size_t)t0 * E + i));
     }
     __syncthreads();
-    if (!s_last) return;
-    // the slab buffers are free: tables in their place
-    uint64_t* s_mask = (uint64_t*)&s_wr[0][0];              // 256 x 8
-    int* s_off = (int*)(s_mask + kMaxExperts);              // 256 x 4
-    int* s_idx = s_off + kMaxExperts;                       // 64 x 16 x 4
-    float* s_w = (float*)(s_idx + kFewTokens * kMaxTopK);   // 64 x 16 x 4
-    static_assert(sizeof(s_wr) >= kMaxExperts * 12 + kFewTokens * kMaxTopK * 8, "tables fit the slab");
-    few_layout(a, s_mask, s_idx, s_w, s_off);
+    if (wave < nt) {
+        int sel;
+        float weight;
+        few_topk(s_logit[wave], E, k, lane, sel, weight);
+        if (lane < k) {
+            const int i = (t0 + wave) * k + lane;
+            s_lists.sel_e[i] = sel;
+            s_lists.sel_w[i] = weight;
+            if (nz > 1) {
+                agent_store(a.sel_e + i, sel);
+                agent_store((int*)a.sel_w + i, __builtin_bit_cast(int, weight));
+            }
+        }
+    }
+    if (nz > 1) {
+        if (!counts_in_last(a.counter, nz, &s_flag)) return;
+        for (int i = tid; i < T * k; i += kFrThreads) {
+            s_lists.sel_e[i] = agent_load(a.sel_e + i);
+            s_lists.sel_w[i] = __builtin_bit_cast(float, agent_load((const int*)a.sel_w + i));
+        }
+    }
+    few_lists(a, s_lists);
 }
 
 void launch_few_route(const FewRoute& a, hipStream_t stream) {
-    const dim3 grid(ceil_div(a.E, kFrEC), ceil_div(a.T, kFrTok));
+    const dim3 grid(kFrRes, ceil_div(a.E, kFrEC), ceil_div(a.T, kFrTok));
     if (a.E % 4 == 0 && ((uintptr_t)a.Wr & 15) == 0)
         hipLaunchKernelGGL(few_route_kernel<true>, grid, dim3(kFrThreads), 0, stream, a);
     else

@@ -338,15 +338,19 @@ constexpr int kFewTokens = 64;  // most tokens of one call: an expert's tokens a
 // Router of a few tokens: logits, top-k, softmax weights and the experts' row
 // lists.  Rows are grouped by expert in ascending order, by token within an
 // expert; the shared expert's T rows come last.
+constexpr int kFewCounters = 16 + (kFewTokens / 8) * (kMaxExperts / 32);
 struct FewRoute {
     const uint16_t* x;   // [T][H]
     const float* Wr;     // [H][E]
     const float* bias;   // [E] or NULL
     int T, H, E, k, shared;
+    float* partial;      // [T][E][16]
     float* logits;       // [T][E]
     uint8_t* xq;         // MXFP8: codes [T][H] to write, or NULL
     uint8_t* xs;         // their scales, operand layout
-    int* counter;        // zero between calls
+    int* counter;        // [kFewCounters], zero between calls
+    int* sel_e;          // [T][k] chosen experts and their weights
+    float* sel_w;
     int* n_act;          // active experts
     int* act_e;          // [n_act] expert, E for the shared one
     int* act_off;        // [n_act + 1] first row

@@ -397,14 +397,16 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t *dy, c
  *   x_codes, x_scales: MOE_PREC_MXFP8, optional: the MXFP8 form of x as
  *       moe_route or moe_add_rmsnorm_fwd wrote it (codes 16-byte aligned,
  *       scales 4); both or neither.  Without them the call quantises x itself.
- *   ws: at least moe_query_few bytes, 256-byte aligned; zero its first 256
- *       bytes once when it is allocated (every call leaves them zero).
+ *   ws: at least moe_query_few bytes, 256-byte aligned; zero its first
+ *       MOE_FEW_COUNTER_BYTES bytes once when it is allocated (every call
+ *       leaves them zero).
  * cfg->minibatch, ring_slots, comm_cus and the flags other than
  * MOE_F_SHARED_EXPERT have no effect.  MOE_E_UNSUPPORTED for more tokens and
  * in identity-expert mode; MOE_E_INVALID for x_codes with MOE_PREC_BF16.
  * Inputs must be finite: a NaN reaches its own token's output only.
  */
 #define MOE_FEW_MAX_TOKENS 64
+#define MOE_FEW_COUNTER_BYTES 512
 moe_status moe_layer_fwd_few(const moe_cfg *cfg, const moe_weights *w, const uint16_t *x,
                              const uint8_t *x_codes, const uint8_t *x_scales, uint16_t *out, void *ws,
                              size_t ws_bytes, void *stream);

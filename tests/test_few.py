@@ -93,7 +93,7 @@ class Few:
         self.packed = torch.empty(moe.moe_query_sizes(self.cfg).packed_weights, dtype=torch.uint8, device="cuda")
         moe.moe_prepare_weights(self.cfg, d(i.Wg), d(i.Wu), d(i.Wd), self.packed, d(i.Wsg), d(i.Wsu), d(i.Wsd))
         self.ws = torch.randint(0, 256, (moe.moe_query_few(self.cfg),), dtype=torch.uint8, device="cuda")
-        self.ws[:256] = 0
+        self.ws[:moe.MOE_FEW_COUNTER_BYTES] = 0
         torch.cuda.synchronize()
 
     def __call__(self, x=None, **kw):
@@ -101,7 +101,7 @@ class Few:
         out = torch.full((x.shape[0] + 1, x.shape[1]), 7.0, dtype=torch.bfloat16, device="cuda")
         moe.moe_layer_fwd_few(self.cfg, self.Wr, self.bias, self.packed, x, out, self.ws, **kw)
         torch.cuda.synchronize()
-        assert not self.ws[:256].any(), "the counters are not back at zero"
+        assert not self.ws[:moe.MOE_FEW_COUNTER_BYTES].any(), "the counters are not back at zero"
         assert (out[-1] == 7).all(), "a row past the last token was written"
         return out[:-1]
 
