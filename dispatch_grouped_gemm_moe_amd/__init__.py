@@ -212,57 +212,43 @@ def moe_mx_quantize(src, codes, scales, stream=None):
                                                       _stream(stream)))
 
 
-def _dense(fn, like, **tensors):
-    """The pointers of dense tensors on one device, by (tensor, dtype, elements); None stays None.
-
-    The kernels see pointers only, so a tensor of another type, with strides,
-    too small or on another device is refused here."""
-    device = like.device
-    out = []
-    for t, dtype, n in tensors.values():
-        if t is None:
-            out.append(None)
-            continue
-        if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.device != device:
-            raise MoeError(fn, MOE_E_INVALID)
-        out.append(t.data_ptr())
-    return out
+def _dense(fn, device, t, dtype, n):
+    """The pointer of a dense tensor of `dtype` with at least n elements on `device` (its index, -1 for
+    the host); None stays None.  The kernels see pointers only, so what they could not read is refused
+    here."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+        raise MoeError(fn, MOE_E_INVALID)
+    return t.data_ptr()
 
 
-class _On:
-    """The device of `t` as the current one (a launch goes to the current
-    device's queues), and the stream as an integer: the given one, or that
-    device's current stream."""
-
-    def __init__(self, t, stream):
-        import torch
-        self.guard = None
-        if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(t.device)
-        self.stream = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, device, stream, *args):
+    """Library function fn(*args, stream) on `device`: the given stream, or that device's current one.  A
+    launch goes to the current device's queues, so that one is made current for the call."""
+    import torch
+    if device < 0 or device == torch.cuda.current_device():
+        if stream is None:
+            s = torch._C._cuda_getCurrentRawStream(max(device, 0))
+        else:
+            s = stream if isinstance(stream, int) else stream.cuda_stream
+        st = getattr(_load(), fn)(*args, s)
+        if st != MOE_OK:
+            raise MoeError(fn, st)
+    else:
+        with torch.cuda.device(device):
+            _call(fn, device, stream, *args)
 
 
 def moe_mx_dequantize(codes, scales, dst, operand_scales=False, stream=None):
     """dst (bf16) = the values of codes [rows, cols] and their scales: [rows, cols/32], or with
     operand_scales the GEMM operand layout [ceil(cols/128), rows, 4]."""
     import torch
+    fn, dev, u8 = "moe_mx_dequantize", codes.get_device(), torch.uint8
     rows, cols = codes.shape
-    u8 = torch.uint8
     n_scales = (cols + 127) // 128 * rows * 4 if operand_scales else rows * (cols // 32)
-    p = _dense("moe_mx_dequantize", codes, codes=(codes, u8, 0), scales=(scales, u8, n_scales),
-               dst=(dst, torch.bfloat16, rows * cols))
-    with _On(codes, stream) as s:
-        _check("moe_mx_dequantize", _load().moe_mx_dequantize(p[0], p[1], rows, cols, 1 if operand_scales else 0, p[2],
-                                                              s))
+    _call(fn, dev, stream, _dense(fn, dev, codes, u8, 0), _dense(fn, dev, scales, u8, n_scales), rows, cols,
+          1 if operand_scales else 0, _dense(fn, dev, dst, torch.bfloat16, rows * cols))
 
 
 def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd=None, y_codes=None, y_scales=None,
@@ -270,15 +256,14 @@ def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd
     """y = rmsnorm(x + residual) * weight over the rows of x [rows, cols]; see include/moe.h for the
     optional outputs (the sum, 1/rms, the MXFP8 form of y, the 8-bit checkpoint of the sum)."""
     import torch
-    fn = "moe_add_rmsnorm_fwd"
+    fn, dev, b16, f32, u8 = "moe_add_rmsnorm_fwd", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     rows, cols = x.shape
-    n, b16, f32, u8 = rows * cols, torch.bfloat16, torch.float32, torch.uint8
-    p = _dense(fn, x, x=(x, b16, n), residual=(residual, b16, n), weight=(weight, f32, cols),
-               summed=(summed, b16, n), y=(y, b16, n), rstd=(rstd, f32, rows), yc=(y_codes, u8, n),
-               ys=(y_scales, u8, (cols + 127) // 128 * rows * 4), cc=(ck_codes, u8, n),
-               cs=(ck_scales, u8, rows * (cols // 32)))
-    with _On(x, stream) as s:
-        _check(fn, _load().moe_add_rmsnorm_fwd(rows, cols, p[0], p[1], p[2], eps, *p[3:], s))
+    n = rows * cols
+    _call(fn, dev, stream, rows, cols, _dense(fn, dev, x, b16, n), _dense(fn, dev, residual, b16, n),
+          _dense(fn, dev, weight, f32, cols), eps, _dense(fn, dev, summed, b16, n), _dense(fn, dev, y, b16, n),
+          _dense(fn, dev, rstd, f32, rows), _dense(fn, dev, y_codes, u8, n),
+          _dense(fn, dev, y_scales, u8, (cols + 127) // 128 * rows * 4), _dense(fn, dev, ck_codes, u8, n),
+          _dense(fn, dev, ck_scales, u8, rows * (cols // 32)))
 
 
 def moe_query_add_rmsnorm_bwd(rows, cols) -> int:
@@ -291,14 +276,14 @@ def moe_add_rmsnorm_bwd(dy, weight, rstd, dx, dweight, ws, summed=None, ck_codes
                         stream=None):
     """dx and dweight of moe_add_rmsnorm_fwd, from the sum or from its 8-bit checkpoint."""
     import torch
-    fn = "moe_add_rmsnorm_bwd"
+    fn, dev, b16, f32, u8 = "moe_add_rmsnorm_bwd", dy.get_device(), torch.bfloat16, torch.float32, torch.uint8
     rows, cols = dy.shape
-    n, b16, f32, u8 = rows * cols, torch.bfloat16, torch.float32, torch.uint8
-    p = _dense(fn, dy, dy=(dy, b16, n), dsum=(dsum, b16, n), summed=(summed, b16, n),
-               cc=(ck_codes, u8, n), cs=(ck_scales, u8, rows * (cols // 32)), weight=(weight, f32, cols),
-               rstd=(rstd, f32, rows), dx=(dx, b16, n), dw=(dweight, f32, cols), ws=(ws, u8, 0))
-    with _On(dy, stream) as s:
-        _check(fn, _load().moe_add_rmsnorm_bwd(rows, cols, *p, ws.numel(), s))
+    n = rows * cols
+    _call(fn, dev, stream, rows, cols, _dense(fn, dev, dy, b16, n), _dense(fn, dev, dsum, b16, n),
+          _dense(fn, dev, summed, b16, n), _dense(fn, dev, ck_codes, u8, n),
+          _dense(fn, dev, ck_scales, u8, rows * (cols // 32)), _dense(fn, dev, weight, f32, cols),
+          _dense(fn, dev, rstd, f32, rows), _dense(fn, dev, dx, b16, n), _dense(fn, dev, dweight, f32, cols),
+          _dense(fn, dev, ws, u8, 0), ws.numel())
 
 
 def moe_query_few(cfg: moe_cfg) -> int:
@@ -311,16 +296,13 @@ def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=
     """Layer forward for cfg.T <= MOE_FEW_MAX_TOKENS tokens; ws: moe_query_few bytes, the first
     MOE_FEW_COUNTER_BYTES of them zeroed once."""
     import torch
-    fn = "moe_layer_fwd_few"
+    fn, dev, b16, f32, u8 = "moe_layer_fwd_few", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     T, H, E = cfg.T, cfg.H, cfg.E
-    b16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
-    p = _dense(fn, x, Wr=(Wr, f32, H * E), bias=(bias, f32, E), packed=(packed, u8, 0), x=(x, b16, T * H),
-               xc=(x_codes, u8, T * H), xs=(x_scales, u8, (H + 127) // 128 * T * 4), out=(out, b16, T * H),
-               ws=(ws, u8, 0))
-    w = moe_weights(p[0], p[1], p[2], packed.numel())
-    with _On(x, stream) as s:
-        _check(fn, _load().moe_layer_fwd_few(ctypes.byref(cfg), ctypes.byref(w), p[3], p[4], p[5], p[6], p[7],
-                                             ws.numel(), s))
+    w = moe_weights(_dense(fn, dev, Wr, f32, H * E), _dense(fn, dev, bias, f32, E), _dense(fn, dev, packed, u8, 0),
+                    packed.numel())
+    _call(fn, dev, stream, ctypes.byref(cfg), ctypes.byref(w), _dense(fn, dev, x, b16, T * H),
+          _dense(fn, dev, x_codes, u8, T * H), _dense(fn, dev, x_scales, u8, (H + 127) // 128 * T * 4),
+          _dense(fn, dev, out, b16, T * H), _dense(fn, dev, ws, u8, 0), ws.numel())
 
 
 def moe_diag_mfma_loop(kind, operands, blocks, iters, clocks, sink, stream=None):
