@@ -11,8 +11,9 @@
 // of 16-wide MFMAs and the expert's tokens the N side, so 16 tokens ride on
 // every weight fragment and nothing is padded past 16 rows.
 //
-// Four launches: the router (logits, top-k, expert row lists), the gate|up
-// product with SwiGLU, the down product, and the weighted sum.  Two other forms
+// Three launches: the router (logits, top-k, expert row lists), the gate|up
+// product with SwiGLU, and the down product with the weighted sum (two launches
+// past 16 tokens).  Two other forms
 // of the products were built and measured on one MXFP8 token (H 7168, I 2048, 8
 // of 32 experts; 85 us a call as it is): all three in one launch with tiles
 // handed out by a ticket, down tiles waiting on counters, took 159 us (atomics
@@ -362,6 +363,14 @@ constexpr int kFgRows = 64;                 // weight rows per workgroup
 constexpr int kFgChunk = 128;               // bytes of a weight row per step: one cache line
 constexpr int kFgLd = kFgRows + 4;          // floats of a token's partial sums in LDS
 
+// What a launch's experts are: bf16, MXFP8, or MXFP8 with the bf16 shared expert.
+enum FewKind { kFewBf16 = 0, kFewMx = 1, kFewMxShared = 2 };
+
+__device__ __forceinline__ bf16x8 few_half(intx8 v, int j) {
+    return __builtin_bit_cast(bf16x8, j == 0 ? __builtin_shufflevector(v, v, 0, 1, 2, 3)
+                                             : __builtin_shufflevector(v, v, 4, 5, 6, 7));
+}
+
 __device__ __forceinline__ intx8 cat8(intx4 a, intx4 b) {
     return intx8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
@@ -630,8 +639,10 @@ __global__ __launch_bounds__(kFgThreads) void few_gemm_kernel(FewGemm a) {
     __shared__ __attribute__((aligned(16))) float s_part[kFgWaves * 16 * kFgLd];
     const int nt = kDown ? a.H / kFgRows : a.I / 32;
     const int i = blockIdx.x / nt, n = blockIdx.x - i * nt;
-    if (i >= ld_layout(a.n_act)) return;
-    const int e = ld_layout(a.act_e + i), row0 = ld_layout(a.act_off + i), rows = ld_layout(a.act_off + i + 1) - row0;
+    // all four at once: the lists hold an entry for every expert of the grid
+    const int n_act = ld_layout(a.n_act), e = ld_layout(a.act_e + i), row0 = ld_layout(a.act_off + i);
+    const int rows = ld_layout(a.act_off + i + 1) - row0;
+    if (i >= n_act) return;
     if (kMx && e < a.E) few_tile_rows<kDown, true, kMost>(a, e, n, row0, rows, s_part);
     else few_tile_rows<kDown, false, kMost>(a, e, n, row0, rows, s_part);
 }
@@ -655,6 +666,242 @@ static void launch_few_gemm(const FewGemm& a, int max_act, hipStream_t stream) {
 
 void launch_few_gate_up(const FewGemm& a, int max_act, hipStream_t s) { launch_few_gemm<false>(a, max_act, s); }
 void launch_few_down(const FewGemm& a, int max_act, hipStream_t s) { launch_few_gemm<true>(a, max_act, s); }
+
+// ---------------------------------------------------------------------------
+// Down product and weighted sum of up to 16 tokens
+// ---------------------------------------------------------------------------
+
+constexpr int kFdWaves = 8;
+constexpr int kFdThreads = kFdWaves * kWave;
+constexpr int kFdTok = 16;    // tokens
+constexpr int kFdCols = 16;   // output columns per workgroup: weight rows of a step
+constexpr int kFdBatch = 4;   // cache lines of a row per step
+constexpr int kFdSlot = kFdBatch * kFdCols * kFgChunk;  // 8 KB of weights per step
+constexpr int kFdRows = kFdTok * (kMaxTopK + 1);
+
+// A value every lane holds alike, as the scalar that it is: a descriptor that
+// the compiler keeps in vector registers makes a loop of every load.
+__device__ __forceinline__ uint32_t scalar(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ __forceinline__ const void* scalar(const void* p) {
+    const uint64_t v = (uint64_t)p;
+    return (const void*)((uint64_t)scalar((uint32_t)v) | (uint64_t)scalar((uint32_t)(v >> 32)) << 32);
+}
+
+// A part of an expert's product with 16 output columns, taken by one wave.
+struct FewUnit {
+    const void *w, *x;        // weight rows, the expert's token rows
+    const void *ws, *xs;      // MXFP8: their scales
+    uint32_t ws_bytes, xs_bytes;
+    int row0, rows;           // token rows
+    int kb, end;              // bytes of a row, last line of the part + 1
+    int mx;
+};
+
+// Output columns 16 n .. 16 n + 15 of every token, over all active experts: the
+// workgroup's waves deal the (expert, part of the row) units among them, each
+// runs through its units without a pause (a unit's first weights are asked for
+// while the one before is multiplied) and adds the weighted results up per
+// token in LDS; one barrier, and the waves' sums are added in order.  Nothing
+// goes through memory, and there is no launch for the weighted sum.
+//
+// There are H / 16 workgroups, fewer than CUs in a small layer, so what one CU
+// can draw from memory counts.  Loads of 16 rows x 64 bytes in the MFMA's lane
+// order reach 36 GB/s a CU, 8 rows x one line straight into LDS 50 GB/s; the
+// fragments are then read from LDS, the 16-byte pieces of a row swizzled by
+// its index so that 16 rows fall on distinct banks.
+template <int kKind>
+__global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int max_act, int max_rows, uint16_t* out) {
+    constexpr bool kMx = kKind != kFewBf16;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_w[kFdWaves][2][kFdSlot];
+    __shared__ __attribute__((aligned(16))) float s_sum[kFdWaves][kFdTok][kFdCols];
+    __shared__ int s_token[kFdRows], s_e[kMaxExperts + 1], s_off[kMaxExperts + 2];
+    __shared__ float s_weight[kFdRows];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = blockIdx.x, H = a.H, I = a.I;
+    // the tables, up to what T and k allow: all asked for at once
+    const int n_act = ld_layout(a.n_act);
+    for (int i = tid; i < max_rows; i += kFdThreads) {
+        s_token[i] = a.row_token[i];
+        s_weight[i] = a.row_w[i];
+    }
+    for (int i = tid; i <= max_act; i += kFdThreads) s_off[i] = a.act_off[i];
+    for (int i = tid; i < max_act; i += kFdThreads) s_e[i] = a.act_e[i];
+    for (int i = tid; i < kFdWaves * kFdTok * kFdCols; i += kFdThreads) (&s_sum[0][0][0])[i] = 0.0f;
+    // parts per expert (2^log_parts): as few as spread the units evenly enough (to a tenth)
+    const int lines = (I * (kMx ? 1 : 2) + kFgChunk - 1) / kFgChunk, batches = (lines + kFdBatch - 1) / kFdBatch;
+    int log_parts = 0;
+    while ((2 << log_parts) <= batches &&
+           10 * ceil_div(n_act << log_parts, kFdWaves) * kFdWaves > 11 * (n_act << log_parts))
+        ++log_parts;
+    const int units = n_act << log_parts;
+    __syncthreads();
+
+    // unit u and its first line; past the last one, the first again with no lines
+    auto unit_of = [&](int u, int& c0) {
+        FewUnit t;
+        const int live = (u - units) >> 31;
+        u &= live;
+        const int i = u >> log_parts, part = u - (i << log_parts);
+        const int e = (int)scalar((uint32_t)s_e[i]);
+        t.row0 = (int)scalar((uint32_t)s_off[i]);
+        t.rows = (int)scalar((uint32_t)s_off[i + 1]) - t.row0;
+        t.mx = kKind == kFewMx || (kKind == kFewMxShared && e < a.E) ? 1 : 0;
+        t.kb = t.mx ? I : 2 * I;
+        const int ln = (t.kb + kFgChunk - 1) / kFgChunk, bt = (ln + kFdBatch - 1) / kFdBatch;
+        c0 = (bt * part >> log_parts) * kFdBatch;
+        t.end = min((bt * (part + 1) >> log_parts) * kFdBatch, ln);
+        if (!live) t.end = c0;
+        const int64_t wrow = (int64_t)e * H + (int64_t)n * kFdCols;
+        const uint32_t groups = (uint32_t)mx_groups(I);
+        t.w = scalar((t.mx ? a.w2q : (const uint8_t*)a.w2) + wrow * t.kb);
+        t.x = scalar((t.mx ? a.hq : (const uint8_t*)a.h) + (int64_t)t.row0 * t.kb);
+        if (kMx) {
+            t.ws = scalar(a.s2 + ((int64_t)e * groups * H + (int64_t)n * kFdCols) * 4);
+            t.ws_bytes = scalar(t.mx ? (groups - 1) * (uint32_t)H * 4 + kFdCols * 4 : 0);
+            t.xs = scalar(a.hs + (int64_t)t.row0 * groups * 4);
+            t.xs_bytes = scalar(t.mx ? (uint32_t)t.rows * groups * 4 : 0);
+        }
+        t.kb = (int)scalar((uint32_t)t.kb);
+        t.end = (int)scalar((uint32_t)t.end);
+        c0 = (int)scalar((uint32_t)c0);
+        return t;
+    };
+
+    const uint32_t lo = (uint32_t)(lane >> 4) * 16, lr = (uint32_t)lane & 15;
+    const int shift = 8 * (lane >> 4);
+    struct Scales { uint32_t s[kMx ? kFdBatch : 1]; };
+    // Ask for the weights of step (t, c) into the slot, load q taking rows 8 (q %
+    // 2) .. + 7 of line c + q / 2.  Past the part's end its last line is repeated
+    // (against zero token rows); past the end of an MXFP8 row, in the middle of a
+    // line, its first half (against zero scale bytes).  And for the scale dwords.
+    auto issue = [&](const FewUnit& t, int c, int slot, Scales& f) {
+        uint8_t* dst = s_w[wave][slot];
+        const int last = max(t.end - 1, 0);
+#pragma unroll
+        for (int q = 0; q < 2 * kFdBatch; ++q) {
+            const int line = min(c + q / 2, last);
+            const uint32_t row = (uint32_t)(q & 1) * 8 + (uint32_t)(lane >> 3);
+            const uint32_t half = kMx && line * kFgChunk + kFgChunk / 2 >= t.kb ? 3 : 7;
+            const uint32_t piece = (((uint32_t)lane & 7) ^ (row & 7)) & half;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(few_rsrc(t.w, (uint32_t)(kFdCols * t.kb)), (lds_void*)(dst + q * 1024),
+                                                     16, row * (uint32_t)t.kb + piece * 16, line * kFgChunk, 0, 0);
+        }
+        if constexpr (kMx) {
+#pragma unroll
+            for (int j = 0; j < kFdBatch; ++j)
+                f.s[j] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(t.ws, t.ws_bytes), lr * 4,
+                                                              min(c + j, last) * H * 4, 0);
+        }
+    };
+    // The weight fragments of a slot: of line j this lane's pieces lane / 16 and
+    // 4 + lane / 16 of row lane % 16.  In one block with its wait: the compiler
+    // would wait for the loads into the other slot too.
+    static_assert(kFdBatch == 4 && kFdCols * kFgChunk == 2048, "the offsets below");
+    auto frags = [&](int slot, intx8 (&w)[kFdBatch]) {
+        const uint32_t g = (uint32_t)lane >> 4, sw = lr & 7;
+        const uint32_t row = (uint32_t)(uintptr_t)(lds_void*)s_w[wave][slot] + lr * kFgChunk;
+        const uint32_t p0 = row + (g ^ sw) * 16, p1 = row + ((4 + g) ^ sw) * 16;
+        intx4 f[2 * kFdBatch];
+        asm volatile(
+            "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\t"
+            "ds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
+            "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %9 offset:4096\n\t"
+            "ds_read_b128 %6, %8 offset:6144\n\tds_read_b128 %7, %9 offset:6144\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(f[4]), "=&v"(f[5]), "=&v"(f[6]), "=&v"(f[7])
+            : "v"(p0), "v"(p1)
+            : "memory");
+#pragma unroll
+        for (int j = 0; j < kFdBatch; ++j) w[j] = __builtin_shufflevector(f[2 * j], f[2 * j + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    floatx4 acc = {0, 0, 0, 0};
+    int u = wave, c;
+    FewUnit t = unit_of(u, c);
+    Scales f0, f1;
+    issue(t, c, 0, f0);
+    auto step = [&](int slot, const Scales& f, Scales& next) {
+        const FewUnit cur = t;
+        const int c0 = c;
+        intx8 x[kFdBatch];
+        uint32_t xs[kMx ? kFdBatch : 1];
+        const uint32_t r = (uint32_t)min((int)lr, cur.rows - 1);  // past the last row: the last one again
+#pragma unroll
+        for (int j = 0; j < kFdBatch; ++j) {
+            const int in = (c0 + j - cur.end) >> 31, at = ((c0 + j) * kFgChunk) & in;
+            const int hi = at + (kFgChunk / 2 & (kMx ? (at + kFgChunk / 2 - cur.kb) >> 31 : -1) & in);
+            const __amdgpu_buffer_rsrc_t d = few_rsrc(cur.x, (uint32_t)(cur.rows * cur.kb & in));
+            const intx4 p0 = __builtin_amdgcn_raw_buffer_load_b128(d, r * (uint32_t)cur.kb + lo, at, 0);
+            const intx4 p1 = __builtin_amdgcn_raw_buffer_load_b128(d, r * (uint32_t)cur.kb + lo, hi, 0);
+            x[j] = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
+            if constexpr (kMx)
+                xs[j] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(cur.xs, cur.xs_bytes),
+                                                             r * (uint32_t)mx_groups(I) * 4, ((c0 + j) * 4) & in, 0);
+        }
+        c += kFdBatch;
+        const bool flush = c >= cur.end;
+        if (flush) {
+            u += kFdWaves;
+            t = unit_of(u, c);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        issue(t, c, slot ^ 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+        // everything before the next step's weights has arrived
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kFdBatch + (kMx ? kFdBatch : 0)) : "memory");
+        intx8 w[kFdBatch];
+        frags(slot, w);
+#pragma unroll
+        for (int j = 0; j < kFdBatch; ++j) {
+            if (kKind == kFewMx || (kKind == kFewMxShared && cur.mx)) {
+                if constexpr (kMx)
+                    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x[j], acc, 0, 0, 0, (int)(f.s[j] >> shift),
+                                                                           0, (int)(xs[j] >> shift));
+            } else {
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_half(w[j], 0), few_half(x[j], 0), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_half(w[j], 1), few_half(x[j], 1), acc, 0, 0, 0);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (flush) {  // lane: columns 4 (l / 16) .. + 3 of token row l % 16
+            if ((int)lr < cur.rows) {
+                floatx4* d = (floatx4*)&s_sum[wave][s_token[cur.row0 + lr]][4 * (lane >> 4)];
+                const float wt = s_weight[cur.row0 + lr];
+                floatx4 v = *d;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(wt, acc[q], v[q]);
+                *d = v;
+            }
+            acc = floatx4{0, 0, 0, 0};
+        }
+    };
+    while (u < units) {  // the second step may be past the last unit
+        step(0, f0, f1);
+        step(1, f1, f0);
+    }
+    __syncthreads();
+    for (int i = tid; i < a.T * kFdCols / 2; i += kFdThreads) {
+        const int tok = i / (kFdCols / 2), col = i % (kFdCols / 2) * 2;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFdWaves; ++w) {
+            s0 += s_sum[w][tok][col];
+            s1 += s_sum[w][tok][col + 1];
+        }
+        *(uint32_t*)(out + (size_t)tok * H + n * kFdCols + col) =
+            (uint32_t)f32_to_bf16_rne(s0) | ((uint32_t)f32_to_bf16_rne(s1) << 16);
+    }
+}
+
+void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, uint16_t* out, hipStream_t stream) {
+    const dim3 grid(a.H / kFdCols), block(kFdThreads);
+    if (!a.xq)
+        hipLaunchKernelGGL(few_down16_kernel<kFewBf16>, grid, block, 0, stream, a, max_act, max_rows, out);
+    else if (!shared)
+        hipLaunchKernelGGL(few_down16_kernel<kFewMx>, grid, block, 0, stream, a, max_act, max_rows, out);
+    else
+        hipLaunchKernelGGL(few_down16_kernel<kFewMxShared>, grid, block, 0, stream, a, max_act, max_rows, out);
+}
 
 // out[t] = the weighted rows of the slots in order, then the shared expert's.
 __global__ __launch_bounds__(256) void few_combine_kernel(FewGemm a, int k, int shared, uint16_t* out) {

@@ -380,6 +380,8 @@ struct FewGemm {
 };
 void launch_few_gate_up(const FewGemm& a, int max_act, hipStream_t stream);
 void launch_few_down(const FewGemm& a, int max_act, hipStream_t stream);
+// up to 16 tokens: the down product with the weighted sum
+void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, uint16_t* out, hipStream_t stream);
 void launch_few_combine(const FewGemm& a, int k, int shared, uint16_t* out, hipStream_t stream);
 
 // ---- residual addition and root-mean-square norm (norm.hip) ----
