@@ -71,6 +71,15 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t h) {
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Barrier over LDS only: this wave's LDS accesses have completed, then
+// s_barrier.  __syncthreads' workgroup fence would also wait for every global
+// memory operation in flight, direct-to-LDS loads and stores included.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void gbl_cvoid;
 typedef int intx8 __attribute__((ext_vector_type(8)));

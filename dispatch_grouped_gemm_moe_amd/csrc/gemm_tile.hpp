@@ -145,15 +145,6 @@ static_assert(kEpiRows * kEpiPitch64 <= kTileSmem, "staged fp32 block must fit")
 // the 16 rows one 128-bit fragment read touches per pass fall on distinct banks.
 __device__ __forceinline__ int swz8(int r) { return (r >> 1) & 7; }
 
-// Barrier over LDS only: this wave's LDS accesses have completed, then
-// s_barrier.  __syncthreads' workgroup fence would also wait for every global
-// memory operation in flight, direct-to-LDS loads and stores included.
-__device__ __forceinline__ void lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // ---------------------------------------------------------------------------
 // Chained tiles.  A tile's first stage otherwise waits for its loads to come
 // from memory after the previous tile's epilogue (about 5 us of a 60 us tile
