@@ -419,25 +419,69 @@ __device__ __forceinline__ void few_load(const FewOperand& o, int kb, int c, con
     }
 }
 
-template <bool MX, int MT>
-__device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<MX, MT>& x, int shift,
-                                         floatx4 (&acc)[4][MT]) {
+// The 32 MXFP8 values of a lane as bf16, scaled (exact: four significand bits
+// and a power of two), eight to an operand of a 16x16x32 MFMA.  Bytes 0 .. 15
+// lie in block (l / 32) of the line, bytes 16 .. 31 in block 2 + l / 32.
+__device__ __forceinline__ void few_widen(const intx4 (&v)[2], uint32_t scales, int lane, bf16x8 (&o)[4]) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t s = scales >> (8 * (lane >> 5));
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < 2; ++j) {
+        const float f = __builtin_bit_cast(float, (s >> (16 * j) & 0xff) << 23);  // its exponent is the scale
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            bf16x2 t[4];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                t[2 * d] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)v[j][2 * q + d], f, false);
+                t[2 * d + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)v[j][2 * q + d], f, true);
+            }
+            o[2 * j + q] = bf16x8{t[0][0], t[0][1], t[1][0], t[1][1], t[2][0], t[2][1], t[3][0], t[3][1]};
+        }
+    }
+}
+
+// kWiden: MXFP8 values go through bf16 MFMAs.  A scaled MFMA joins 128 products
+// in one step with about 16 bits below the largest (measured: sums of 1664
+// products off by 1.7e-5 of their norm), which is too coarse for what is
+// quantised again: 16 of 11648 values of h took another code, this way none,
+// in the same time.
+template <bool MX, int MT, bool kWiden>
+__device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<MX, MT>& x, int lane,
+                                         floatx4 (&acc)[4][MT]) {
+    if constexpr (MX && kWiden) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (MX) {
-                acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    cat8(w.v[i][0], w.v[i][1]), cat8(x.v[m][0], x.v[m][1]), acc[i][m], 0, 0, 0, (int)(w.s[i] >> shift),
-                    0, (int)(x.s[m] >> shift));
-            } else {
+            bf16x8 wb[4];
+            few_widen(w.v[i], w.s[i], lane, wb);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[i][j]),
-                                                                        __builtin_bit_cast(bf16x8, x.v[m][j]),
-                                                                        acc[i][m], 0, 0, 0);
+            for (int m = 0; m < MT; ++m) {
+                bf16x8 xb[4];
+                few_widen(x.v[m], x.s[m], lane, xb);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xb[j], acc[i][m], 0, 0, 0);
             }
         }
+    } else {
+        const int shift = 8 * (lane >> 4);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (MX) {
+                    acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        cat8(w.v[i][0], w.v[i][1]), cat8(x.v[m][0], x.v[m][1]), acc[i][m], 0, 0, 0,
+                        (int)(w.s[i] >> shift), 0, (int)(x.s[m] >> shift));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[i][j]),
+                                                                            __builtin_bit_cast(bf16x8, x.v[m][j]),
+                                                                            acc[i][m], 0, 0, 0);
+                }
+            }
+    }
 }
 
 // acc[i][m] (+)= weight rows 16 i .. of the tile times token rows 16 m .., over
@@ -446,7 +490,7 @@ __device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<
 // from the L2, are loaded in their own step, ahead of the next weights, so that
 // waiting for them (loads return in order) leaves those in flight.  Steps past
 // the end load zeros, so the loop has one exit and keeps its registers.
-template <bool MX, int MT>
+template <bool MX, int MT, bool kWiden>
 __device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperand& xo, int kb, int wave, int lane,
                                            const uint32_t (&xrow)[MT], const uint32_t (&xsoff)[MT],
                                            floatx4 (&acc)[4][MT]) {
@@ -459,14 +503,13 @@ __device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperan
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) xoff[m] = xrow[m] + lo;
-    const int shift = 8 * (lane >> 4);
     FewFrag<MX, 4> w0, w1;
     FewFrag<MX, MT> x;
     auto step = [&](int c, const FewFrag<MX, 4>& w, FewFrag<MX, 4>& next) {
         few_load<MX, MT>(xo, kb, c, xoff, xsoff, x);
         few_load<MX, 4>(wo, kb, c + kFgWaves, woff, wsoff, next);
         __builtin_amdgcn_sched_barrier(0);
-        few_mfma<MX, MT>(w, x, shift, acc);
+        few_mfma<MX, MT, kWiden>(w, x, lane, acc);
         __builtin_amdgcn_sched_barrier(0);
     };
     few_load<MX, 4>(wo, kb, wave, woff, wsoff, w0);
@@ -519,7 +562,7 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT, true>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
     // thread (token tid / 32, column tid % 32): the tile's rows are 32 gate
     // columns and the 32 up columns of the same indices
     const int tt = tid >> 5, col = tid & 31;
@@ -553,6 +596,9 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
                 }
             }
         } else if (r < rows) {
+            // bf16, as the layer forward keeps h: an operand of the next MFMA.  In
+            // two bf16 parts the layer's error would be 2^-8.5 rather than 2^-8 of
+            // its output, for 2 us of 29 (one token, H 2048) and 25 of 536 (64, H 7168).
             a.h[(size_t)(row0 + r) * I + n * 32 + col] = f32_to_bf16_rne(h);
         }
     }
@@ -592,7 +638,7 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT, false>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
     const int tt = tid >> 5, col = (tid & 31) * 2;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
