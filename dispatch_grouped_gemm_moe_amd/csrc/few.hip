@@ -32,9 +32,6 @@ namespace moe {
 // Router
 // ---------------------------------------------------------------------------
 
-constexpr int kFrThreads = 512;
-constexpr int kFrWaves = kFrThreads / kWave;
-constexpr int kFrTok = kFrWaves;  // tokens per workgroup, one per wave
 constexpr int kFrEC = 32;         // experts per workgroup: a cache line of a router weight row
 constexpr int kFrRes = 16;        // residue groups: group l takes h mod 64 in {l, l + 16, l + 32, l + 48}
 constexpr int kFrSlab = 128;      // 64-wide chunks of h per LDS slab
@@ -135,17 +132,14 @@ struct FewLists {
 
 // The experts' row lists.  At most 64 tokens: an expert's tokens are one 64-bit
 // mask, and a row's rank within its expert a population count.
+template <int kThreads>
 __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = a.T * a.k;
-    static_assert(kFewTokens * kMaxTopK == 2 * kFrThreads && kMaxExperts <= kFrThreads, "selections and experts per thread");
+    static_assert(kMaxExperts <= kThreads && kThreads % kWave == 0, "an expert per thread");
     if (tid < kMaxExperts) s.mask[tid] = 0;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int i = tid + j * kFrThreads;
-        if (i < n) atomicOr((unsigned long long*)&s.mask[s.sel_e[i]], 1ull << (i / a.k));
-    }
+    for (int i = tid; i < n; i += kThreads) atomicOr((unsigned long long*)&s.mask[s.sel_e[i]], 1ull << (i / a.k));
     __syncthreads();
     // exclusive prefixes over the experts, of rows and of experts that have any
     int c = 0, inc = 0;
@@ -190,16 +184,12 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
         *a.n_act = act;
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int i = tid + j * kFrThreads;
-        if (i < n) {
-            const int t = i / a.k, e = s.sel_e[i];
-            const int row = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1ull));
-            a.row_token[row] = t;
-            a.row_w[row] = s.sel_w[i];
-            a.slot_row[i] = row;
-        }
+    for (int i = tid; i < n; i += kThreads) {
+        const int t = i / a.k, e = s.sel_e[i];
+        const int row = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1ull));
+        a.row_token[row] = t;
+        a.row_w[row] = s.sel_w[i];
+        a.slot_row[i] = row;
     }
     if (a.shared && tid < a.T) {
         a.row_token[n + tid] = tid;
@@ -208,7 +198,7 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
 }
 
 // Workgroup (l, x, y): residues l, l + 16, l + 32, l + 48 of h mod 64, experts
-// 32 x .. 32 x + 31, tokens 8 y .. 8 y + 7, a wave per token.
+// 32 x .. 32 x + 31, tokens kTok y .. + kTok - 1, a wave per token.
 //
 // The logits' order is moe_route's: p[r] sums h = r, r + 64, ... with fused
 // multiply-adds, a halving tree joins the 64 p[r], the bias comes last.  The
@@ -224,19 +214,21 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
 // l + 16 half + 32: the first two tree levels stay in the wave.  The workgroup
 // of an (x, y) that counts in last joins the 16 groups' sums to logits, the
 // last of a y picks its tokens' experts, the last y builds the row lists.
-template <bool kVec4>
-__global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
+template <bool kVec4, int kTok>
+__global__ __launch_bounds__(kTok * kWave) void few_route_kernel(FewRoute a) {
+    constexpr int kThreads = kTok * kWave;
     __shared__ __attribute__((aligned(1024))) float s_wr[kFrSlab * 4][kFrEC];
-    __shared__ __attribute__((aligned(16))) float s_x[kFrTok][2][kFrSlab][2];
-    __shared__ float s_logit[kFrTok][kMaxExperts];
-    __shared__ FewLists s_lists;
+    __shared__ __attribute__((aligned(16))) float s_x[kTok][2][kFrSlab][2];
+    __shared__ float s_logit[kTok][kMaxExperts];
     __shared__ int s_flag;
+    static_assert(sizeof(FewLists) <= sizeof(s_wr), "the lists take the slab's place");
+    FewLists& s_lists = *(FewLists*)&s_wr[0][0];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l = blockIdx.x, e0 = blockIdx.y * kFrEC, t0 = blockIdx.z * kFrTok;
+    const int l = blockIdx.x, e0 = blockIdx.y * kFrEC, t0 = blockIdx.z * kTok;
     const int ng = gridDim.y, nz = gridDim.z;
     const int T = a.T, H = a.H, E = a.E, k = a.k;
-    const int nt = min(kFrTok, T - t0), ne = min(kFrEC, E - e0);
+    const int nt = min(kTok, T - t0), ne = min(kFrEC, E - e0);
     const int half = lane >> 5, el = lane & 31;
     float p0 = 0.0f, p1 = 0.0f;
     for (int c0 = 0; c0 < H / kWave; c0 += kFrSlab) {
@@ -246,12 +238,12 @@ __global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
         auto h_of = [&](int r) { return (c0 + (r >> 2)) * kWave + l + 16 * (r & 3); };
         if (kVec4 && ne == kFrEC) {
             // eight rows per load; a slab's rows are a multiple of four
-            for (int r = wave * 8; r < nc * 4; r += kFrWaves * 8)
+            for (int r = wave * 8; r < nc * 4; r += kTok * 8)
                 __builtin_amdgcn_global_load_lds(
                     (gbl_cvoid*)(a.Wr + (size_t)h_of(min(r + (lane >> 3), nc * 4 - 1)) * E + e0 + (lane & 7) * 4),
                     (lds_void*)s_wr[r], 16, 0, 0);
         } else {
-            for (int i = tid; i < nc * 4 * kFrEC; i += kFrThreads) {
+            for (int i = tid; i < nc * 4 * kFrEC; i += kThreads) {
                 const int r = i / kFrEC, q = i % kFrEC;
                 s_wr[r][q] = q < ne ? a.Wr[(size_t)h_of(r) * E + e0 + q] : 0.0f;
             }
@@ -268,6 +260,17 @@ __global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s_x[wave][j & 1][i * kWave + lane][j >> 1] = bf16_to_f32(v[i][j]);
         }
+        // MXFP8: the tokens' codes and operand-layout scales, a block of 32 per
+        // thread, while the slab is on its way
+        if (a.xq && c0 == 0) {
+            const int nb = H / 32, n = gridDim.x * ng * nz;
+            for (int i = ((blockIdx.z * ng + blockIdx.y) * gridDim.x + l) * kThreads + tid; i < T * nb;
+                 i += n * kThreads) {
+                const int ti = i / nb, b = i - ti * nb;
+                const uint8_t sc = mx_quant_block32(a.x + (size_t)ti * H + b * 32, a.xq + (size_t)ti * H + b * 32);
+                mx_store_scale_byte(a.xs, T, ti, b, nb, sc);
+            }
+        }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads into LDS too
         __syncthreads();
         if (wave < nt) {
@@ -280,23 +283,13 @@ __global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
         }
     }
     {
-        float v = p0 + p1;             // p[r] + p[r + 32]
+        float v = p0 + p1;                 // p[r] + p[r + 32]
         v = v + __shfl_xor(v, 32, kWave);  // + 16
         if (wave < nt && half == 0 && el < ne)
             agent_store((int*)a.partial + ((size_t)(t0 + wave) * E + e0 + el) * kFrRes + l, __builtin_bit_cast(int, v));
     }
-    // MXFP8: the tokens' codes and operand-layout scales, a block of 32 per thread
-    if (a.xq) {
-        const int nb = H / 32, n = gridDim.x * ng * nz;
-        for (int i = ((blockIdx.z * ng + blockIdx.y) * gridDim.x + l) * kFrThreads + tid; i < T * nb;
-             i += n * kFrThreads) {
-            const int ti = i / nb, b = i - ti * nb;
-            const uint8_t sc = mx_quant_block32(a.x + (size_t)ti * H + b * 32, a.xq + (size_t)ti * H + b * 32);
-            mx_store_scale_byte(a.xs, T, ti, b, nb, sc);
-        }
-    }
-    if (!counts_in_last(a.counter + 16 + blockIdx.z * ng + blockIdx.y, kFrRes, &s_flag)) return;
-    for (int i = tid; i < nt * ne; i += kFrThreads) {
+    if (!counts_in_last(a.counter + 1 + kFewTokens / 4 + blockIdx.z * ng + blockIdx.y, kFrRes, &s_flag)) return;
+    for (int i = tid; i < nt * ne; i += kThreads) {
         const int ti = i / ne, ei = i - ti * ne;
         const uint64_t* q = (const uint64_t*)(a.partial + ((size_t)(t0 + ti) * E + e0 + ei) * kFrRes);
         float v[kFrRes];
@@ -316,8 +309,8 @@ __global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
         if (ng > 1) agent_store((int*)a.logits + (size_t)(t0 + ti) * E + e0 + ei, __builtin_bit_cast(int, z));
     }
     if (ng > 1) {
-        if (!counts_in_last(a.counter + 8 + blockIdx.z, ng, &s_flag)) return;
-        for (int i = tid; i < nt * E; i += kFrThreads)
+        if (!counts_in_last(a.counter + 1 + blockIdx.z, ng, &s_flag)) return;
+        for (int i = tid; i < nt * E; i += kThreads)
             s_logit[i / E][i % E] = __builtin_bit_cast(float, agent_load((const int*)a.logits + (size_t)t0 * E + i));
     }
     __syncthreads();
@@ -337,20 +330,29 @@ __global__ __launch_bounds__(kFrThreads) void few_route_kernel(FewRoute a) {
     }
     if (nz > 1) {
         if (!counts_in_last(a.counter, nz, &s_flag)) return;
-        for (int i = tid; i < T * k; i += kFrThreads) {
+        for (int i = tid; i < T * k; i += kThreads) {
             s_lists.sel_e[i] = agent_load(a.sel_e + i);
             s_lists.sel_w[i] = __builtin_bit_cast(float, agent_load((const int*)a.sel_w + i));
         }
     }
-    few_lists(a, s_lists);
+    few_lists<kThreads>(a, s_lists);
+}
+
+template <int kTok>
+static void launch_few_route_of(const FewRoute& a, hipStream_t stream) {
+    const dim3 grid(kFrRes, ceil_div(a.E, kFrEC), ceil_div(a.T, kTok));
+    if (a.E % 4 == 0 && ((uintptr_t)a.Wr & 15) == 0)
+        hipLaunchKernelGGL((few_route_kernel<true, kTok>), grid, dim3(kTok * kWave), 0, stream, a);
+    else
+        hipLaunchKernelGGL((few_route_kernel<false, kTok>), grid, dim3(kTok * kWave), 0, stream, a);
 }
 
 void launch_few_route(const FewRoute& a, hipStream_t stream) {
-    const dim3 grid(kFrRes, ceil_div(a.E, kFrEC), ceil_div(a.T, kFrTok));
-    if (a.E % 4 == 0 && ((uintptr_t)a.Wr & 15) == 0)
-        hipLaunchKernelGGL(few_route_kernel<true>, grid, dim3(kFrThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL(few_route_kernel<false>, grid, dim3(kFrThreads), 0, stream, a);
+    // up to eight tokens in one group: one count less (7 tokens, H 1024, 256
+    // experts, 14.7 against 16.0 us).  Past that four a group, for fewer lines a
+    // workgroup (16 tokens, H 7168, 32 experts, MXFP8, 13.7 against 16.2 us).
+    if (a.T <= 8) launch_few_route_of<8>(a, stream);
+    else launch_few_route_of<4>(a, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -338,7 +338,7 @@ constexpr int kFewTokens = 64;  // most tokens of one call: an expert's tokens a
 // Router of a few tokens: logits, top-k, softmax weights and the experts' row
 // lists.  Rows are grouped by expert in ascending order, by token within an
 // expert; the shared expert's T rows come last.
-constexpr int kFewCounters = 16 + (kFewTokens / 8) * (kMaxExperts / 32);
+constexpr int kFewCounters = 1 + (kFewTokens / 4) * (1 + kMaxExperts / 32);
 struct FewRoute {
     const uint16_t* x;   // [T][H]
     const float* Wr;     // [H][E]
