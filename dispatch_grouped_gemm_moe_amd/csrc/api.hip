@@ -997,7 +997,7 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t* dy, c
 
 // Workspace of moe_layer_fwd_few (byte offsets).
 struct FewPlan {
-    size_t counter, partial, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row, logits, xq, xs, h, hq, hs, y, total;
+    size_t counter, partial, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row, col_count, logits, xq, xs, h, hq, hs, y, total;
     int max_act;  // experts that T * k choices can reach, and the shared one
 };
 
@@ -1018,10 +1018,11 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
     f->row_token = take(rows * 4);
     f->row_w = take(rows * 4);
     f->slot_row = take(Tk * 4);
+    f->col_count = take(H / 16 * 4);
     f->partial = take(T * p->E * 16 * 4);
     f->logits = take(T * p->E * 4);
     f->h = take(rows * I * 2);
-    f->y = take(rows * H * 4);
+    f->y = take(std::max(rows, T * kFewMaxSplits) * H * 4);
     if (p->mx) {
         f->xq = take(T * H);
         f->xs = take((size_t)mx_groups(H) * T * 4);
@@ -1068,11 +1069,13 @@ moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uin
     r.sel_e = (int*)(b + f.sel_e); r.sel_w = (float*)(b + f.sel_w);
     r.n_act = (int*)(b + f.n_act); r.act_e = (int*)(b + f.act_e); r.act_off = (int*)(b + f.act_off);
     r.row_token = (int*)(b + f.row_token); r.row_w = (float*)(b + f.row_w); r.slot_row = (int*)(b + f.slot_row);
+    r.col_count = (int*)(b + f.col_count);
     TIMED(MOE_K_ROUTE, s, launch_few_route(r, s));
     FewGemm g{};
     g.T = p.T; g.H = p.H; g.I = p.I; g.E = p.E;
     g.n_act = r.n_act; g.act_e = r.act_e; g.act_off = r.act_off; g.row_token = r.row_token; g.row_w = r.row_w;
     g.slot_row = r.slot_row;
+    g.col_count = r.col_count;
     g.x = x; g.w1 = (const uint16_t*)(pk + p.pk_w1t); g.w2 = (const uint16_t*)(pk + p.pk_w2t);
     g.h = (uint16_t*)(b + f.h); g.y = (float*)(b + f.y);
     if (p.mx) {
@@ -1082,17 +1085,9 @@ moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uin
         g.hq = b + f.hq; g.hs = b + f.hs;
     }
     TIMED(MOE_K_GEMM_GATE_UP, s, launch_few_gate_up(g, f.max_act, s));
-    // Up to 16 tokens, the down product and the weighted sum are one launch of
-    // H / 16 workgroups, unless so few of them have so much to read that they
-    // would draw on memory less than the whole chip's tiles (33 KB/us each
-    // against 4.5 MB/us, less 3.5 us for the sum's launch).  Measured, one launch
-    // against two: H 2048, I 1024, 6 of 64 experts, 1 token bf16 (128 workgroups
-    // of 192 KB) 9.0 and 10.6 us; the same in MXFP8 with 8 tokens (590 KB) 22.7
-    // and 24.5 us; H 1024, I 512, 16 of 256, 7 tokens (64 of 750 KB) 26.4 and
-    // 22.2 us.
-    const int64_t few_wgs = p.H / 16, wg_kb = (int64_t)f.max_act * 16 * p.I * (p.mx ? 1 : 2) / 1024;
-    if (p.T <= 16 && wg_kb * (136 - few_wgs) < 16000) {
-        TIMED(MOE_K_GEMM_DOWN, s, launch_few_down16(g, f.max_act, p.T * (p.k + p.shared), p.shared, out, s));
+    if (p.T <= 16) {  // the down product and the weighted sum in one launch
+        const int splits = few_down16_splits(p.H, (int64_t)f.max_act * 16 * p.I * (p.mx ? 1 : 2) / 1024);
+        TIMED(MOE_K_GEMM_DOWN, s, launch_few_down16(g, f.max_act, p.T * (p.k + p.shared), p.shared, splits, out, s));
     } else {
         TIMED(MOE_K_GEMM_DOWN, s, launch_few_down(g, f.max_act, s));
         TIMED(MOE_K_COMBINE, s, launch_few_combine(g, p.k, p.shared, out, s));

@@ -139,6 +139,7 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
     static_assert(kMaxExperts <= kThreads && kThreads % kWave == 0, "an expert per thread");
     if (tid < kMaxExperts) s.mask[tid] = 0;
     __syncthreads();
+    for (int i = tid; i < a.H / 16; i += kThreads) a.col_count[i] = 0;  // of the down product's launch
     for (int i = tid; i < n; i += kThreads) atomicOr((unsigned long long*)&s.mask[s.sel_e[i]], 1ull << (i / a.k));
     __syncthreads();
     // exclusive prefixes over the experts, of rows and of experts that have any
@@ -759,6 +760,7 @@ struct FewUnit {
 // its index so that 16 rows fall on distinct banks.
 template <int kKind>
 __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int max_act, int max_rows, uint16_t* out) {
+    __shared__ int s_flag;
     constexpr bool kMx = kKind != kFewBf16;
     __shared__ __attribute__((aligned(1024))) uint8_t s_w[kFdWaves][2][kFdSlot];
     __shared__ __attribute__((aligned(16))) float s_sum[kFdWaves][kFdTok][kFdCols];
@@ -766,7 +768,7 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
     __shared__ float s_weight[kFdRows];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = blockIdx.x, H = a.H, I = a.I;
+    const int n = blockIdx.x, splits = gridDim.y, H = a.H, I = a.I;
     // the tables, up to what T and k allow: all asked for at once
     const int n_act = ld_layout(a.n_act);
     for (int i = tid; i < max_rows; i += kFdThreads) {
@@ -778,9 +780,10 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
     for (int i = tid; i < kFdWaves * kFdTok * kFdCols; i += kFdThreads) (&s_sum[0][0][0])[i] = 0.0f;
     // parts per expert (2^log_parts): as few as spread the units evenly enough (to a tenth)
     const int lines = (I * (kMx ? 1 : 2) + kFgChunk - 1) / kFgChunk, batches = (lines + kFdBatch - 1) / kFdBatch;
+    const int stride = kFdWaves * splits;
     int log_parts = 0;
     while ((2 << log_parts) <= batches &&
-           10 * ceil_div(n_act << log_parts, kFdWaves) * kFdWaves > 11 * (n_act << log_parts))
+           10 * ceil_div(n_act << log_parts, stride) * stride > 11 * (n_act << log_parts))
         ++log_parts;
     const int units = n_act << log_parts;
     __syncthreads();
@@ -864,7 +867,7 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
         for (int j = 0; j < kFdBatch; ++j) w[j] = __builtin_shufflevector(f[2 * j], f[2 * j + 1], 0, 1, 2, 3, 4, 5, 6, 7);
     };
     floatx4 acc = {0, 0, 0, 0};
-    int u = wave, c;
+    int u = blockIdx.y * kFdWaves + wave, c;
     FewUnit t = unit_of(u, c);
     Scales f0, f1;
     issue(t, c, 0, f0);
@@ -889,7 +892,7 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
         c += kFdBatch;
         const bool flush = c >= cur.end;
         if (flush) {
-            u += kFdWaves;
+            u += stride;
             t = unit_of(u, c);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -928,21 +931,50 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
         step(1, f1, f0);
     }
     __syncthreads();
-    for (int i = tid; i < a.T * kFdCols / 2; i += kFdThreads) {
-        const int tok = i / (kFdCols / 2), col = i % (kFdCols / 2) * 2;
-        float s0 = 0.0f, s1 = 0.0f;
+    // T x 16 sums, two a thread
+    const int tok = tid / (kFdCols / 2), col = tid % (kFdCols / 2) * 2;
+    static_assert(kFdTok * kFdCols / 2 <= kFdThreads, "two sums a thread");
+    float s0 = 0.0f, s1 = 0.0f;
+    if (tok < a.T) {
 #pragma unroll
         for (int w = 0; w < kFdWaves; ++w) {
             s0 += s_sum[w][tok][col];
             s1 += s_sum[w][tok][col + 1];
         }
+    }
+    if (splits > 1) {
+        uint64_t* part = (uint64_t*)a.y + ((size_t)n * splits * a.T + tok) * (kFdCols / 2) + col / 2;
+        const size_t next = (size_t)a.T * (kFdCols / 2);
+        if (tok < a.T)
+            __hip_atomic_store(part + blockIdx.y * next,
+                               (uint64_t)__builtin_bit_cast(uint32_t, s0) |
+                                   (uint64_t)__builtin_bit_cast(uint32_t, s1) << 32,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (!counts_in_last(a.col_count + n, splits, &s_flag)) return;
+        s0 = s1 = 0.0f;
+        if (tok < a.T)
+            for (int z = 0; z < splits; ++z) {
+                const uint64_t two = __hip_atomic_load(part + z * next, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                s0 += __builtin_bit_cast(float, (uint32_t)two);
+                s1 += __builtin_bit_cast(float, (uint32_t)(two >> 32));
+            }
+    }
+    if (tok < a.T)
         *(uint32_t*)(out + (size_t)tok * H + n * kFdCols + col) =
             (uint32_t)f32_to_bf16_rne(s0) | ((uint32_t)f32_to_bf16_rne(s1) << 16);
-    }
 }
 
-void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, uint16_t* out, hipStream_t stream) {
-    const dim3 grid(a.H / kFdCols), block(kFdThreads);
+int few_down16_splits(int H, int64_t column_kb) {
+    // as many workgroups as CUs, each with about 100 KB to read at least
+    const int n = H / kFdCols;
+    const int64_t by_work = column_kb / 100, by_cus = 256 / n;
+    const int64_t z = by_work < by_cus ? by_work : by_cus;
+    return z < 1 ? 1 : (z > kFewMaxSplits ? kFewMaxSplits : (int)z);
+}
+
+void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, int splits, uint16_t* out,
+                       hipStream_t stream) {
+    const dim3 grid(a.H / kFdCols, splits), block(kFdThreads);
     if (!a.xq)
         hipLaunchKernelGGL(few_down16_kernel<kFewBf16>, grid, block, 0, stream, a, max_act, max_rows, out);
     else if (!shared)

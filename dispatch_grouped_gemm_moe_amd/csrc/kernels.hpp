@@ -357,6 +357,7 @@ struct FewRoute {
     int* row_token;      // [rows]
     float* row_w;        // [rows] weight, 1 for the shared expert
     int* slot_row;       // [T][k] row of each selection
+    int* col_count;      // [H / 16] cleared for launch_few_down16
 };
 void launch_few_route(const FewRoute& a, hipStream_t stream);
 
@@ -376,12 +377,17 @@ struct FewGemm {
     const uint8_t *w1q, *s1, *w2q, *s2;
     uint8_t* hq;                       // [rows][I]
     uint8_t* hs;                       // [rows][mx_groups(I)][4]
-    float* y;                          // [rows][H] weighted expert outputs
+    float* y;                          // [rows][H] weighted expert outputs; launch_few_down16: [H/16][splits][T][16]
+    int* col_count;                    // [H / 16], zero
 };
 void launch_few_gate_up(const FewGemm& a, int max_act, hipStream_t stream);
 void launch_few_down(const FewGemm& a, int max_act, hipStream_t stream);
-// up to 16 tokens: the down product with the weighted sum
-void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, uint16_t* out, hipStream_t stream);
+// up to 16 tokens: the down product with the weighted sum; column_kb: what the
+// weight rows of 16 output columns come to over the active experts
+constexpr int kFewMaxSplits = 8;
+int few_down16_splits(int H, int64_t column_kb);
+void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, int splits, uint16_t* out,
+                       hipStream_t stream);
 void launch_few_combine(const FewGemm& a, int k, int shared, uint16_t* out, hipStream_t stream);
 
 // ---- residual addition and root-mean-square norm (norm.hip) ----
