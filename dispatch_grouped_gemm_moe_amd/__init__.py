@@ -225,11 +225,14 @@ def _dense(fn, device, t, dtype, n):
 
 def _call(fn, device, stream, *args):
     """Library function fn(*args, stream) on `device`: the given stream, or that device's current one.  A
-    launch goes to the current device's queues, so that one is made current for the call."""
+    launch goes to the current device's queues, so that one is made current for the call.  Host tensors
+    are refused: the kernels would fault on them."""
     import torch
-    if device < 0 or device == torch.cuda.current_device():
+    if device < 0:
+        raise MoeError(fn, MOE_E_INVALID)
+    if device == torch.cuda.current_device():
         if stream is None:
-            s = torch._C._cuda_getCurrentRawStream(max(device, 0))
+            s = torch._C._cuda_getCurrentRawStream(device)
         else:
             s = stream if isinstance(stream, int) else stream.cuda_stream
         st = getattr(_load(), fn)(*args, s)
