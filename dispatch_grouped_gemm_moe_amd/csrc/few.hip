@@ -12,14 +12,18 @@
 // every weight fragment and nothing is padded past 16 rows.
 //
 // Three launches: the router (logits, top-k, expert row lists), the gate|up
-// product with SwiGLU, and the down product with the weighted sum (two launches
-// past 16 tokens).  Two other forms
-// of the products were built and measured on one MXFP8 token (H 7168, I 2048, 8
-// of 32 experts; 85 us a call as it is): all three in one launch with tiles
-// handed out by a ticket, down tiles waiting on counters, took 159 us (atomics
-// on one cache line complete one per 30 ns); workgroups that stay and ask for
-// their next tile's weights before they reduce the present one, 82 us, and 343
-// us against 301 us for 16 tokens with the shared expert, by register spills.
+// product with SwiGLU, and the down product with the weighted sum; past 16
+// tokens the weighted sum has a launch of its own.  One MXFP8 token of H 7168, I
+// 2048, 8 of 32 experts takes 82 us (363 MB of weights: 4.4 TB/s over the call,
+// 5.4 over the gate|up product's 44 us), 64 bf16 tokens of the same sizes 533 us
+// (2.82 GB, 5.3 TB/s).
+//
+// Two other forms of the products were built and measured on that one token, then
+// 85 us: all three in one launch with tiles handed out by a ticket, down tiles
+// waiting on counters, took 159 us (atomics on one cache line complete one per
+// 30 ns); workgroups that stay and ask for their next tile's weights before they
+// reduce the present one, 82 us, and 343 us against 301 us for 16 tokens with the
+// shared expert, by register spills.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "mxfp8.hpp"
@@ -701,14 +705,15 @@ static void launch_few_gemm(const FewGemm& a, int max_act, hipStream_t stream) {
     const dim3 grid((unsigned)max_act * (unsigned)(kDown ? a.H / kFgRows : a.I / 32)), block(kFgThreads);
     const int mt = ceil_div(a.T, 16);  // an expert has at most T rows
 #define FEW_LAUNCH(MX, MT) hipLaunchKernelGGL((few_gemm_kernel<kDown, MX, MT>), grid, block, 0, stream, a)
-    if (a.xq) {
-        if (mt == 1) FEW_LAUNCH(true, 1);
-        else if (mt == 2) FEW_LAUNCH(true, 2);
-        else FEW_LAUNCH(true, 4);
-    } else {
-        if (mt == 1) FEW_LAUNCH(false, 1);
-        else if (mt == 2) FEW_LAUNCH(false, 2);
+    if (mt > 2) {
+        if (a.xq) FEW_LAUNCH(true, 4);
         else FEW_LAUNCH(false, 4);
+    } else if (kDown || mt == 2) {  // the down product of up to 16 tokens is few_down16_kernel's
+        if (a.xq) FEW_LAUNCH(true, 2);
+        else FEW_LAUNCH(false, 2);
+    } else if constexpr (!kDown) {
+        if (a.xq) FEW_LAUNCH(true, 1);
+        else FEW_LAUNCH(false, 1);
     }
 #undef FEW_LAUNCH
 }
@@ -824,8 +829,8 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
     struct Scales { uint32_t s[kMx ? kFdBatch : 1]; };
     // Ask for the weights of step (t, c) into the slot, load q taking rows 8 (q %
     // 2) .. + 7 of line c + q / 2.  Past the part's end its last line is repeated
-    // (against zero token rows); past the end of an MXFP8 row, in the middle of a
-    // line, its first half (against zero scale bytes).  And for the scale dwords.
+    // (and dropped); past the end of an MXFP8 row, in the middle of a line,
+    // its first half (against zero scale bytes).  And for the scale dwords.
     auto issue = [&](const FewUnit& t, int c, int slot, Scales& f) {
         uint8_t* dst = s_w[wave][slot];
         const int last = max(t.end - 1, 0);
@@ -877,17 +882,18 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
         intx8 x[kFdBatch];
         uint32_t xs[kMx ? kFdBatch : 1];
         const uint32_t r = (uint32_t)min((int)lr, cur.rows - 1);  // past the last row: the last one again
+        const int last = max(cur.end - 1, 0);
+        const __amdgpu_buffer_rsrc_t d = few_rsrc(cur.x, (uint32_t)(cur.rows * cur.kb));
 #pragma unroll
         for (int j = 0; j < kFdBatch; ++j) {
-            const int in = (c0 + j - cur.end) >> 31, at = ((c0 + j) * kFgChunk) & in;
-            const int hi = at + (kFgChunk / 2 & (kMx ? (at + kFgChunk / 2 - cur.kb) >> 31 : -1) & in);
-            const __amdgpu_buffer_rsrc_t d = few_rsrc(cur.x, (uint32_t)(cur.rows * cur.kb & in));
+            const int line = min(c0 + j, last), at = line * kFgChunk;
+            const int hi = kMx && at + kFgChunk / 2 >= cur.kb ? at : at + kFgChunk / 2;
             const intx4 p0 = __builtin_amdgcn_raw_buffer_load_b128(d, r * (uint32_t)cur.kb + lo, at, 0);
             const intx4 p1 = __builtin_amdgcn_raw_buffer_load_b128(d, r * (uint32_t)cur.kb + lo, hi, 0);
             x[j] = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
             if constexpr (kMx)
                 xs[j] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(cur.xs, cur.xs_bytes),
-                                                             r * (uint32_t)mx_groups(I) * 4, ((c0 + j) * 4) & in, 0);
+                                                             r * (uint32_t)mx_groups(I) * 4, line * 4, 0);
         }
         c += kFdBatch;
         const bool flush = c >= cur.end;
@@ -902,6 +908,11 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kFdBatch + (kMx ? kFdBatch : 0)) : "memory");
         intx8 w[kFdBatch];
         frags(slot, w);
+        if (c0 + kFdBatch > cur.end) {  // zero times zero past the part's end, whatever the last line holds
+#pragma unroll
+            for (int j = 0; j < kFdBatch; ++j)
+                if (c0 + j >= cur.end) w[j] = x[j] = intx8{};
+        }
 #pragma unroll
         for (int j = 0; j < kFdBatch; ++j) {
             if (kKind == kFewMx || (kKind == kFewMxShared && cur.mx)) {
@@ -965,7 +976,11 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
 }
 
 int few_down16_splits(int H, int64_t column_kb) {
-    // as many workgroups as CUs, each with about 100 KB to read at least
+    // As many workgroups as CUs, each with about 100 KB to read at least.  64
+    // column blocks of 750 KB take 26.4 us whole and 16.8 us in four (7 tokens, H
+    // 1024, 16 of 256 experts), 128 of 590 KB 22.7 and 19.8 us in two; 128 of 192
+    // KB (9.0 us whole) stay whole: each part reads the row lists anew and the last
+    // to finish reads every part's sums.
     const int n = H / kFdCols;
     const int64_t by_work = column_kb / 100, by_cus = 256 / n;
     const int64_t z = by_work < by_cus ? by_work : by_cus;

@@ -63,6 +63,17 @@ def test_few_refuses_small_buffers_and_misaligned_codes():
     assert _call(cfg, packed_bytes=s.packed_weights - 1) == moe.MOE_E_WORKSPACE
 
 
+def test_few_binding_refuses_host_tensors():
+    cfg = _cfg()
+    u8, b16 = torch.uint8, torch.bfloat16
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_layer_fwd_few(cfg, torch.zeros(128, 8), None,
+                              torch.zeros(moe.moe_query_sizes(cfg).packed_weights, dtype=u8),
+                              torch.zeros(8, 128, dtype=b16), torch.zeros(8, 128, dtype=b16),
+                              torch.zeros(moe.moe_query_few(cfg), dtype=u8), stream=0)
+    assert e.value.status == moe.MOE_E_INVALID
+
+
 def test_few_binding_refuses_tensors_the_kernels_cannot_read():
     cfg = _cfg()
     ok = dict(Wr=torch.zeros(128, 8), bias=None, packed=torch.zeros(16, dtype=torch.uint8),
@@ -188,6 +199,64 @@ def test_few_a_token_that_is_not_finite_spoils_only_itself(gpu_lib, bad):
     got = few(x)
     keep = torch.arange(20, device="cuda") != 3
     assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[3]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [12, 20])
+def test_few_mxfp8_token_that_is_not_finite_spoils_only_itself(gpu_lib, T, bad):
+    # every expert is chosen by every token, so that the sums of the others keep their order
+    w = _wl(T, 256, 64, 4, 4, prec="mxfp8", shared=True)
+    few = Few(w)
+    want = few()
+    x = few.x.clone()
+    x[3, 17] = bad
+    got = few(x)
+    keep = torch.arange(T, device="cuda") != 3
+    assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[3]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("I", [64, 192, 448])
+@pytest.mark.parametrize("T", [3, 20])
+def test_few_an_infinite_weight_gives_infinity(gpu_lib, T, I):
+    # the last row of Wd: steps past the end of I must not meet it again
+    w = _wl(T, 128, I, 4, 4)
+    inp = make_inputs(w)
+    inp.x[:, 0] = 8  # gate and up of the last column are 8, so that h there is positive
+    for m in (inp.Wg, inp.Wu):
+        m[:, :, I - 1] = 0
+        m[:, 0, I - 1] = 1
+    clean = Few(w, inp)
+    inp.Wd[:, I - 1, 5] = float("inf")
+    few = Few(w, inp)
+    got, want = few(), clean()
+    other = torch.arange(128, device="cuda") != 5
+    assert torch.equal(got[:, other], want[:, other])
+    # h of the last column is positive for every token and expert: +inf, not NaN
+    assert (got[:, 5] == float("inf")).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("shape", [(1, 448, 64, 256, 16), (6, 64, 64, 8, 3), (11, 2112, 64, 33, 7), (64, 320, 128, 256, 16)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_few_routes_as_the_router_does(gpu_lib, shape, prec):
+    # silu(64) / 64 is 1 in fp32: expert e's output is 1 in column e, the layer's the routing weights
+    w = _wl(*shape, prec=prec, bias="normal")
+    inp = make_inputs(w)
+    inp.x[:, 0] = 1
+    for m in (inp.Wg, inp.Wu, inp.Wd):
+        m.zero_()
+    inp.Wg[:, 0, 0], inp.Wu[:, 0, 0] = 64, 1 / 64
+    for e in range(w.E):
+        inp.Wd[e, 0, e] = 1
+    few = Few(w, inp)
+    idx = torch.empty(w.T, w.k, dtype=torch.int32, device="cuda")
+    gw = torch.empty(w.T, w.k, device="cuda")
+    moe.moe_route(few.cfg, few.x, few.Wr, few.bias, idx, gw)
+    want = torch.zeros(w.T, w.H, device="cuda").scatter_(1, idx.long(), gw).bfloat16()
+    assert torch.equal(few(), want)
 
 
 @pytest.mark.gpu
