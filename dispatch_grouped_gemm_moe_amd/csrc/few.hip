@@ -364,7 +364,12 @@ void launch_few_route(const FewRoute& a, hipStream_t stream) {
 // Expert products
 // ---------------------------------------------------------------------------
 
-constexpr int kFgThreads = 512;
+// Four waves, whose partial sums meet in LDS once per tile.  Eight a workgroup
+// give a wave half the steps for the same start and epilogue: 61.0 against 54.5
+// us a call (7 tokens, H 1024, I 512, 16 of 256 experts, MXFP8), 114 against 90
+// (24 tokens, H 2048, I 1024, 6 of 64).  Two double the tokens' loads and the
+// epilogue of a wave: 557 against 531 us (64 tokens, H 7168, I 2048, 8 of 32).
+constexpr int kFgThreads = 256;
 constexpr int kFgWaves = kFgThreads / kWave;
 constexpr int kFgRows = 64;                 // weight rows per workgroup
 constexpr int kFgChunk = 128;               // bytes of a weight row per step: one cache line
@@ -492,7 +497,7 @@ __device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<
 }
 
 // acc[i][m] (+)= weight rows 16 i .. of the tile times token rows 16 m .., over
-// the steps wave, wave + 8, ... of the rows' kb bytes.  The weights of one step
+// the steps wave, wave + 4, ... of the rows' kb bytes.  The weights of one step
 // are in flight while the step before is multiplied; the tokens, which come
 // from the L2, are loaded in their own step, ahead of the next weights, so that
 // waiting for them (loads return in order) leaves those in flight.  Steps past
@@ -570,43 +575,45 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
     few_stream<MX, MT, true>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
-    // thread (token tid / 32, column tid % 32): the tile's rows are 32 gate
+    // thread (tokens tid / 32, + 8; column tid % 32): the tile's rows are 32 gate
     // columns and the 32 up columns of the same indices
-    const int tt = tid >> 5, col = tid & 31;
+    const int col = tid & 31;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         if (m * 16 >= rows) break;
         __syncthreads();
         few_stage<MT>(acc, m, wave, lane, s_part);
         __syncthreads();
-        float g = 0.0f, u = 0.0f;
+        for (int tt = tid >> 5; tt < 16; tt += kFgThreads / 32) {
+            float g = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFgWaves; ++w) {
-            g += s_part[(w * 16 + tt) * kFgLd + col];
-            u += s_part[(w * 16 + tt) * kFgLd + 32 + col];
-        }
-        const float h = g / (1.0f + expf(-g)) * u;
-        const int r = m * 16 + tt;
-        if (MX) {  // the 32 columns of a token are one MXFP8 block, held by half a wave
-            float am = fabsf(h);
-#pragma unroll
-            for (int s = 16; s >= 1; s >>= 1) am = fmaxf(am, __shfl_xor(am, s, kWave));
-            const int ex = mx_scale_exp(am);
-            const uint32_t code = fp8x4(ldexpf(h, -ex), 0.0f, 0.0f, 0.0f);
-            if (r < rows) {
-                a.hq[(size_t)(row0 + r) * I + n * 32 + col] = (uint8_t)code;
-                if (col == 0) {  // a row's scale dwords are adjacent; the last group's spare bytes are zero
-                    uint8_t* d = a.hs + (size_t)(row0 + r) * mx_groups(I) * 4 + n;
-                    d[0] = (uint8_t)(ex + 127);
-                    if (n + 1 == I / 32)
-                        for (int z = 1; (n + z) & 3; ++z) d[z] = 0;
-                }
+            for (int w = 0; w < kFgWaves; ++w) {
+                g += s_part[(w * 16 + tt) * kFgLd + col];
+                u += s_part[(w * 16 + tt) * kFgLd + 32 + col];
             }
-        } else if (r < rows) {
-            // bf16, as the layer forward keeps h: an operand of the next MFMA.  In
-            // two bf16 parts the layer's error would be 2^-8.5 rather than 2^-8 of
-            // its output, for 2 us of 29 (one token, H 2048) and 25 of 536 (64, H 7168).
-            a.h[(size_t)(row0 + r) * I + n * 32 + col] = f32_to_bf16_rne(h);
+            const float h = g / (1.0f + expf(-g)) * u;
+            const int r = m * 16 + tt;
+            if (MX) {  // the 32 columns of a token are one MXFP8 block, held by half a wave
+                float am = fabsf(h);
+#pragma unroll
+                for (int s = 16; s >= 1; s >>= 1) am = fmaxf(am, __shfl_xor(am, s, kWave));
+                const int ex = mx_scale_exp(am);
+                const uint32_t code = fp8x4(ldexpf(h, -ex), 0.0f, 0.0f, 0.0f);
+                if (r < rows) {
+                    a.hq[(size_t)(row0 + r) * I + n * 32 + col] = (uint8_t)code;
+                    if (col == 0) {  // a row's scale dwords are adjacent; the last group's spare bytes are zero
+                        uint8_t* d = a.hs + (size_t)(row0 + r) * mx_groups(I) * 4 + n;
+                        d[0] = (uint8_t)(ex + 127);
+                        if (n + 1 == I / 32)
+                            for (int z = 1; (n + z) & 3; ++z) d[z] = 0;
+                    }
+                }
+            } else if (r < rows) {
+                // bf16, as the layer forward keeps h: an operand of the next MFMA.  In
+                // two bf16 parts the layer's error would be 2^-8.5 rather than 2^-8 of
+                // its output, for 2 us of 29 (one token, H 2048) and 25 of 536 (64, H 7168).
+                a.h[(size_t)(row0 + r) * I + n * 32 + col] = f32_to_bf16_rne(h);
+            }
         }
     }
 }
@@ -646,25 +653,27 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
     few_stream<MX, MT, false>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
-    const int tt = tid >> 5, col = (tid & 31) * 2;
+    const int col = (tid & 31) * 2;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         if (m * 16 >= rows) break;
         __syncthreads();
         few_stage<MT>(acc, m, wave, lane, s_part);
         __syncthreads();
-        float y0 = 0.0f, y1 = 0.0f;
+        for (int tt = tid >> 5; tt < 16; tt += kFgThreads / 32) {
+            float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFgWaves; ++w) {
-            y0 += s_part[(w * 16 + tt) * kFgLd + col];
-            y1 += s_part[(w * 16 + tt) * kFgLd + col + 1];
-        }
-        const int r = m * 16 + tt;
-        if (r < rows) {
-            const float wt = a.row_w[row0 + r];
-            float* d = a.y + (size_t)(row0 + r) * H + n * kFgRows + col;
-            d[0] = wt * y0;
-            d[1] = wt * y1;
+            for (int w = 0; w < kFgWaves; ++w) {
+                y0 += s_part[(w * 16 + tt) * kFgLd + col];
+                y1 += s_part[(w * 16 + tt) * kFgLd + col + 1];
+            }
+            const int r = m * 16 + tt;
+            if (r < rows) {
+                const float wt = a.row_w[row0 + r];
+                float* d = a.y + (size_t)(row0 + r) * H + n * kFgRows + col;
+                d[0] = wt * y0;
+                d[1] = wt * y1;
+            }
         }
     }
 }
@@ -686,13 +695,16 @@ __device__ __forceinline__ void few_tile_rows(const FewGemm& a, int e, int n, in
 
 // Workgroup b: active expert b / n_tiles, weight rows 64 (b % n_tiles) .. + 63.
 // The host sizes the grid for every expert that T * k choices can reach; the
-// workgroups past the active ones end at once.  kMost: 16-row fragments of T.
+// workgroups past the active ones end at once.  kMost: 16-row fragments of T.  The
+// bound on waves keeps the compiler from spreading over accumulation registers,
+// which would halve the waves per SIMD past 16 tokens.
 template <bool kDown, bool kMx, int kMost>
-__global__ __launch_bounds__(kFgThreads) void few_gemm_kernel(FewGemm a) {
+__global__ __launch_bounds__(kFgThreads, kMost == 1 ? 1 : (kMost == 4 ? 2 : (kMx ? 3 : 4))) void few_gemm_kernel(
+    FewGemm a) {
     __shared__ __attribute__((aligned(16))) float s_part[kFgWaves * 16 * kFgLd];
     const int nt = kDown ? a.H / kFgRows : a.I / 32;
     const int i = blockIdx.x / nt, n = blockIdx.x - i * nt;
-    // all four at once: the lists hold an entry for every expert of the grid
+    // the lists hold an entry for every expert of the grid
     const int n_act = ld_layout(a.n_act), e = ld_layout(a.act_e + i), row0 = ld_layout(a.act_off + i);
     const int rows = ld_layout(a.act_off + i + 1) - row0;
     if (i >= n_act) return;
