@@ -376,7 +376,8 @@ moe_status moe_query_add_rmsnorm_bwd(int64_t rows, int32_t cols, size_t *workspa
  *   checkpoint ck_codes, ck_scales: exactly one of the two, the other NULL;
  *   rstd fp32 [rows], weight fp32 [cols]: the forward's;
  *   dx bf16 [rows, cols], which may be dy or dsum itself;
- *   ws: at least moe_query_add_rmsnorm_bwd bytes, 16-byte aligned, of any content.
+ *   ws: at least moe_query_add_rmsnorm_bwd bytes, 16-byte aligned, of any
+ *       content; calls that overlap on two streams take one each.
  * Sums have a fixed order, so results are bitwise repeatable.  Refusals as
  * moe_add_rmsnorm_fwd's, and MOE_E_WORKSPACE for a smaller workspace.
  */
@@ -392,14 +393,16 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t *dy, c
  * moe_prepare_weights buffer serves both) and formula, the same expert choice
  * and weights bit for bit; the outputs differ from moe_layer_fwd's by the
  * rounding of sums taken in another order (here the expert outputs stay fp32
- * until the weighted sum).  Runs of one call are bitwise repeatable.
+ * until the weighted sum).  Runs of one call are bitwise repeatable; a token's
+ * sums may be taken in another order beside other tokens.
  *   x, out [T,H] bf16, 16-byte aligned; they may not overlap;
  *   x_codes, x_scales: MOE_PREC_MXFP8, optional: the MXFP8 form of x as
  *       moe_route or moe_add_rmsnorm_fwd wrote it (codes 16-byte aligned,
  *       scales 4); both or neither.  Without them the call quantises x itself.
  *   ws: at least moe_query_few bytes, 256-byte aligned; zero its first
  *       MOE_FEW_COUNTER_BYTES bytes once when it is allocated (every call
- *       leaves them zero).
+ *       leaves them zero).  One call at a time: calls that overlap on two
+ *       streams take a workspace each.
  * cfg->minibatch, ring_slots, comm_cus and the flags other than
  * MOE_F_SHARED_EXPERT have no effect.  MOE_E_UNSUPPORTED for more tokens and
  * in identity-expert mode; MOE_E_INVALID for x_codes with MOE_PREC_BF16.

@@ -337,3 +337,17 @@ def test_few_on_another_stream(gpu_lib):
         moe.moe_layer_fwd_few(few.cfg, few.Wr, few.bias, few.packed, x, out, few.ws)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+def test_few_two_calls_at_once(gpu_lib):
+    few = [Few(_wl(12, 512, 256, 8, 2, prec="mxfp8")), Few(_wl(40, 512, 256, 8, 3))]
+    want = [f() for f in few]
+    outs = [torch.zeros_like(f.x) for f in few]
+    streams = [torch.cuda.Stream() for _ in few]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for f, o, s in zip(few, outs, streams):
+            moe.moe_layer_fwd_few(f.cfg, f.Wr, f.bias, f.packed, f.x, o, f.ws, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
