@@ -32,7 +32,7 @@ EXPORTS = ("moe_status_string", "moe_abi_version", "moe_validate_cfg", "moe_quer
            "moe_add_rmsnorm_fwd", "moe_add_rmsnorm_bwd", "moe_query_add_rmsnorm_bwd", "moe_layer_fwd_few",
            "moe_query_few")
 MOE_STATIC_WORKSPACE_BYTES = 256 << 20
-MOE_FEW_MAX_TOKENS, MOE_FEW_COUNTER_BYTES = 64, 1024
+MOE_FEW_MAX_TOKENS, MOE_FEW_COUNTER_BYTES = 64, 36864
 KERNEL_KINDS = ("route", "layout", "gemm_gate_up", "gemm_down", "combine", "gather", "other", "wgrad",
                 "dgrad_down", "dgrad_gate_up", "shared_gemm", "layer")
 

@@ -997,7 +997,7 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t* dy, c
 
 // Workspace of moe_layer_fwd_few (byte offsets).
 struct FewPlan {
-    size_t counter, partial, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row, col_count, logits, xq, xs, h, hq, hs, y, total;
+    size_t counter, partial, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row, logits, xq, xs, h, hq, hs, y, total;
     int max_act;  // experts that T * k choices can reach, and the shared one
 };
 
@@ -1006,7 +1006,8 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
     if (st != MOE_OK) return st;
     if (p->T > kFewTokens || p->identity) return MOE_E_UNSUPPORTED;
     const size_t T = p->T, H = p->H, I = p->I, Tk = T * p->k, rows = Tk + (p->shared ? T : 0);
-    static_assert(kFewCounters * 4 <= MOE_FEW_COUNTER_BYTES, "the counters fit their block");
+    static_assert((kFewCounters + kFewMaxSplitCols) * kFewCounterInts * 4 <= MOE_FEW_COUNTER_BYTES,
+                  "the counters fit their block");
     size_t o = MOE_FEW_COUNTER_BYTES;  // the counters, zero between calls
     f->counter = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
@@ -1018,7 +1019,6 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
     f->row_token = take(rows * 4);
     f->row_w = take(rows * 4);
     f->slot_row = take(Tk * 4);
-    f->col_count = take(H / 16 * 4);
     f->partial = take(T * p->E * 16 * 4);
     f->logits = take(T * p->E * 4);
     f->h = take(rows * I * 2);
@@ -1069,13 +1069,12 @@ moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uin
     r.sel_e = (int*)(b + f.sel_e); r.sel_w = (float*)(b + f.sel_w);
     r.n_act = (int*)(b + f.n_act); r.act_e = (int*)(b + f.act_e); r.act_off = (int*)(b + f.act_off);
     r.row_token = (int*)(b + f.row_token); r.row_w = (float*)(b + f.row_w); r.slot_row = (int*)(b + f.slot_row);
-    r.col_count = (int*)(b + f.col_count);
     TIMED(MOE_K_ROUTE, s, launch_few_route(r, s));
     FewGemm g{};
     g.T = p.T; g.H = p.H; g.I = p.I; g.E = p.E;
     g.n_act = r.n_act; g.act_e = r.act_e; g.act_off = r.act_off; g.row_token = r.row_token; g.row_w = r.row_w;
     g.slot_row = r.slot_row;
-    g.col_count = r.col_count;
+    g.col_count = r.counter + kFewCounters * kFewCounterInts;
     g.x = x; g.w1 = (const uint16_t*)(pk + p.pk_w1t); g.w2 = (const uint16_t*)(pk + p.pk_w2t);
     g.h = (uint16_t*)(b + f.h); g.y = (float*)(b + f.y);
     if (p.mx) {

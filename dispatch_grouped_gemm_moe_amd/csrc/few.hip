@@ -143,7 +143,6 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
     static_assert(kMaxExperts <= kThreads && kThreads % kWave == 0, "an expert per thread");
     if (tid < kMaxExperts) s.mask[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < a.H / 16; i += kThreads) a.col_count[i] = 0;  // of the down product's launch
     for (int i = tid; i < n; i += kThreads) atomicOr((unsigned long long*)&s.mask[s.sel_e[i]], 1ull << (i / a.k));
     __syncthreads();
     // exclusive prefixes over the experts, of rows and of experts that have any
@@ -293,7 +292,7 @@ __global__ __launch_bounds__(kTok * kWave) void few_route_kernel(FewRoute a) {
         if (wave < nt && half == 0 && el < ne)
             agent_store((int*)a.partial + ((size_t)(t0 + wave) * E + e0 + el) * kFrRes + l, __builtin_bit_cast(int, v));
     }
-    if (!counts_in_last(a.counter + 1 + kFewTokens / 4 + blockIdx.z * ng + blockIdx.y, kFrRes, &s_flag)) return;
+    if (!counts_in_last(a.counter + (1 + kFewTokens / 4 + blockIdx.z * ng + blockIdx.y) * kFewCounterInts, kFrRes, &s_flag)) return;
     for (int i = tid; i < nt * ne; i += kThreads) {
         const int ti = i / ne, ei = i - ti * ne;
         const uint64_t* q = (const uint64_t*)(a.partial + ((size_t)(t0 + ti) * E + e0 + ei) * kFrRes);
@@ -314,7 +313,7 @@ __global__ __launch_bounds__(kTok * kWave) void few_route_kernel(FewRoute a) {
         if (ng > 1) agent_store((int*)a.logits + (size_t)(t0 + ti) * E + e0 + ei, __builtin_bit_cast(int, z));
     }
     if (ng > 1) {
-        if (!counts_in_last(a.counter + 1 + blockIdx.z, ng, &s_flag)) return;
+        if (!counts_in_last(a.counter + (1 + blockIdx.z) * kFewCounterInts, ng, &s_flag)) return;
         for (int i = tid; i < nt * E; i += kThreads)
             s_logit[i / E][i % E] = __builtin_bit_cast(float, agent_load((const int*)a.logits + (size_t)t0 * E + i));
     }
@@ -973,7 +972,7 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
                                (uint64_t)__builtin_bit_cast(uint32_t, s0) |
                                    (uint64_t)__builtin_bit_cast(uint32_t, s1) << 32,
                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (!counts_in_last(a.col_count + n, splits, &s_flag)) return;
+        if (!counts_in_last(a.col_count + n * kFewCounterInts, splits, &s_flag)) return;
         s0 = s1 = 0.0f;
         if (tok < a.T)
             for (int z = 0; z < splits; ++z) {
@@ -994,6 +993,7 @@ int few_down16_splits(int H, int64_t column_kb) {
     // KB (9.0 us whole) stay whole: each part reads the row lists anew and the last
     // to finish reads every part's sums.
     const int n = H / kFdCols;
+    static_assert(256 / (kFewMaxSplitCols + 1) < 2, "a counter for every column block that is split");
     const int64_t by_work = column_kb / 100, by_cus = 256 / n;
     const int64_t z = by_work < by_cus ? by_work : by_cus;
     return z < 1 ? 1 : (z > kFewMaxSplits ? kFewMaxSplits : (int)z);

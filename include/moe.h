@@ -409,7 +409,7 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t *dy, c
  * Inputs must be finite: a NaN reaches its own token's output only.
  */
 #define MOE_FEW_MAX_TOKENS 64
-#define MOE_FEW_COUNTER_BYTES 1024
+#define MOE_FEW_COUNTER_BYTES 36864
 moe_status moe_layer_fwd_few(const moe_cfg *cfg, const moe_weights *w, const uint16_t *x,
                              const uint8_t *x_codes, const uint8_t *x_scales, uint16_t *out, void *ws,
                              size_t ws_bytes, void *stream);
