@@ -242,16 +242,24 @@ __global__ __launch_bounds__(kTok * kWave) void few_route_kernel(FewRoute a) {
         if (c0) __syncthreads();  // the previous slab is summed
         // LDS row 4 c + j: h = 64 (c0 + c) + l + 16 j
         auto h_of = [&](int r) { return (c0 + (r >> 2)) * kWave + l + 16 * (r & 3); };
-        if (kVec4 && ne == kFrEC) {
+        // (the columns past the last expert hold anything: nobody reads their sums)
+        if (kVec4) {
             // eight rows per load; a slab's rows are a multiple of four
-            for (int r = wave * 8; r < nc * 4; r += kTok * 8)
-                __builtin_amdgcn_global_load_lds(
-                    (gbl_cvoid*)(a.Wr + (size_t)h_of(min(r + (lane >> 3), nc * 4 - 1)) * E + e0 + (lane & 7) * 4),
-                    (lds_void*)s_wr[r], 16, 0, 0);
+            if ((lane & 7) * 4 < ne)
+                for (int r = wave * 8; r < nc * 4; r += kTok * 8)
+                    __builtin_amdgcn_global_load_lds(
+                        (gbl_cvoid*)(a.Wr + (size_t)h_of(min(r + (lane >> 3), nc * 4 - 1)) * E + e0 + (lane & 7) * 4),
+                        (lds_void*)s_wr[r], 16, 0, 0);
         } else {
-            for (int i = tid; i < nc * 4 * kFrEC; i += kThreads) {
-                const int r = i / kFrEC, q = i % kFrEC;
-                s_wr[r][q] = q < ne ? a.Wr[(size_t)h_of(r) * E + e0 + q] : 0.0f;
+            // a row per half wave, eight loads of a thread at once
+            constexpr int kRows = kThreads / kFrEC;
+            const int q = min(el, ne - 1);
+            for (int r0 = tid / kFrEC; r0 < nc * 4; r0 += 8 * kRows) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = a.Wr[(size_t)h_of(min(r0 + j * kRows, nc * 4 - 1)) * E + e0 + q];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s_wr[min(r0 + j * kRows, nc * 4 - 1)][el] = v[j];
             }
         }
         if (wave < nt) {
