@@ -997,8 +997,10 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t* dy, c
 
 // Workspace of moe_layer_fwd_few (byte offsets).
 struct FewPlan {
-    size_t counter, partial, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row, logits, xq, xs, h, hq, hs, y, total;
-    int max_act;  // experts that T * k choices can reach, and the shared one
+    size_t counter, partial, logits, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row;
+    size_t xq, xs, gu_part, h, hq, hs, y, total;
+    int max_act;    // experts that T * k choices can reach, and the shared one
+    int gu_splits;  // parts of H in the gate|up product
 };
 
 static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
@@ -1006,7 +1008,7 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
     if (st != MOE_OK) return st;
     if (p->T > kFewTokens || p->identity) return MOE_E_UNSUPPORTED;
     const size_t T = p->T, H = p->H, I = p->I, Tk = T * p->k, rows = Tk + (p->shared ? T : 0);
-    static_assert((kFewCounters + kFewMaxSplitCols) * kFewCounterInts * 4 <= MOE_FEW_COUNTER_BYTES,
+    static_assert((kFewCounters + kFewMaxSplitTiles) * kFewCounterInts * 4 <= MOE_FEW_COUNTER_BYTES,
                   "the counters fit their block");
     size_t o = MOE_FEW_COUNTER_BYTES;  // the counters, zero between calls
     f->counter = 0;
@@ -1029,8 +1031,10 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
         f->hq = take(Tk * I);
         f->hs = take(Tk * (size_t)mx_groups(I) * 4);
     }
-    f->total = o;
     f->max_act = std::min(p->E, (int)Tk) + (p->shared ? 1 : 0);
+    f->gu_splits = few_gate_up_splits((int64_t)f->max_act * (I / 32), (int)H * (p->mx && !p->shared ? 1 : 2));
+    f->gu_part = f->gu_splits > 1 ? take(rows * (I / 32) * f->gu_splits * 64 * 4) : 0;
+    f->total = o;
     return MOE_OK;
 }
 
@@ -1074,7 +1078,7 @@ moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uin
     g.T = p.T; g.H = p.H; g.I = p.I; g.E = p.E;
     g.n_act = r.n_act; g.act_e = r.act_e; g.act_off = r.act_off; g.row_token = r.row_token; g.row_w = r.row_w;
     g.slot_row = r.slot_row;
-    g.col_count = r.counter + kFewCounters * kFewCounterInts;
+    g.tile_count = r.counter + kFewCounters * kFewCounterInts;
     g.x = x; g.w1 = (const uint16_t*)(pk + p.pk_w1t); g.w2 = (const uint16_t*)(pk + p.pk_w2t);
     g.h = (uint16_t*)(b + f.h); g.y = (float*)(b + f.y);
     if (p.mx) {
@@ -1083,6 +1087,8 @@ moe_status moe_layer_fwd_few(const moe_cfg* cfg, const moe_weights* w, const uin
         g.w1q = pk + p.pk_w1q; g.s1 = pk + p.pk_s1; g.w2q = pk + p.pk_w2q; g.s2 = pk + p.pk_s2;
         g.hq = b + f.hq; g.hs = b + f.hs;
     }
+    g.gu_splits = f.gu_splits;
+    g.gu_part = (float*)(b + f.gu_part);
     TIMED(MOE_K_GEMM_GATE_UP, s, launch_few_gate_up(g, f.max_act, s));
     if (p.T <= 16) {  // the down product and the weighted sum in one launch
         const int splits = few_down16_splits(p.H, (int64_t)f.max_act * 16 * p.I * (p.mx ? 1 : 2) / 1024);

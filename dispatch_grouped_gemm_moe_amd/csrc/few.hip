@@ -429,7 +429,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void* p, uint32
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
 }
 
-// Fragments of step c of rows of kb bytes: zeros past the row's end, which for
+// Fragments of step c of rows up to byte kb: zeros past it, a row's end, which for
 // MXFP8 rows of an odd multiple of 64 columns is in the middle of a line.  (The
 // scalar offset counts against the buffer's size, so it is zero there too.)
 template <bool MX, int N>
@@ -514,15 +514,15 @@ __device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<
 }
 
 // acc[i][m] (+)= weight rows 16 i .. of the tile times token rows 16 m .., over
-// the steps wave, wave + 4, ... of the rows' kb bytes.  The weights of one step
-// are in flight while the step before is multiplied; the tokens, which come
+// the steps c0 + wave, c0 + wave + 4, ... of the rows' kb bytes up to byte `end`.
+// The weights of one step are in flight while the step before is multiplied; the tokens, which come
 // from the L2, are loaded in their own step, ahead of the next weights, so that
 // waiting for them (loads return in order) leaves those in flight.  Steps past
 // the end load zeros, so the loop has one exit and keeps its registers.
 template <bool MX, int MT, bool kWiden>
-__device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperand& xo, int kb, int wave, int lane,
-                                           const uint32_t (&xrow)[MT], const uint32_t (&xsoff)[MT],
-                                           floatx4 (&acc)[4][MT]) {
+__device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperand& xo, int kb, int c0, int end,
+                                           int wave, int lane, const uint32_t (&xrow)[MT],
+                                           const uint32_t (&xsoff)[MT], floatx4 (&acc)[4][MT]) {
     const uint32_t lo = (uint32_t)(lane >> 4) * 16;
     uint32_t woff[4], wsoff[4], xoff[MT];
 #pragma unroll
@@ -535,14 +535,14 @@ __device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperan
     FewFrag<MX, 4> w0, w1;
     FewFrag<MX, MT> x;
     auto step = [&](int c, const FewFrag<MX, 4>& w, FewFrag<MX, 4>& next) {
-        few_load<MX, MT>(xo, kb, c, xoff, xsoff, x);
-        few_load<MX, 4>(wo, kb, c + kFgWaves, woff, wsoff, next);
+        few_load<MX, MT>(xo, end, c, xoff, xsoff, x);
+        few_load<MX, 4>(wo, end, c + kFgWaves, woff, wsoff, next);
         __builtin_amdgcn_sched_barrier(0);
         few_mfma<MX, MT, kWiden>(w, x, lane, acc);
         __builtin_amdgcn_sched_barrier(0);
     };
-    few_load<MX, 4>(wo, kb, wave, woff, wsoff, w0);
-    for (int c = wave; c * kFgChunk < kb; c += 2 * kFgWaves) {
+    few_load<MX, 4>(wo, end, c0 + wave, woff, wsoff, w0);
+    for (int c = c0 + wave; c * kFgChunk < end; c += 2 * kFgWaves) {
         step(c, w0, w1);
         step(c + kFgWaves, w1, w0);
     }
@@ -558,7 +558,8 @@ __device__ __forceinline__ void few_stage(const floatx4 (&acc)[4][MT], int m, in
 }
 
 template <bool MX, int MT>
-__device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
+__device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int row0, int rows, int z, int counter,
+                                            float* s_part) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int H = a.H, I = a.I;
@@ -591,10 +592,38 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT, true>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
+    const int lines = ((int)kb + kFgChunk - 1) / kFgChunk, splits = a.gu_splits;
+    const int end = z + 1 == splits ? (int)kb : lines * (z + 1) / splits * kFgChunk;
+    few_stream<MX, MT, true>(wo, xo, (int)kb, lines * z / splits, end, wave, lane, xrow, xsrow, acc);
     // thread (tokens tid / 32, + 8; column tid % 32): the tile's rows are 32 gate
     // columns and the 32 up columns of the same indices
     const int col = tid & 31;
+    auto finish = [&](int r, float g, float u) {
+        const float h = g / (1.0f + expf(-g)) * u;
+        if (MX) {  // the 32 columns of a token are one MXFP8 block, held by half a wave
+            float am = fabsf(h);
+#pragma unroll
+            for (int s = 16; s >= 1; s >>= 1) am = fmaxf(am, __shfl_xor(am, s, kWave));
+            const int ex = mx_scale_exp(am);
+            const uint32_t code = fp8x4(ldexpf(h, -ex), 0.0f, 0.0f, 0.0f);
+            if (r < rows) {
+                a.hq[(size_t)(row0 + r) * I + n * 32 + col] = (uint8_t)code;
+                if (col == 0) {  // a row's scale dwords are adjacent; the last group's spare bytes are zero
+                    uint8_t* d = a.hs + (size_t)(row0 + r) * mx_groups(I) * 4 + n;
+                    d[0] = (uint8_t)(ex + 127);
+                    if (n + 1 == I / 32)
+                        for (int s = 1; (n + s) & 3; ++s) d[s] = 0;
+                }
+            }
+        } else if (r < rows) {
+            // bf16, as the layer forward keeps h: an operand of the next MFMA.  In
+            // two bf16 parts the layer's error would be 2^-8.5 rather than 2^-8 of
+            // its output, for 2 us of 29 (one token, H 2048) and 25 of 536 (64, H 7168).
+            a.h[(size_t)(row0 + r) * I + n * 32 + col] = f32_to_bf16_rne(h);
+        }
+    };
+    // the parts' sums of row r: [row][tile of 32 columns][part][64]
+    auto part = [&](int r) { return a.gu_part + ((size_t)(row0 + r) * (I / 32) + n) * splits * kFgRows + col; };
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         if (m * 16 >= rows) break;
@@ -608,30 +637,25 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
                 g += s_part[(w * 16 + tt) * kFgLd + col];
                 u += s_part[(w * 16 + tt) * kFgLd + 32 + col];
             }
-            const float h = g / (1.0f + expf(-g)) * u;
             const int r = m * 16 + tt;
-            if (MX) {  // the 32 columns of a token are one MXFP8 block, held by half a wave
-                float am = fabsf(h);
-#pragma unroll
-                for (int s = 16; s >= 1; s >>= 1) am = fmaxf(am, __shfl_xor(am, s, kWave));
-                const int ex = mx_scale_exp(am);
-                const uint32_t code = fp8x4(ldexpf(h, -ex), 0.0f, 0.0f, 0.0f);
-                if (r < rows) {
-                    a.hq[(size_t)(row0 + r) * I + n * 32 + col] = (uint8_t)code;
-                    if (col == 0) {  // a row's scale dwords are adjacent; the last group's spare bytes are zero
-                        uint8_t* d = a.hs + (size_t)(row0 + r) * mx_groups(I) * 4 + n;
-                        d[0] = (uint8_t)(ex + 127);
-                        if (n + 1 == I / 32)
-                            for (int z = 1; (n + z) & 3; ++z) d[z] = 0;
-                    }
-                }
+            if (splits == 1) {
+                finish(r, g, u);
             } else if (r < rows) {
-                // bf16, as the layer forward keeps h: an operand of the next MFMA.  In
-                // two bf16 parts the layer's error would be 2^-8.5 rather than 2^-8 of
-                // its output, for 2 us of 29 (one token, H 2048) and 25 of 536 (64, H 7168).
-                a.h[(size_t)(row0 + r) * I + n * 32 + col] = f32_to_bf16_rne(h);
+                int* d = (int*)part(r) + z * kFgRows;
+                agent_store(d, __builtin_bit_cast(int, g));
+                agent_store(d + 32, __builtin_bit_cast(int, u));
             }
         }
+    }
+    if (splits == 1 || !counts_in_last(a.tile_count + counter * kFewCounterInts, splits, (int*)s_part)) return;
+    for (int r = tid >> 5; r < ((rows + 1) & ~1); r += kFgThreads / 32) {  // whole waves
+        const int* q = (const int*)part(min(r, rows - 1));
+        float g = 0.0f, u = 0.0f;
+        for (int s = 0; s < splits; ++s) {
+            g += __builtin_bit_cast(float, agent_load(q + s * kFgRows));
+            u += __builtin_bit_cast(float, agent_load(q + s * kFgRows + 32));
+        }
+        finish(r, g, u);
     }
 }
 
@@ -669,7 +693,7 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT, false>(wo, xo, (int)kb, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT, false>(wo, xo, (int)kb, 0, (int)kb, wave, lane, xrow, xsrow, acc);
     const int col = (tid & 31) * 2;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -696,18 +720,20 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
 }
 
 template <bool kDown, bool MX, int MT>
-__device__ __forceinline__ void few_tile(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
+__device__ __forceinline__ void few_tile(const FewGemm& a, int e, int n, int row0, int rows, int z, int counter,
+                                         float* s_part) {
     if constexpr (kDown) few_down<MX, MT>(a, e, n, row0, rows, s_part);
-    else few_gate_up<MX, MT>(a, e, n, row0, rows, s_part);
+    else few_gate_up<MX, MT>(a, e, n, row0, rows, z, counter, s_part);
 }
 
 // The tile's code by the 16-row fragments that the expert's rows fill (three
 // run as four, the rows past the last repeating it).
 template <bool kDown, bool MX, int kMost>
-__device__ __forceinline__ void few_tile_rows(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
-    if (kMost == 1 || rows <= 16) few_tile<kDown, MX, 1>(a, e, n, row0, rows, s_part);
-    else if (kMost == 2 || rows <= 32) few_tile<kDown, MX, 2>(a, e, n, row0, rows, s_part);
-    else few_tile<kDown, MX, 4>(a, e, n, row0, rows, s_part);
+__device__ __forceinline__ void few_tile_rows(const FewGemm& a, int e, int n, int row0, int rows, int z, int counter,
+                                              float* s_part) {
+    if (kMost == 1 || rows <= 16) few_tile<kDown, MX, 1>(a, e, n, row0, rows, z, counter, s_part);
+    else if (kMost == 2 || rows <= 32) few_tile<kDown, MX, 2>(a, e, n, row0, rows, z, counter, s_part);
+    else few_tile<kDown, MX, 4>(a, e, n, row0, rows, z, counter, s_part);
 }
 
 // Workgroup b: active expert b / n_tiles, weight rows 64 (b % n_tiles) .. + 63.
@@ -720,18 +746,19 @@ __global__ __launch_bounds__(kFgThreads, kMost == 1 ? 1 : (kMost == 4 ? 2 : (kMx
     FewGemm a) {
     __shared__ __attribute__((aligned(16))) float s_part[kFgWaves * 16 * kFgLd];
     const int nt = kDown ? a.H / kFgRows : a.I / 32;
-    const int i = blockIdx.x / nt, n = blockIdx.x - i * nt;
+    const int t = kDown ? blockIdx.x : blockIdx.x / a.gu_splits, z = kDown ? 0 : blockIdx.x - t * a.gu_splits;
+    const int i = t / nt, n = t - i * nt;
     // the lists hold an entry for every expert of the grid
     const int n_act = ld_layout(a.n_act), e = ld_layout(a.act_e + i), row0 = ld_layout(a.act_off + i);
     const int rows = ld_layout(a.act_off + i + 1) - row0;
     if (i >= n_act) return;
-    if (kMx && e < a.E) few_tile_rows<kDown, true, kMost>(a, e, n, row0, rows, s_part);
-    else few_tile_rows<kDown, false, kMost>(a, e, n, row0, rows, s_part);
+    if (kMx && e < a.E) few_tile_rows<kDown, true, kMost>(a, e, n, row0, rows, z, t, s_part);
+    else few_tile_rows<kDown, false, kMost>(a, e, n, row0, rows, z, t, s_part);
 }
 
 template <bool kDown>
 static void launch_few_gemm(const FewGemm& a, int max_act, hipStream_t stream) {
-    const dim3 grid((unsigned)max_act * (unsigned)(kDown ? a.H / kFgRows : a.I / 32)), block(kFgThreads);
+    const dim3 grid((unsigned)max_act * (unsigned)(kDown ? a.H / kFgRows : a.I / 32 * a.gu_splits)), block(kFgThreads);
     const int mt = ceil_div(a.T, 16);  // an expert has at most T rows
 #define FEW_LAUNCH(MX, MT) hipLaunchKernelGGL((few_gemm_kernel<kDown, MX, MT>), grid, block, 0, stream, a)
     if (mt > 2) {
@@ -745,6 +772,17 @@ static void launch_few_gemm(const FewGemm& a, int max_act, hipStream_t stream) {
         else FEW_LAUNCH(false, 1);
     }
 #undef FEW_LAUNCH
+}
+
+int few_gate_up_splits(int64_t tiles, int row_bytes) {
+    // As many workgroups as CUs, each wave with about three steps at least: a wave
+    // that is alone on its SIMD takes 1.2 us a step.  16 tiles over bf16 rows of H
+    // 6784: 29.4 us whole, 10.4 us in eight; 6 over MXFP8 rows of H 6400: 17.3 and
+    // 9.7 us in four; 12 over MXFP8 rows of H 2944 stay whole (9.7 us, of which
+    // the join would be 3 again).
+    const int64_t by_cus = 256 / tiles, by_work = row_bytes / (3 * kFgWaves * kFgChunk);
+    const int64_t z = by_work < by_cus ? by_work : by_cus;
+    return z < 1 ? 1 : (z > kFewMaxSplits ? kFewMaxSplits : (int)z);
 }
 
 void launch_few_gate_up(const FewGemm& a, int max_act, hipStream_t s) { launch_few_gemm<false>(a, max_act, s); }
@@ -990,7 +1028,7 @@ __global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int m
                                (uint64_t)__builtin_bit_cast(uint32_t, s0) |
                                    (uint64_t)__builtin_bit_cast(uint32_t, s1) << 32,
                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (!counts_in_last(a.col_count + n * kFewCounterInts, splits, &s_flag)) return;
+        if (!counts_in_last(a.tile_count + n * kFewCounterInts, splits, &s_flag)) return;
         s0 = s1 = 0.0f;
         if (tok < a.T)
             for (int z = 0; z < splits; ++z) {
@@ -1011,7 +1049,7 @@ int few_down16_splits(int H, int64_t column_kb) {
     // KB (9.0 us whole) stay whole: each part reads the row lists anew and the last
     // to finish reads every part's sums.
     const int n = H / kFdCols;
-    static_assert(256 / (kFewMaxSplitCols + 1) < 2, "a counter for every column block that is split");
+    static_assert(256 / (kFewMaxSplitTiles + 1) < 2, "a counter for every column block that is split");
     const int64_t by_work = column_kb / 100, by_cus = 256 / n;
     const int64_t z = by_work < by_cus ? by_work : by_cus;
     return z < 1 ? 1 : (z > kFewMaxSplits ? kFewMaxSplits : (int)z);

@@ -340,13 +340,14 @@ constexpr int kFewTokens = 64;  // most tokens of one call: an expert's tokens a
 // expert; the shared expert's T rows come last.
 //
 // Counters, a cache line each: for the token groups, each group's expert groups
-// and each of those's residue groups (kFewCounters), and for the column blocks
-// of a split down product.  (Adjacent they delay each other: the router of 64
+// and each of those's residue groups (kFewCounters), and for the tiles or column
+// blocks of a split product.  (Adjacent they delay each other: the router of 64
 // tokens took 16.6 us instead of 14.7, 7 tokens over 256 experts 55.1 us a call
 // instead of 53.8.)
 constexpr int kFewCounterInts = 32;
 constexpr int kFewCounters = 1 + (kFewTokens / 4) * (1 + kMaxExperts / 32);
-constexpr int kFewMaxSplitCols = 128;
+constexpr int kFewMaxSplitTiles = 128;  // a product in more column blocks or tiles is not split
+constexpr int kFewMaxSplits = 8;
 struct FewRoute {
     const uint16_t* x;   // [T][H]
     const float* Wr;     // [H][E]
@@ -385,13 +386,16 @@ struct FewGemm {
     uint8_t* hq;                       // [rows][I]
     uint8_t* hs;                       // [rows][mx_groups(I)][4]
     float* y;                          // [rows][H] weighted expert outputs; launch_few_down16: [H/16][splits][T][16]
-    int* col_count;                    // column blocks' counters, zero between calls
+    int* tile_count;                   // counters of the tiles or column blocks of a split product
+    int gu_splits;                     // parts of H in the gate|up product, 1: whole
+    float* gu_part;                    // their sums [rows][I/32][gu_splits][64]
 };
+// parts for a gate|up product of at most `tiles` tiles and token rows of row_bytes
+int few_gate_up_splits(int64_t tiles, int row_bytes);
 void launch_few_gate_up(const FewGemm& a, int max_act, hipStream_t stream);
 void launch_few_down(const FewGemm& a, int max_act, hipStream_t stream);
 // up to 16 tokens: the down product with the weighted sum; column_kb: what the
 // weight rows of 16 output columns come to over the active experts
-constexpr int kFewMaxSplits = 8;
 int few_down16_splits(int H, int64_t column_kb);
 void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, int splits, uint16_t* out,
                        hipStream_t stream);
