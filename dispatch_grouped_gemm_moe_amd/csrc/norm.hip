@@ -37,17 +37,19 @@ __device__ __forceinline__ intx4 pack8(const float (&v)[8]) {
     return o;
 }
 
+// Sum over the kLanes lanes of a row's group.
+template <int kLanes = kWave>
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+    for (int s = kLanes / 2; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
     return v;
 }
 
 // Sum over the workgroup (kWaves waves), the same in every thread and in the
 // same order on every call.
-template <int kWaves>
+template <int kWaves, int kLanes>
 __device__ __forceinline__ float group_sum(float v, float* s_sum) {
-    v = wave_sum(v);
+    v = wave_sum<kLanes>(v);
     if constexpr (kWaves == 1) return v;
     if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = v;
     lds_barrier();  // the stores in flight need not have ended
@@ -72,14 +74,15 @@ __device__ __forceinline__ uint64_t block_codes(const float (&v)[8], uint8_t& sc
     return (uint64_t)lo | ((uint64_t)hi << 32);
 }
 
-// A row per group of kWaves waves, kNV vectors per thread; kPer rows of a
-// workgroup side by side (kWaves = 1).
-template <int kWaves, int kNV, int kPer>
-__global__ __launch_bounds__(kWaves * kWave * kPer) void norm_fwd_kernel(NormFwd a) {
+// A row per group of kWaves waves, kNV vectors per thread, or (kWaves = 1) of
+// kLanes lanes, 256 / kLanes rows in a workgroup: 262144 rows of 128 take 42 us
+// (6.4 TB/s) with 16 lanes a row and 92 us with 64.
+template <int kWaves, int kNV, int kLanes>
+__global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_fwd_kernel(NormFwd a) {
     __shared__ float s_sum[kWaves];
-    const int lid = kPer == 1 ? threadIdx.x : threadIdx.x & 63;
-    const int64_t r = kPer == 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kPer + (threadIdx.x >> 6);
-    if (kPer > 1 && r >= a.rows) return;  // whole waves; no barrier follows
+    const int lid = kWaves > 1 ? threadIdx.x : threadIdx.x % kLanes;
+    const int64_t r = kWaves > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    if (kWaves == 1 && r >= a.rows) return;  // whole rows; no barrier follows
     const int nv = a.cols / kNormVec;
     const int64_t base = r * a.cols;
     float v[kNV][8];
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(kWaves * kWave * kPer) void norm_fwd_kernel(NormFwd
 #pragma unroll
         for (int c = 0; c < 8; ++c) ss = __builtin_fmaf(v[i][c], v[i][c], ss);
     }
-    const float rstd = 1.0f / sqrtf(group_sum<kWaves>(ss, s_sum) / (float)a.cols + a.eps);
+    const float rstd = 1.0f / sqrtf(group_sum<kWaves, kLanes>(ss, s_sum) / (float)a.cols + a.eps);
     if (a.rstd && lid == 0) a.rstd[r] = rstd;
     const int nb = a.cols / 32;
 #pragma unroll
@@ -132,16 +135,20 @@ __global__ __launch_bounds__(kWaves * kWave * kPer) void norm_fwd_kernel(NormFwd
 
 void launch_norm_fwd(const NormFwd& a, hipStream_t stream) {
     const int nv = a.cols / kNormVec;
-#define NORM_FWD(W, NV, PER)                                                                                       \
-    hipLaunchKernelGGL((norm_fwd_kernel<W, NV, PER>), dim3((unsigned)((a.rows + PER - 1) / PER)), dim3(W * kWave * PER), \
-                       0, stream, a)
-    if (nv <= 64) NORM_FWD(1, 1, 4);
-    else if (nv <= 128) NORM_FWD(1, 2, 4);
-    else if (nv <= 256) NORM_FWD(2, 2, 1);
-    else if (nv <= 512) NORM_FWD(4, 2, 1);
-    else if (nv <= 1024) NORM_FWD(8, 2, 1);
-    else if (nv <= 2048) NORM_FWD(16, 2, 1);
-    else NORM_FWD(16, 4, 1);
+#define NORM_FWD(W, NV, LANES)                                                                            \
+    hipLaunchKernelGGL((norm_fwd_kernel<W, NV, LANES>),                                                   \
+                       dim3((unsigned)(W > 1 ? a.rows : (a.rows + 256 / LANES - 1) / (256 / LANES))),     \
+                       dim3(W > 1 ? W * kWave : 256), 0, stream, a)
+    if (nv <= 8) NORM_FWD(1, 1, 8);
+    else if (nv <= 16) NORM_FWD(1, 1, 16);
+    else if (nv <= 32) NORM_FWD(1, 1, 32);
+    else if (nv <= 64) NORM_FWD(1, 1, 64);
+    else if (nv <= 128) NORM_FWD(1, 2, 64);
+    else if (nv <= 256) NORM_FWD(2, 2, 64);
+    else if (nv <= 512) NORM_FWD(4, 2, 64);
+    else if (nv <= 1024) NORM_FWD(8, 2, 64);
+    else if (nv <= 2048) NORM_FWD(16, 2, 64);
+    else NORM_FWD(16, 4, 64);
 #undef NORM_FWD
 }
 
@@ -149,10 +156,19 @@ void launch_norm_fwd(const NormFwd& a, hipStream_t stream) {
 // Backward
 // ---------------------------------------------------------------------------
 
-constexpr int kNormParts = 512;  // most partial sums of dw
+constexpr int kNormParts = 512;   // most partial sums of dw
+constexpr int kNarrowVecs = 128;  // vectors of a row that one wave holds, up to two a lane
+
+// Lanes of a row where one wave holds it, of a 256-thread workgroup's rows; 0 for
+// wider rows, a workgroup each.
+static int narrow_lanes(int cols) {
+    const int nv = cols / kNormVec;
+    return nv <= 8 ? 8 : nv <= 16 ? 16 : nv <= 32 ? 32 : nv <= kNarrowVecs ? 64 : 0;
+}
 
 int norm_bwd_parts(int64_t rows, int cols) {
-    (void)cols;
+    const int lanes = narrow_lanes(cols);
+    if (lanes) rows = (rows + 256 / lanes - 1) / (256 / lanes);
     return (int)(rows < kNormParts ? rows : kNormParts);
 }
 
@@ -163,6 +179,23 @@ struct NormVec {
     uint64_t q;
     int e;
 };
+
+// Its s.
+template <bool kCk>
+__device__ __forceinline__ void norm_values(const NormVec<kCk>& v, float (&s)[8]) {
+    if constexpr (kCk) {
+        const int e = v.e - 127;
+        const uint32_t lo = (uint32_t)v.q, hi = (uint32_t)(v.q >> 32);
+        s[0] = __builtin_amdgcn_cvt_f32_fp8(lo, 0); s[1] = __builtin_amdgcn_cvt_f32_fp8(lo, 1);
+        s[2] = __builtin_amdgcn_cvt_f32_fp8(lo, 2); s[3] = __builtin_amdgcn_cvt_f32_fp8(lo, 3);
+        s[4] = __builtin_amdgcn_cvt_f32_fp8(hi, 0); s[5] = __builtin_amdgcn_cvt_f32_fp8(hi, 1);
+        s[6] = __builtin_amdgcn_cvt_f32_fp8(hi, 2); s[7] = __builtin_amdgcn_cvt_f32_fp8(hi, 3);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[c] = ldexpf(s[c], e);
+    } else {
+        unpack8(v.s, s);
+    }
+}
 
 // Workgroup b takes rows b, b + parts, ...; dw's partial sums stay in
 // registers over them.  Up to four vectors a thread, the next row is asked for
@@ -217,18 +250,7 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) 
             const bool in = lid + i * (int)blockDim.x < nv;
             NormVec<kCk>& v = t[kAhead ? i : 0];
             if constexpr (!kAhead) load(r, i, v);
-            if constexpr (kCk) {
-                const int e = v.e - 127;
-                const uint32_t lo = (uint32_t)v.q, hi = (uint32_t)(v.q >> 32);
-                xh[i][0] = __builtin_amdgcn_cvt_f32_fp8(lo, 0); xh[i][1] = __builtin_amdgcn_cvt_f32_fp8(lo, 1);
-                xh[i][2] = __builtin_amdgcn_cvt_f32_fp8(lo, 2); xh[i][3] = __builtin_amdgcn_cvt_f32_fp8(lo, 3);
-                xh[i][4] = __builtin_amdgcn_cvt_f32_fp8(hi, 0); xh[i][5] = __builtin_amdgcn_cvt_f32_fp8(hi, 1);
-                xh[i][6] = __builtin_amdgcn_cvt_f32_fp8(hi, 2); xh[i][7] = __builtin_amdgcn_cvt_f32_fp8(hi, 3);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) xh[i][c] = ldexpf(xh[i][c], e);
-            } else {
-                unpack8(v.s, xh[i]);
-            }
+            norm_values<kCk>(v, xh[i]);
             unpack8(v.dy, gy[i]);
             if constexpr (kAhead) unpack8(ds[i], dv[i]);
             const float* wp = a.weight + vec_of(i) * kNormVec;  // cached
@@ -281,6 +303,100 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) 
     }
 }
 
+// The same for rows that one wave holds: kLanes lanes a row, 256 / kLanes rows of
+// a workgroup side by side, so that narrow rows (a head's) fill their lanes and
+// no barrier stands in the loop.  The rows' sums of dw meet in LDS at the end.
+// Against a workgroup a row: 262144 rows of 128 377 -> 47 us (5.7 TB/s), 65536 of
+// 512 103 -> 45 us, 16384 of 1024 37 -> 26 us.  Rows of 2048 would need four
+// vectors a lane and 256 registers: 4096 of them from the checkpoint take 21 us
+// that way and 18 us with a workgroup each.
+template <int kLanes, int kNV, bool kCk>
+__global__ __launch_bounds__(256) void norm_bwd_narrow_kernel(NormBwd a) {
+    constexpr int kRows = 256 / kLanes;
+    __shared__ float s_dw[kRows][kLanes * kNV * kNormVec];
+    const int lid = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+    const int nv = a.cols / kNormVec, nb = a.cols / 32;
+    auto vec_of = [&](int i) { return min(lid + i * kLanes, nv - 1); };
+    NormVec<kCk> t[kNV];
+    intx4 ds[kNV];
+    float rstd;
+    auto load = [&](int64_t r) {
+        rstd = a.rstd[r];
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const int p = vec_of(i);
+            const int64_t at = r * a.cols + p * kNormVec;
+            t[i].dy = *(const intx4*)(a.dy + at);
+            if constexpr (kCk) {
+                t[i].q = *(const uint64_t*)(a.ckq + at);
+                t[i].e = a.cks[r * nb + (p >> 2)];
+            } else {
+                t[i].s = *(const intx4*)(a.summed + at);
+            }
+            ds[i] = a.dsum ? *(const intx4*)(a.dsum + at) : intx4{0, 0, 0, 0};
+        }
+    };
+    float dw[kNV][8], w[kNV][8];
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        const float* wp = a.weight + vec_of(i) * kNormVec;
+        const floatx4 w0 = *(const floatx4*)wp, w1 = *(const floatx4*)(wp + 4);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            dw[i][c] = 0.0f;
+            w[i][c] = c < 4 ? w0[c] : w1[c - 4];
+        }
+    }
+    const int64_t first = (int64_t)blockIdx.x * kRows + row, stride = (int64_t)gridDim.x * kRows;
+    load(min(first, a.rows - 1));
+    for (int64_t r = first; r < a.rows; r += stride) {
+        float xh[kNV][8], gy[kNV][8], dv[kNV][8];
+        const float rs = rstd;
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            norm_values<kCk>(t[i], xh[i]);
+            unpack8(t[i].dy, gy[i]);
+            unpack8(ds[i], dv[i]);
+            const bool in = lid + i * kLanes < nv;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                xh[i][c] *= rs;
+                dw[i][c] = __builtin_fmaf(gy[i][c], xh[i][c], dw[i][c]);
+                gy[i][c] *= w[i][c];
+                if (in) dot = __builtin_fmaf(gy[i][c], xh[i][c], dot);
+            }
+        }
+        load(min(r + stride, a.rows - 1));
+        const float mean = wave_sum<kLanes>(dot) / (float)a.cols;
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const int p = lid + i * kLanes;
+            float d[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d[c] = rs * (gy[i][c] - xh[i][c] * mean) + dv[i][c];
+            if (p < nv) *(intx4*)(a.dx + r * a.cols + p * kNormVec) = pack8(d);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        floatx4* d = (floatx4*)&s_dw[row][(lid + i * kLanes) * kNormVec];
+        d[0] = floatx4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        d[1] = floatx4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+        float v[kRows];
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) v[g] = s_dw[g][c];
+#pragma unroll
+        for (int n = kRows / 2; n >= 1; n >>= 1)
+#pragma unroll
+            for (int g = 0; g < n; ++g) v[g] += v[g + n];
+        a.partial[(int64_t)blockIdx.x * a.cols + c] = v[0];
+    }
+}
+
 // dw[c] = the partial sums in a fixed order: 32 columns per workgroup, thread
 // (group, column quad) sums every 128th part, then a tree over the groups.
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* partial, int parts, int cols, float* dw) {
@@ -309,12 +425,25 @@ void launch_norm_bwd(const NormBwd& a, hipStream_t stream) {
         else                                                                                                     \
             hipLaunchKernelGGL((norm_bwd_kernel<MAX, NV, false>), dim3(parts), block, 0, stream, a);             \
     } while (0)
+#define NORM_BWD_NARROW(LANES, NV)                                                                               \
+    do {                                                                                                         \
+        if (a.ckq)                                                                                               \
+            hipLaunchKernelGGL((norm_bwd_narrow_kernel<LANES, NV, true>), dim3(parts), dim3(256), 0, stream, a); \
+        else                                                                                                     \
+            hipLaunchKernelGGL((norm_bwd_narrow_kernel<LANES, NV, false>), dim3(parts), dim3(256), 0, stream, a); \
+    } while (0)
     // up to eight waves a row: a compiler bound of more would spill the row
-    if (nv <= 512) NORM_BWD(8, 1);
+    if (nv <= 8) NORM_BWD_NARROW(8, 1);
+    else if (nv <= 16) NORM_BWD_NARROW(16, 1);
+    else if (nv <= 32) NORM_BWD_NARROW(32, 1);
+    else if (nv <= 64) NORM_BWD_NARROW(64, 1);
+    else if (nv <= kNarrowVecs) NORM_BWD_NARROW(64, 2);
+    else if (nv <= 512) NORM_BWD(8, 1);
     else if (nv <= 1024) NORM_BWD(8, 2);
     else if (nv <= 2048) NORM_BWD(8, 4);
     else NORM_BWD(8, 8);
 #undef NORM_BWD
+#undef NORM_BWD_NARROW
     hipLaunchKernelGGL(norm_dw_kernel, dim3(a.cols / 32), dim3(1024), 0, stream, a.partial, parts, a.cols, a.dw);
 }
 

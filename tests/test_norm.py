@@ -95,7 +95,7 @@ def test_norm_binding_refuses_tensors_the_kernels_cannot_read():
 
 # ------------------------------------------------------------------ GPU
 
-COLS = [32, 64, 96, 512, 544, 1024, 1056, 2080, 4096, 4128, 7168, 8192, 8224, 16384, 32768]
+COLS = [32, 64, 96, 128, 224, 512, 544, 1024, 1056, 2080, 4096, 4128, 7168, 8192, 8224, 16384, 32768]
 
 
 def _rand(g, *shape, sigma=1.0, dtype=torch.bfloat16):
@@ -236,6 +236,13 @@ def test_norm_backward(gpu_lib, rows, cols):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(20000, 64), (9001, 128), (9000, 224), (4001, 512), (2100, 992)])
+def test_norm_backward_of_many_narrow_rows(gpu_lib, rows, cols):
+    # a workgroup takes several rows at once, several times
+    test_norm_backward(gpu_lib, rows, cols)
+
+
+@pytest.mark.gpu
 def test_norm_backward_against_differences(gpu_lib):
     """The kernel's gradients against central differences of the forward in 64 bits, along random
     directions.  The forward is smooth: with a step of 1e-5 the difference quotient is off by under
@@ -264,8 +271,8 @@ def test_norm_backward_against_differences(gpu_lib):
 
 
 @pytest.mark.gpu
-def test_norm_backward_in_place(gpu_lib):
-    rows, cols = 33, 4128
+@pytest.mark.parametrize("rows,cols", [(33, 4128), (9000, 96), (2500, 800)])
+def test_norm_backward_in_place(gpu_lib, rows, cols):
     g, x, r, w = _norm_inputs(rows, cols, 8)
     o = _forward(x, w, r)
     dy, ds = _rand(g, rows, cols), _rand(g, rows, cols)
