@@ -159,6 +159,9 @@ void launch_norm_fwd(const NormFwd& a, hipStream_t stream) {
 constexpr int kNormParts = 512;   // most partial sums of dw
 constexpr int kNarrowVecs = 128;  // vectors of a row that one wave holds, up to two a lane
 
+constexpr int kBwdWaves = 8;      // most waves that hold a row and ask for the next
+constexpr int kWideWaves = 16;    // waves of a row past what those hold
+
 // Lanes of a row where one wave holds it, of a 256-thread workgroup's rows; 0 for
 // wider rows, a workgroup each.
 static int narrow_lanes(int cols) {
@@ -198,15 +201,13 @@ __device__ __forceinline__ void norm_values(const NormVec<kCk>& v, float (&s)[8]
 }
 
 // Workgroup b takes rows b, b + parts, ...; dw's partial sums stay in
-// registers over them.  Up to four vectors a thread, the next row is asked for
-// before this one's sum is joined over the workgroup, so a row's loads (all of
-// them at once) have the barrier and the arithmetic of a row to arrive: 4096
-// rows of 2048 from the checkpoint 23.3 -> 16.2 us, 16384 of 7168 191 -> 179 us
-// (5.2 TB/s).
-template <int kMaxWaves, int kNV, bool kCk>
-__global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) {
-    constexpr bool kAhead = kNV <= 4;
-    __shared__ float s_sum[2][kMaxWaves];
+// registers over them.  The next row is asked for before this one's sum is joined
+// over the workgroup, so a row's loads (all of them at once) have the barrier and
+// the arithmetic of a row to arrive: 4096 rows of 2048 from the checkpoint 23.3 ->
+// 16.2 us, 16384 of 7168 191 -> 179 us (5.2 TB/s).
+template <int kNV, bool kCk>
+__global__ __launch_bounds__(kBwdWaves * kWave) void norm_bwd_kernel(NormBwd a) {
+    __shared__ float s_sum[2][kBwdWaves];
     const int lid = threadIdx.x, waves = blockDim.x / kWave;
     const int nv = a.cols / kNormVec, nb = a.cols / 32;
     float dw[kNV][8];
@@ -230,29 +231,25 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) 
     auto load_ds = [&](int64_t r, int i) {
         return a.dsum ? *(const intx4*)(a.dsum + r * a.cols + vec_of(i) * kNormVec) : intx4{0, 0, 0, 0};
     };
-    NormVec<kCk> t[kAhead ? kNV : 1];
-    intx4 ds[kAhead ? kNV : 1];
+    NormVec<kCk> t[kNV];
+    intx4 ds[kNV];
     float rstd = a.rstd[blockIdx.x];  // there are no more workgroups than rows
-    if constexpr (kAhead) {
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            load(blockIdx.x, i, t[i]);
-            ds[i] = load_ds(blockIdx.x, i);
-        }
+    for (int i = 0; i < kNV; ++i) {
+        load(blockIdx.x, i, t[i]);
+        ds[i] = load_ds(blockIdx.x, i);
     }
     int half = 0;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, half ^= 1) {
-        float xh[kNV][8], gy[kNV][8], dv[kAhead ? kNV : 1][8];
+        float xh[kNV][8], gy[kNV][8], dv[kNV][8];
         const float rs = rstd;
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             const bool in = lid + i * (int)blockDim.x < nv;
-            NormVec<kCk>& v = t[kAhead ? i : 0];
-            if constexpr (!kAhead) load(r, i, v);
-            norm_values<kCk>(v, xh[i]);
-            unpack8(v.dy, gy[i]);
-            if constexpr (kAhead) unpack8(ds[i], dv[i]);
+            norm_values<kCk>(t[i], xh[i]);
+            unpack8(t[i].dy, gy[i]);
+            unpack8(ds[i], dv[i]);
             const float* wp = a.weight + vec_of(i) * kNormVec;  // cached
             const floatx4 w0 = *(const floatx4*)wp, w1 = *(const floatx4*)(wp + 4);
 #pragma unroll
@@ -266,12 +263,10 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) 
         {
             const int64_t rn = r + gridDim.x < a.rows ? r + gridDim.x : r;
             rstd = a.rstd[rn];
-            if constexpr (kAhead) {
 #pragma unroll
-                for (int i = 0; i < kNV; ++i) {
-                    load(rn, i, t[i]);
-                    ds[i] = load_ds(rn, i);
-                }
+            for (int i = 0; i < kNV; ++i) {
+                load(rn, i, t[i]);
+                ds[i] = load_ds(rn, i);
             }
         }
         dot = wave_sum(dot);
@@ -286,10 +281,9 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) 
         for (int i = 0; i < kNV; ++i) {
             const int p = lid + i * (int)blockDim.x;
             if (p >= nv) continue;
-            if constexpr (!kAhead) unpack8(load_ds(r, i), dv[0]);
             float d[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) d[c] = rs * (gy[i][c] - xh[i][c] * mean) + dv[kAhead ? i : 0][c];
+            for (int c = 0; c < 8; ++c) d[c] = rs * (gy[i][c] - xh[i][c] * mean) + dv[i][c];
             *(intx4*)(a.dx + r * a.cols + p * kNormVec) = pack8(d);
         }
     }
@@ -297,6 +291,87 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void norm_bwd_kernel(NormBwd a) 
     for (int i = 0; i < kNV; ++i) {
         const int p = lid + i * (int)blockDim.x;
         if (p >= nv) continue;
+        float* d = a.partial + (int64_t)blockIdx.x * a.cols + p * kNormVec;
+        *(floatx4*)d = floatx4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        *(floatx4*)(d + 4) = floatx4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+    }
+}
+
+// The same for rows past 16384, sixteen waves and up to four vectors a lane: 128
+// registers a lane hold dw's sums but not the row, which is read again after its
+// sum (from the L2 or the cache behind it): 2048 rows of 32768 170 us (3.2 TB/s).
+// Eight waves of eight vectors that keep it spill, and so do sixteen of four:
+// 324 and 265 us.
+template <bool kCk>
+__global__ __launch_bounds__(kWideWaves * kWave) void norm_bwd_wide_kernel(NormBwd a) {
+    constexpr int kNV = 4, kThreads = kWideWaves * kWave;
+    __shared__ float s_sum[2][kWideWaves];
+    const int lid = threadIdx.x;
+    const int nv = a.cols / kNormVec, nb = a.cols / 32;
+    float dw[kNV][8];
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dw[i][c] = 0.0f;
+    // xhat, dy and the weights of vector p, an address of 32 bits from a scalar one
+    auto values = [&](int64_t r, uint32_t p, float rs, float (&xh)[8], float (&gy)[8], float (&w)[8]) {
+        const int64_t row = r * a.cols;
+        const uint32_t at = p * kNormVec;
+        NormVec<kCk> t;
+        t.dy = *(const intx4*)(a.dy + row + at);
+        if constexpr (kCk) {
+            t.q = *(const uint64_t*)(a.ckq + row + at);
+            t.e = (a.cks + r * nb)[p >> 2];
+        } else {
+            t.s = *(const intx4*)(a.summed + row + at);
+        }
+        const floatx4 w0 = *(const floatx4*)(a.weight + at), w1 = *(const floatx4*)(a.weight + at + 4);
+        norm_values<kCk>(t, xh);
+        unpack8(t.dy, gy);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            xh[c] *= rs;
+            w[c] = c < 4 ? w0[c] : w1[c - 4];
+        }
+    };
+    int half = 0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, half ^= 1) {
+        const float rs = a.rstd[r];
+        float dot = 0.0f, xh[8], gy[8], w[8];
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            const uint32_t p = lid + i * kThreads;
+            if ((int)p >= nv) break;
+            values(r, p, rs, xh, gy, w);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                dw[i][c] = __builtin_fmaf(gy[c], xh[c], dw[i][c]);
+                dot = __builtin_fmaf(gy[c] * w[c], xh[c], dot);
+            }
+        }
+        dot = wave_sum(dot);
+        if ((lid & 63) == 0) s_sum[half][lid >> 6] = dot;
+        asm volatile("" ::: "memory");  // read again, not kept
+        lds_barrier();
+        dot = s_sum[half][0];
+#pragma unroll
+        for (int v = 1; v < kWideWaves; ++v) dot += s_sum[half][v];
+        const float mean = dot / (float)a.cols;
+#pragma unroll 1
+        for (uint32_t p = lid; (int)p < nv; p += kThreads) {
+            const int64_t row = r * a.cols;
+            float d[8];
+            values(r, p, rs, xh, gy, w);
+            unpack8(a.dsum ? *(const intx4*)(a.dsum + row + p * kNormVec) : intx4{0, 0, 0, 0}, d);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d[c] = rs * (gy[c] * w[c] - xh[c] * mean) + d[c];
+            *(intx4*)(a.dx + row + p * kNormVec) = pack8(d);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+        const int p = lid + i * kThreads;
+        if (p >= nv) break;
         float* d = a.partial + (int64_t)blockIdx.x * a.cols + p * kNormVec;
         *(floatx4*)d = floatx4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
         *(floatx4*)(d + 4) = floatx4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
@@ -417,13 +492,13 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* partial, int
 void launch_norm_bwd(const NormBwd& a, hipStream_t stream) {
     const int nv = a.cols / kNormVec;
     const int parts = norm_bwd_parts(a.rows, a.cols);
-#define NORM_BWD(MAX, NV)                                                                                        \
+#define NORM_BWD(NV)                                                                                             \
     do {                                                                                                         \
         const dim3 block(ceil_div(ceil_div(nv, NV), kWave) * kWave);                                             \
         if (a.ckq)                                                                                               \
-            hipLaunchKernelGGL((norm_bwd_kernel<MAX, NV, true>), dim3(parts), block, 0, stream, a);              \
+            hipLaunchKernelGGL((norm_bwd_kernel<NV, true>), dim3(parts), block, 0, stream, a);              \
         else                                                                                                     \
-            hipLaunchKernelGGL((norm_bwd_kernel<MAX, NV, false>), dim3(parts), block, 0, stream, a);             \
+            hipLaunchKernelGGL((norm_bwd_kernel<NV, false>), dim3(parts), block, 0, stream, a);             \
     } while (0)
 #define NORM_BWD_NARROW(LANES, NV)                                                                               \
     do {                                                                                                         \
@@ -432,16 +507,18 @@ void launch_norm_bwd(const NormBwd& a, hipStream_t stream) {
         else                                                                                                     \
             hipLaunchKernelGGL((norm_bwd_narrow_kernel<LANES, NV, false>), dim3(parts), dim3(256), 0, stream, a); \
     } while (0)
-    // up to eight waves a row: a compiler bound of more would spill the row
     if (nv <= 8) NORM_BWD_NARROW(8, 1);
     else if (nv <= 16) NORM_BWD_NARROW(16, 1);
     else if (nv <= 32) NORM_BWD_NARROW(32, 1);
     else if (nv <= 64) NORM_BWD_NARROW(64, 1);
     else if (nv <= kNarrowVecs) NORM_BWD_NARROW(64, 2);
-    else if (nv <= 512) NORM_BWD(8, 1);
-    else if (nv <= 1024) NORM_BWD(8, 2);
-    else if (nv <= 2048) NORM_BWD(8, 4);
-    else NORM_BWD(8, 8);
+    else if (nv <= 512) NORM_BWD(1);
+    else if (nv <= 1024) NORM_BWD(2);
+    else if (nv <= 2048) NORM_BWD(4);
+    else if (a.ckq)
+        hipLaunchKernelGGL(norm_bwd_wide_kernel<true>, dim3(parts), dim3(kWideWaves * kWave), 0, stream, a);
+    else
+        hipLaunchKernelGGL(norm_bwd_wide_kernel<false>, dim3(parts), dim3(kWideWaves * kWave), 0, stream, a);
 #undef NORM_BWD
 #undef NORM_BWD_NARROW
     hipLaunchKernelGGL(norm_dw_kernel, dim3(a.cols / 32), dim3(1024), 0, stream, a.partial, parts, a.cols, a.dw);

@@ -271,7 +271,7 @@ def test_norm_backward_against_differences(gpu_lib):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,cols", [(33, 4128), (9000, 96), (2500, 800)])
+@pytest.mark.parametrize("rows,cols", [(33, 4128), (9000, 96), (2500, 800), (600, 16416)])
 def test_norm_backward_in_place(gpu_lib, rows, cols):
     g, x, r, w = _norm_inputs(rows, cols, 8)
     o = _forward(x, w, r)
