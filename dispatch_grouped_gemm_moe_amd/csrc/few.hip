@@ -792,8 +792,6 @@ void launch_few_down(const FewGemm& a, int max_act, hipStream_t s) { launch_few_
 // Down product and weighted sum of up to 16 tokens
 // ---------------------------------------------------------------------------
 
-constexpr int kFdWaves = 8;
-constexpr int kFdThreads = kFdWaves * kWave;
 constexpr int kFdTok = 16;    // tokens
 constexpr int kFdCols = 16;   // output columns per workgroup: weight rows of a step
 constexpr int kFdBatch = 4;   // cache lines of a row per step
@@ -829,9 +827,13 @@ struct FewUnit {
 // can draw from memory counts.  Loads of 16 rows x 64 bytes in the MFMA's lane
 // order reach 36 GB/s a CU, 8 rows x one line straight into LDS 50 GB/s; the
 // fragments are then read from LDS, the 16-byte pieces of a row swizzled by
-// its index so that 16 rows fall on distinct banks.
-template <int kKind>
-__global__ __launch_bounds__(kFdThreads) void few_down16_kernel(FewGemm a, int max_act, int max_rows, uint16_t* out) {
+// its index so that 16 rows fall on distinct banks.  H 7168, I 2048: 25.1 us for
+// one MXFP8 token (8 experts, 121 MB, 4.8 TB/s), 162 us for 16 bf16 ones (939 MB,
+// 5.8 TB/s).
+template <int kKind, int kFdWaves>
+__global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a, int max_act, int max_rows,
+                                                                      uint16_t* out) {
+    constexpr int kFdThreads = kFdWaves * kWave;
     __shared__ int s_flag;
     constexpr bool kMx = kKind != kFewBf16;
     __shared__ __attribute__((aligned(1024))) uint8_t s_w[kFdWaves][2][kFdSlot];
@@ -1057,13 +1059,24 @@ int few_down16_splits(int H, int64_t column_kb) {
 
 void launch_few_down16(const FewGemm& a, int max_act, int max_rows, int shared, int splits, uint16_t* out,
                        hipStream_t stream) {
-    const dim3 grid(a.H / kFdCols, splits), block(kFdThreads);
-    if (!a.xq)
-        hipLaunchKernelGGL(few_down16_kernel<kFewBf16>, grid, block, 0, stream, a, max_act, max_rows, out);
-    else if (!shared)
-        hipLaunchKernelGGL(few_down16_kernel<kFewMx>, grid, block, 0, stream, a, max_act, max_rows, out);
-    else
-        hipLaunchKernelGGL(few_down16_kernel<kFewMxShared>, grid, block, 0, stream, a, max_act, max_rows, out);
+    const dim3 grid(a.H / kFdCols, splits);
+#define FEW_DOWN16(KIND, WAVES)                                                                            \
+    hipLaunchKernelGGL((few_down16_kernel<KIND, WAVES>), grid, dim3(WAVES * kWave), 0, stream, a, max_act, \
+                       max_rows, out)
+    // With more column blocks than CUs, two workgroups of four waves fit a CU and
+    // even its load out: one token of H 7168, MXFP8, 27.7 -> 25.1 us, H 4608 and I
+    // 512 11.1 -> 7.2 us.  With fewer, eight waves ask for more at once: H 3584, I
+    // 2048, 8 experts 12.0 us against 13.6 us in four waves and twice the parts.
+    if (a.H / kFdCols > 256) {
+        if (!a.xq) FEW_DOWN16(kFewBf16, 4);
+        else if (!shared) FEW_DOWN16(kFewMx, 4);
+        else FEW_DOWN16(kFewMxShared, 4);
+    } else {
+        if (!a.xq) FEW_DOWN16(kFewBf16, 8);
+        else if (!shared) FEW_DOWN16(kFewMx, 8);
+        else FEW_DOWN16(kFewMxShared, 8);
+    }
+#undef FEW_DOWN16
 }
 
 // out[t] = the weighted rows of the slots in order, then the shared expert's.
