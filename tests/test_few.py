@@ -126,7 +126,7 @@ def _wl(T, H, I, E, k, prec="bf16", shared=False, bias="none", **kw):
 SHAPES = [(1, 64, 64, 1, 1), (1, 128, 64, 8, 2), (2, 2112, 128, 5, 3), (5, 192, 320, 6, 3), (7, 448, 64, 256, 16),
           (16, 320, 192, 4, 4), (17, 256, 128, 8, 2), (31, 128, 192, 7, 1), (33, 448, 320, 16, 5), (48, 64, 128, 2, 1),
           (64, 128, 64, 1, 1), (64, 4160, 64, 3, 2), (64, 192, 64, 200, 16), (9, 256, 1984, 8, 4), (16, 2240, 192, 6, 2),
-          (7, 8256, 64, 1, 1), (50, 6208, 128, 2, 2), (1, 3136, 64, 32, 5)]
+          (7, 8256, 64, 1, 1), (4, 4160, 192, 6, 2), (50, 6208, 128, 2, 2), (1, 3136, 64, 32, 5)]
 
 
 @pytest.mark.gpu
