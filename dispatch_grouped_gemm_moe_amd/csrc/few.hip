@@ -14,8 +14,8 @@
 // Three launches: the router (logits, top-k, expert row lists), the gate|up
 // product with SwiGLU, and the down product with the weighted sum; past 16
 // tokens the weighted sum has a launch of its own.  One MXFP8 token of H 7168, I
-// 2048, 8 of 32 experts takes 82 us (363 MB of weights: 4.4 TB/s over the call,
-// 5.4 over the gate|up product's 44 us), 64 bf16 tokens of the same sizes 533 us
+// 2048, 8 of 32 experts takes 79 us (363 MB of weights: 4.6 TB/s over the call,
+// 5.5 over the gate|up product's 44 us), 64 bf16 tokens of the same sizes 530 us
 // (2.82 GB, 5.3 TB/s).
 //
 // Two other forms of the products were built and measured on that one token, then
@@ -37,6 +37,7 @@ namespace moe {
 // ---------------------------------------------------------------------------
 
 constexpr int kFrEC = 32;         // experts per workgroup: a cache line of a router weight row
+constexpr int kFrTok = 4;         // tokens per workgroup, a wave each
 constexpr int kFrRes = 16;        // residue groups: group l takes h mod 64 in {l, l + 16, l + 32, l + 48}
 constexpr int kFrSlab = 128;      // 64-wide chunks of h per LDS slab
 
@@ -202,7 +203,9 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
 }
 
 // Workgroup (l, x, y): residues l, l + 16, l + 32, l + 48 of h mod 64, experts
-// 32 x .. 32 x + 31, tokens kTok y .. + kTok - 1, a wave per token.
+// 32 x .. 32 x + 31, tokens 4 y .. 4 y + 3, a wave per token.  (Eight tokens a
+// workgroup gather more of x's lines in one: 16 tokens of H 7168 16.1 against 13.4
+// us; 5 tokens over 64 experts, one count less, 9.9 against 10.5.)
 //
 // The logits' order is moe_route's: p[r] sums h = r, r + 64, ... with fused
 // multiply-adds, a halving tree joins the 64 p[r], the bias comes last.  The
@@ -219,10 +222,10 @@ __device__ __forceinline__ void few_lists(const FewRoute& a, FewLists& s) {
 // of a y that counts in last joins the 16 groups' sums to logits and picks its
 // tokens' experts, the last y builds the row lists.  With more than a logit per
 // thread to join, the last of an (x, y) joins, the last of a y picks: one count
-// more (one token, 64 experts: 9.1 against 7.9 us; 8 tokens the same either way).
-template <bool kVec4, int kTok>
-__global__ __launch_bounds__(kTok * kWave) void few_route_kernel(FewRoute a) {
-    constexpr int kThreads = kTok * kWave;
+// more (one token, 64 experts: 9.1 against 7.9 us).
+template <bool kVec4>
+__global__ __launch_bounds__(kFrTok * kWave) void few_route_kernel(FewRoute a) {
+    constexpr int kTok = kFrTok, kThreads = kTok * kWave;
     __shared__ __attribute__((aligned(1024))) float s_wr[kFrSlab * 4][kFrEC];
     __shared__ __attribute__((aligned(16))) float s_x[kTok][2][kFrSlab][2];
     __shared__ float s_logit[kTok][kMaxExperts];
@@ -360,21 +363,12 @@ __global__ __launch_bounds__(kTok * kWave) void few_route_kernel(FewRoute a) {
     few_lists<kThreads>(a, s_lists);
 }
 
-template <int kTok>
-static void launch_few_route_of(const FewRoute& a, hipStream_t stream) {
-    const dim3 grid(kFrRes, ceil_div(a.E, kFrEC), ceil_div(a.T, kTok));
-    if (a.E % 4 == 0 && ((uintptr_t)a.Wr & 15) == 0)
-        hipLaunchKernelGGL((few_route_kernel<true, kTok>), grid, dim3(kTok * kWave), 0, stream, a);
-    else
-        hipLaunchKernelGGL((few_route_kernel<false, kTok>), grid, dim3(kTok * kWave), 0, stream, a);
-}
-
 void launch_few_route(const FewRoute& a, hipStream_t stream) {
-    // up to eight tokens in one group: one count less (7 tokens, H 1024, 256
-    // experts, 14.7 against 16.0 us).  Past that four a group, for fewer lines a
-    // workgroup (16 tokens, H 7168, 32 experts, MXFP8, 13.7 against 16.2 us).
-    if (a.T <= 8) launch_few_route_of<8>(a, stream);
-    else launch_few_route_of<4>(a, stream);
+    const dim3 grid(kFrRes, ceil_div(a.E, kFrEC), ceil_div(a.T, kFrTok)), block(kFrTok * kWave);
+    if (a.E % 4 == 0 && ((uintptr_t)a.Wr & 15) == 0)
+        hipLaunchKernelGGL(few_route_kernel<true>, grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL(few_route_kernel<false>, grid, block, 0, stream, a);
 }
 
 // ---------------------------------------------------------------------------
