@@ -352,3 +352,31 @@ def test_few_two_calls_at_once(gpu_lib):
             moe.moe_layer_fwd_few(f.cfg, f.Wr, f.bias, f.packed, f.x, o, f.ws, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,prec", [(1, "bf16"), (20, "bf16"), (2, "mxfp8")])
+def test_few_weights_past_32_bits(gpu_lib, T, prec):
+    # the bias sends every token to the last two experts; alone they are the same layer
+    H, I, E = 8192, 2112, 66 if prec == "bf16" else 132  # gate and up of every expert: 2^32 bytes and more
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)
+    Wg, Wu, Wd = (torch.zeros(E, *s, device="cuda", dtype=torch.bfloat16) for s in ((H, I), (H, I), (I, H)))
+    for m in (Wg, Wu, Wd):
+        m[-2:] = rand(2, *m.shape[1:]) / 64
+    x, Wr = rand(T, H), torch.randn(H, E, generator=g, device="cuda") / 64
+    bias = torch.full((E,), -1e4, device="cuda")
+    bias[-2:] = 0
+    got = []
+    for n in (E, 2):
+        cfg = moe.make_cfg(T, H, I, n, 2, prec=moe.MOE_PREC_MXFP8 if prec == "mxfp8" else 0)
+        packed = torch.empty(moe.moe_query_sizes(cfg).packed_weights, dtype=torch.uint8, device="cuda")
+        moe.moe_prepare_weights(cfg, *(m[-n:].contiguous() for m in (Wg, Wu, Wd)), packed)
+        ws = torch.zeros(moe.moe_query_few(cfg), dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(x)
+        moe.moe_layer_fwd_few(cfg, Wr[:, -n:].contiguous(), bias[-n:].contiguous(), packed, x, out, ws)
+        torch.cuda.synchronize()
+        got.append(out)
+        del packed
+    assert got[0].abs().max() > 0.01 and torch.isfinite(got[0]).all()
+    assert torch.equal(got[0], got[1])

@@ -324,6 +324,44 @@ def test_dequantize_nan_and_the_quantisers_own_codes(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cols", [1024, 1056, 20480])
+def test_norm_offsets_past_32_bits(gpu_lib, cols):
+    """Rows are independent, so the last rows of more than 2^32 bytes give what they give alone; only
+    the very last row has a gradient, so dw has one term to add up."""
+    rows, n = min(1 << 21, (1 << 31) // cols + 5), 3
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = torch.randn(n, cols, generator=g, device="cuda").bfloat16()
+    w = torch.randn(cols, generator=g, device="cuda")
+    y, rstd = torch.empty_like(x), torch.empty(rows, device="cuda")
+    ck, cs = torch.empty(rows, cols, dtype=torch.uint8, device="cuda"), torch.empty(rows, cols // 32, dtype=torch.uint8,
+                                                                                   device="cuda")
+    yq, ys = torch.empty_like(ck), torch.empty((cols + 127) // 128, rows, 4, dtype=torch.uint8, device="cuda")
+    moe.moe_add_rmsnorm_fwd(x, w, y, eps=EPS, rstd=rstd, y_codes=yq, y_scales=ys, ck_codes=ck, ck_scales=cs)
+    small = _forward(x[-n:].contiguous(), w, codes=True, checkpoint=True)
+    assert torch.equal(y[-n:], small["y"]) and torch.equal(rstd[-n:], small["rstd"])
+    assert torch.equal(yq[-n:], small["y_codes"]) and torch.equal(ys[:, -n:], small["y_scales"])
+    assert torch.equal(ck[-n:], small["ck_codes"]) and torch.equal(cs[-n:], small["ck_scales"])
+    back = torch.empty(n, cols, dtype=torch.bfloat16, device="cuda")
+    moe.moe_mx_dequantize(ck, cs, y)
+    moe.moe_mx_dequantize(small["ck_codes"], small["ck_scales"], back)
+    assert torch.equal(y[-n:], back)
+    moe.moe_mx_dequantize(yq, ys, y, operand_scales=True)
+    moe.moe_mx_dequantize(small["y_codes"], small["y_scales"], back, operand_scales=True)
+    assert torch.equal(y[-n:], back)
+    dy = torch.zeros_like(x)
+    dy[-1] = torch.randn(cols, generator=g, device="cuda").bfloat16()
+    ws = torch.empty(moe.moe_query_add_rmsnorm_bwd(rows, cols), dtype=torch.uint8, device="cuda")
+    for src, part in ((dict(summed=x), dict(summed=x[-n:].contiguous())),
+                      (dict(ck_codes=ck, ck_scales=cs), dict(ck_codes=small["ck_codes"], ck_scales=small["ck_scales"]))):
+        dw, dw_part, dx_part = torch.empty_like(w), torch.empty_like(w), torch.empty_like(back)
+        moe.moe_add_rmsnorm_bwd(dy, w, rstd, y, dw, ws, **src)
+        moe.moe_add_rmsnorm_bwd(dy[-n:].contiguous(), w, small["rstd"], dx_part, dw_part, ws, **part)
+        torch.cuda.synchronize()
+        assert torch.equal(y[-n:], dx_part) and torch.equal(dw, dw_part)
+
+
+@pytest.mark.gpu
 def test_norm_captured_and_replayed(gpu_lib):
     rows, cols = 600, 2080
     g, x, r, w = _norm_inputs(rows, cols, 12)
