@@ -178,6 +178,18 @@ def test_few_ties_go_to_the_lower_expert(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("repeat", [1, 3, 50, 64, 70])
+def test_few_ties_among_many_experts(gpu_lib, repeat):
+    # expert e has the logit of expert e % repeat
+    w = _wl(6, 128, 64, 200, 9)
+    inp = make_inputs(w)
+    inp.Wr = inp.Wr[:, torch.arange(200) % repeat].contiguous()
+    few = Few(w, inp)
+    ref, bound = few_layer(inp, w.T)
+    assert (np.abs(few().double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
 def test_few_reads_nothing_of_an_expert_that_no_token_chose(gpu_lib, prec):
     w = _wl(4, 128, 64, 6, 2, prec=prec)
