@@ -908,7 +908,8 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
     // Ask for the weights of step (t, c) into the slot, load q taking rows 8 (q %
     // 2) .. + 7 of line c + q / 2.  Past the part's end its last line is repeated
     // (and dropped); past the end of an MXFP8 row, in the middle of a line,
-    // its first half (against zero scale bytes).  And for the scale dwords.
+    // its first half (against zero scale bytes).  And for the scale dwords; a bf16
+    // unit has none: no bytes, at scalar offset 0 (it counts against the size).
     auto issue = [&](const FewUnit& t, int c, int slot, Scales& f) {
         uint8_t* dst = s_w[wave][slot];
         const int last = max(t.end - 1, 0);
@@ -925,7 +926,7 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
 #pragma unroll
             for (int j = 0; j < kFdBatch; ++j)
                 f.s[j] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(t.ws, t.ws_bytes), lr * 4,
-                                                              min(c + j, last) * H * 4, 0);
+                                                              t.mx ? min(c + j, last) * H * 4 : 0, 0);
         }
     };
     // The weight fragments of a slot: of line j this lane's pieces lane / 16 and
@@ -971,7 +972,7 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
             x[j] = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
             if constexpr (kMx)
                 xs[j] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(cur.xs, cur.xs_bytes),
-                                                             r * (uint32_t)mx_groups(I) * 4, line * 4, 0);
+                                                             r * (uint32_t)mx_groups(I) * 4, cur.mx ? line * 4 : 0, 0);
         }
         c += kFdBatch;
         const bool flush = c >= cur.end;
