@@ -1023,7 +1023,7 @@ static moe_status make_few_plan(const moe_cfg* c, Plan* p, FewPlan* f) {
     f->slot_row = take(Tk * 4);
     f->partial = take(T * p->E * 16 * 4);
     f->logits = take(T * p->E * 4);
-    f->h = take(rows * I * 2);
+    f->h = take(rows * I * 4);
     f->y = take(std::max(rows, T * kFewMaxSplits) * H * 4);
     if (p->mx) {
         f->xq = take(T * H);

@@ -484,8 +484,10 @@ __device__ __forceinline__ void few_widen(const intx4 (&v)[2], uint32_t scales, 
 // products off by 1.7e-5 of their norm), which is too coarse for what is
 // quantised again: 16 of 11648 values of h took another code, this way none,
 // in the same time.
-template <bool MX, int MT, bool kWiden>
-__device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<MX, MT>& x, int lane,
+//
+// kParts: fragments MT .. of x are the second parts of tokens in two bf16 parts.
+template <bool MX, int MT, int kParts, bool kWiden>
+__device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<MX, MT * kParts>& x, int lane,
                                          floatx4 (&acc)[4][MT]) {
     if constexpr (MX && kWiden) {
 #pragma unroll
@@ -513,10 +515,10 @@ __device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<
                         (int)(w.s[i] >> shift), 0, (int)(x.s[m] >> shift));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[i][j]),
-                                                                            __builtin_bit_cast(bf16x8, x.v[m][j]),
-                                                                            acc[i][m], 0, 0, 0);
+                    for (int j = 0; j < 2 * kParts; ++j)
+                        acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, w.v[i][j & 1]),
+                            __builtin_bit_cast(bf16x8, x.v[m + MT * (j >> 1)][j & 1]), acc[i][m], 0, 0, 0);
                 }
             }
     }
@@ -528,26 +530,26 @@ __device__ __forceinline__ void few_mfma(const FewFrag<MX, 4>& w, const FewFrag<
 // from the L2, are loaded in their own step, ahead of the next weights, so that
 // waiting for them (loads return in order) leaves those in flight.  Steps past
 // the end load zeros, so the loop has one exit and keeps its registers.
-template <bool MX, int MT, bool kWiden>
+template <bool MX, int MT, int kParts, bool kWiden>
 __device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperand& xo, int kb, int c0, int end,
-                                           int wave, int lane, const uint32_t (&xrow)[MT],
-                                           const uint32_t (&xsoff)[MT], floatx4 (&acc)[4][MT]) {
+                                           int wave, int lane, const uint32_t (&xrow)[MT * kParts],
+                                           const uint32_t (&xsoff)[MT * kParts], floatx4 (&acc)[4][MT]) {
     const uint32_t lo = (uint32_t)(lane >> 4) * 16;
-    uint32_t woff[4], wsoff[4], xoff[MT];
+    uint32_t woff[4], wsoff[4], xoff[MT * kParts];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         woff[i] = (uint32_t)(i * 16 + (lane & 15)) * (uint32_t)kb + lo;
         wsoff[i] = (uint32_t)(i * 16 + (lane & 15)) * 4;
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xoff[m] = xrow[m] + lo;
+    for (int m = 0; m < MT * kParts; ++m) xoff[m] = xrow[m] + lo;
     FewFrag<MX, 4> w0, w1;
-    FewFrag<MX, MT> x;
+    FewFrag<MX, MT * kParts> x;
     auto step = [&](int c, const FewFrag<MX, 4>& w, FewFrag<MX, 4>& next) {
-        few_load<MX, MT>(xo, end, c, xoff, xsoff, x);
+        few_load<MX, MT * kParts>(xo, end, c, xoff, xsoff, x);
         few_load<MX, 4>(wo, end, c + kFgWaves, woff, wsoff, next);
         __builtin_amdgcn_sched_barrier(0);
-        few_mfma<MX, MT, kWiden>(w, x, lane, acc);
+        few_mfma<MX, MT, kParts, kWiden>(w, x, lane, acc);
         __builtin_amdgcn_sched_barrier(0);
     };
     few_load<MX, 4>(wo, end, c0 + wave, woff, wsoff, w0);
@@ -555,6 +557,16 @@ __device__ __forceinline__ void few_stream(const FewOperand& wo, const FewOperan
         step(c, w0, w1);
         step(c + kFgWaves, w1, w0);
     }
+}
+
+// v in two bf16 parts of its sign, neither zero unless v is (or next to nothing):
+// the first cut off towards zero, and one step smaller still where that would
+// leave nothing, so that an infinite weight gives v's infinity in both products.
+__device__ __forceinline__ void few_split(float v, uint16_t& hi, uint16_t& lo) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    hi = (uint16_t)(b >> 16);
+    if ((b & 0xffff) == 0 && (hi & 0x7fff) != 0 && (hi & 0x7fff) < 0x7f80) --hi;
+    lo = f32_to_bf16_rne((hi & 0x7fff) < 0x7f80 ? v - bf16_to_f32(hi) : v);
 }
 
 // One M tile's partial sums of every wave into LDS: s_part[wave][token][row].
@@ -603,7 +615,7 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
     const int lines = ((int)kb + kFgChunk - 1) / kFgChunk, splits = a.gu_splits;
     const int end = z + 1 == splits ? (int)kb : lines * (z + 1) / splits * kFgChunk;
-    few_stream<MX, MT, true>(wo, xo, (int)kb, lines * z / splits, end, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT, 1, true>(wo, xo, (int)kb, lines * z / splits, end, wave, lane, xrow, xsrow, acc);
     // thread (tokens tid / 32, + 8; column tid % 32): the tile's rows are 32 gate
     // columns and the 32 up columns of the same indices
     const int col = tid & 31;
@@ -625,10 +637,17 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
                 }
             }
         } else if (r < rows) {
-            // bf16, as the layer forward keeps h: an operand of the next MFMA.  In
-            // two bf16 parts the layer's error would be 2^-8.5 rather than 2^-8 of
-            // its output, for 2 us of 29 (one token, H 2048) and 25 of 536 (64, H 7168).
-            a.h[(size_t)(row0 + r) * I + n * 32 + col] = f32_to_bf16_rne(h);
+            // Two bf16 parts, operands of the next MFMAs: 2^-15 of h is lost.  One part
+            // would add an error as large as the output's own rounding (measured
+            // against 64 bits, 0.0024 to 0.0028 instead of 0.0017 of the output).  Where
+            // an expert has up to eight rows the parts share a fragment and cost next
+            // to nothing (one token, H 2048: 0.5 of 28 us; as products of their own,
+            // 2); for 64 tokens of H 7168 the down product takes 196 us instead of 182.
+            uint16_t hi, lo;
+            few_split(h, hi, lo);
+            uint16_t* d = a.h + (size_t)(row0 + r) * 2 * I + n * 32 + col;
+            d[0] = hi;
+            d[I] = lo;
         }
     };
     // the parts' sums of row r: [row][tile of 32 columns][part][64]
@@ -668,7 +687,9 @@ __device__ __forceinline__ void few_gate_up(const FewGemm& a, int e, int n, int 
     }
 }
 
-template <bool MX, int MT>
+// kPairs: up to eight rows whose two bf16 parts are rows of their own, 2 r and 2 r
+// + 1 (as they lie in memory): both products in one 16-wide fragment.
+template <bool MX, int MT, bool kPairs>
 __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row0, int rows, float* s_part) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -676,7 +697,8 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
     const uint32_t kb = (uint32_t)I * (MX ? 1 : 2);
     FewOperand wo{}, xo{};
     wo.bytes = kFgRows * kb;
-    xo.bytes = (uint32_t)rows * kb;
+    constexpr int kParts = MX || kPairs ? 1 : 2;  // of a token in fragments of their own
+    xo.bytes = (uint32_t)rows * kb * (MX ? 1 : 2);
     if constexpr (MX) {
         wo.data = a.w2q + ((int64_t)e * H + (int64_t)n * kFgRows) * I;
         wo.scale = a.s2 + ((int64_t)e * mx_groups(I) * H + (int64_t)n * kFgRows) * 4;
@@ -688,13 +710,13 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
         xo.scale_bytes = (uint32_t)rows * (uint32_t)mx_groups(I) * 4;
     } else {
         wo.data = a.w2 + ((int64_t)e * H + (int64_t)n * kFgRows) * I;
-        xo.data = a.h + (int64_t)row0 * I;
+        xo.data = a.h + (int64_t)row0 * 2 * I;
     }
-    uint32_t xrow[MT], xsrow[MT];
+    uint32_t xrow[MT * kParts], xsrow[MT * kParts];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const uint32_t r = (uint32_t)min(m * 16 + (lane & 15), rows - 1);
-        xrow[m] = r * kb;
+    for (int m = 0; m < MT * kParts; ++m) {
+        const uint32_t r = (uint32_t)min(m % MT * 16 + (lane & 15), (kPairs ? 2 * rows : rows) - 1);
+        xrow[m] = (r * kParts + m / MT) * kb;
         xsrow[m] = r * (uint32_t)mx_groups(I) * 4;
     }
     floatx4 acc[4][MT];
@@ -702,7 +724,7 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0, 0, 0, 0};
-    few_stream<MX, MT, false>(wo, xo, (int)kb, 0, (int)kb, wave, lane, xrow, xsrow, acc);
+    few_stream<MX, MT, kParts, false>(wo, xo, (int)kb, 0, (int)kb, wave, lane, xrow, xsrow, acc);
     const int col = (tid & 31) * 2;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -717,7 +739,12 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
                 y0 += s_part[(w * 16 + tt) * kFgLd + col];
                 y1 += s_part[(w * 16 + tt) * kFgLd + col + 1];
             }
-            const int r = m * 16 + tt;
+            int r = m * 16 + tt;
+            if constexpr (kPairs) {  // the pair's other part: half a wave further on
+                y0 += __shfl_xor(y0, 32, kWave);
+                y1 += __shfl_xor(y1, 32, kWave);
+                r = tt & 1 ? rows : tt >> 1;
+            }
             if (r < rows) {
                 const float wt = a.row_w[row0 + r];
                 float* d = a.y + (size_t)(row0 + r) * H + n * kFgRows + col;
@@ -731,7 +758,7 @@ __device__ __forceinline__ void few_down(const FewGemm& a, int e, int n, int row
 template <bool kDown, bool MX, int MT>
 __device__ __forceinline__ void few_tile(const FewGemm& a, int e, int n, int row0, int rows, int z, int counter,
                                          float* s_part) {
-    if constexpr (kDown) few_down<MX, MT>(a, e, n, row0, rows, s_part);
+    if constexpr (kDown) few_down<MX, MT, false>(a, e, n, row0, rows, s_part);
     else few_gate_up<MX, MT>(a, e, n, row0, rows, z, counter, s_part);
 }
 
@@ -740,7 +767,8 @@ __device__ __forceinline__ void few_tile(const FewGemm& a, int e, int n, int row
 template <bool kDown, bool MX, int kMost>
 __device__ __forceinline__ void few_tile_rows(const FewGemm& a, int e, int n, int row0, int rows, int z, int counter,
                                               float* s_part) {
-    if (kMost == 1 || rows <= 16) few_tile<kDown, MX, 1>(a, e, n, row0, rows, z, counter, s_part);
+    if (kDown && !MX && rows <= 8) few_down<MX, 1, true>(a, e, n, row0, rows, s_part);
+    else if (kMost == 1 || rows <= 16) few_tile<kDown, MX, 1>(a, e, n, row0, rows, z, counter, s_part);
     else if (kMost == 2 || rows <= 32) few_tile<kDown, MX, 2>(a, e, n, row0, rows, z, counter, s_part);
     else few_tile<kDown, MX, 4>(a, e, n, row0, rows, z, counter, s_part);
 }
@@ -751,7 +779,7 @@ __device__ __forceinline__ void few_tile_rows(const FewGemm& a, int e, int n, in
 // bound on waves keeps the compiler from spreading over accumulation registers,
 // which would halve the waves per SIMD past 16 tokens.
 template <bool kDown, bool kMx, int kMost>
-__global__ __launch_bounds__(kFgThreads, kMost == 1 ? 1 : (kMost == 4 ? 2 : (kMx ? 3 : 4))) void few_gemm_kernel(
+__global__ __launch_bounds__(kFgThreads, kMost == 1 ? 1 : (kMost == 4 ? 2 : (kMx || kDown ? 3 : 4))) void few_gemm_kernel(
     FewGemm a) {
     __shared__ __attribute__((aligned(16))) float s_part[kFgWaves * 16 * kFgLd];
     const int nt = kDown ? a.H / kFgRows : a.I / 32;
@@ -823,6 +851,7 @@ struct FewUnit {
     int row0, rows;           // token rows
     int kb, end;              // bytes of a row, last line of the part + 1
     int mx;
+    bool pairs;               // bf16 rows few enough that their two parts are rows of one fragment
 };
 
 // Output columns 16 n .. 16 n + 15 of every token, over all active experts: the
@@ -837,8 +866,12 @@ struct FewUnit {
 // order reach 36 GB/s a CU, 8 rows x one line straight into LDS 50 GB/s; the
 // fragments are then read from LDS, the 16-byte pieces of a row swizzled by
 // its index so that 16 rows fall on distinct banks.  H 7168, I 2048: 25.1 us for
-// one MXFP8 token (8 experts, 121 MB, 4.8 TB/s), 162 us for 16 bf16 ones (939 MB,
-// 5.8 TB/s).
+// one MXFP8 token (8 experts, 121 MB, 4.8 TB/s), 171 us for 16 bf16 ones (939 MB,
+// 5.5 TB/s).
+//
+// The two bf16 parts of an expert's h lie as rows 2 r and 2 r + 1: up to eight
+// rows are one fragment, whose neighbouring columns are added at the end; past
+// that the second parts are loaded and multiplied on their own.
 template <int kKind, int kFdWaves>
 __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a, int max_act, int max_rows,
                                                                       uint16_t* out) {
@@ -882,6 +915,7 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
         t.rows = (int)scalar((uint32_t)s_off[i + 1]) - t.row0;
         t.mx = kKind == kFewMx || (kKind == kFewMxShared && e < a.E) ? 1 : 0;
         t.kb = t.mx ? I : 2 * I;
+        t.pairs = kKind != kFewMx && !t.mx && t.rows <= kFdTok / 2;
         const int ln = (t.kb + kFgChunk - 1) / kFgChunk, bt = (ln + kFdBatch - 1) / kFdBatch;
         c0 = (bt * part >> log_parts) * kFdBatch;
         t.end = min((bt * (part + 1) >> log_parts) * kFdBatch, ln);
@@ -889,7 +923,7 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
         const int64_t wrow = (int64_t)e * H + (int64_t)n * kFdCols;
         const uint32_t groups = (uint32_t)mx_groups(I);
         t.w = scalar((t.mx ? a.w2q : (const uint8_t*)a.w2) + wrow * t.kb);
-        t.x = scalar((t.mx ? a.hq : (const uint8_t*)a.h) + (int64_t)t.row0 * t.kb);
+        t.x = scalar(t.mx ? a.hq + (int64_t)t.row0 * I : (const uint8_t*)(a.h + (int64_t)t.row0 * 2 * I));
         if (kMx) {
             t.ws = scalar(a.s2 + ((int64_t)e * groups * H + (int64_t)n * kFdCols) * 4);
             t.ws_bytes = scalar(t.mx ? (groups - 1) * (uint32_t)H * 4 + kFdCols * 4 : 0);
@@ -958,21 +992,33 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
     auto step = [&](int slot, const Scales& f, Scales& next) {
         const FewUnit cur = t;
         const int c0 = c;
-        intx8 x[kFdBatch];
+        constexpr int kXl = kKind == kFewMx ? 0 : kFdBatch;
+        intx8 x[kFdBatch], xl[kXl + 1];  // xl: the second parts, where they are not rows of their own
         uint32_t xs[kMx ? kFdBatch : 1];
-        const uint32_t r = (uint32_t)min((int)lr, cur.rows - 1);  // past the last row: the last one again
+        const uint32_t r = (uint32_t)min((int)lr, (cur.pairs ? 2 * cur.rows : cur.rows) - 1);  // past the last: that again
         const int last = max(cur.end - 1, 0);
-        const __amdgpu_buffer_rsrc_t d = few_rsrc(cur.x, (uint32_t)(cur.rows * cur.kb));
+        const bool two = kKind != kFewMx && !cur.mx && !cur.pairs;
+        const uint32_t xoff = r * (uint32_t)(two ? 2 * cur.kb : cur.kb) + lo;
+        const __amdgpu_buffer_rsrc_t d = few_rsrc(cur.x, (uint32_t)(cur.mx ? cur.rows : 2 * cur.rows) * (uint32_t)cur.kb);
 #pragma unroll
         for (int j = 0; j < kFdBatch; ++j) {
             const int line = min(c0 + j, last), at = line * kFgChunk;
             const int hi = kMx && at + kFgChunk / 2 >= cur.kb ? at : at + kFgChunk / 2;
-            const intx4 p0 = __builtin_amdgcn_raw_buffer_load_b128(d, r * (uint32_t)cur.kb + lo, at, 0);
-            const intx4 p1 = __builtin_amdgcn_raw_buffer_load_b128(d, r * (uint32_t)cur.kb + lo, hi, 0);
+            const intx4 p0 = __builtin_amdgcn_raw_buffer_load_b128(d, xoff, at, 0);
+            const intx4 p1 = __builtin_amdgcn_raw_buffer_load_b128(d, xoff, hi, 0);
             x[j] = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
             if constexpr (kMx)
                 xs[j] = __builtin_amdgcn_raw_buffer_load_b32(few_rsrc(cur.xs, cur.xs_bytes),
                                                              r * (uint32_t)mx_groups(I) * 4, cur.mx ? line * 4 : 0, 0);
+        }
+        if (two) {
+#pragma unroll
+            for (int j = 0; j < kXl; ++j) {
+                const int at = min(c0 + j, last) * kFgChunk + cur.kb;
+                const intx4 p0 = __builtin_amdgcn_raw_buffer_load_b128(d, xoff, at, 0);
+                const intx4 p1 = __builtin_amdgcn_raw_buffer_load_b128(d, xoff, at + kFgChunk / 2, 0);
+                xl[j] = __builtin_shufflevector(p0, p1, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
         }
         c += kFdBatch;
         const bool flush = c >= cur.end;
@@ -990,7 +1036,17 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
         if (c0 + kFdBatch > cur.end) {  // zero times zero past the part's end, whatever the last line holds
 #pragma unroll
             for (int j = 0; j < kFdBatch; ++j)
-                if (c0 + j >= cur.end) w[j] = x[j] = intx8{};
+                if (c0 + j >= cur.end) {
+                    w[j] = x[j] = intx8{};
+                    if constexpr (kKind != kFewMx) xl[j] = intx8{};
+                }
+        }
+        if (two) {
+#pragma unroll
+            for (int j = 0; j < kXl; ++j) {
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_half(w[j], 0), few_half(xl[j], 0), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(few_half(w[j], 1), few_half(xl[j], 1), acc, 0, 0, 0);
+            }
         }
 #pragma unroll
         for (int j = 0; j < kFdBatch; ++j) {
@@ -1004,10 +1060,20 @@ __global__ __launch_bounds__(kFdWaves * kWave) void few_down16_kernel(FewGemm a,
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (flush) {  // lane: columns 4 (l / 16) .. + 3 of token row l % 16
-            if ((int)lr < cur.rows) {
-                floatx4* d = (floatx4*)&s_sum[wave][s_token[cur.row0 + lr]][4 * (lane >> 4)];
-                const float wt = s_weight[cur.row0 + lr];
+        if (flush) {  // lane: columns 4 (l / 16) .. + 3 of token row l % 16, or of the part of row l % 16 / 2
+            int tr = (int)lr;
+            if (kKind != kFewMx && cur.pairs) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // + the neighbour's
+                    const float v = acc[q];
+                    acc[q] = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1,
+                                                                                    0xF, 0xF, true));
+                }
+                tr = tr & 1 ? cur.rows : tr >> 1;
+            }
+            if (tr < cur.rows) {
+                floatx4* d = (floatx4*)&s_sum[wave][s_token[cur.row0 + tr]][4 * (lane >> 4)];
+                const float wt = s_weight[cur.row0 + tr];
                 floatx4 v = *d;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(wt, acc[q], v[q]);

@@ -379,7 +379,7 @@ struct FewGemm {
     const int* slot_row;
     const uint16_t* x;                 // [T][H]
     const uint16_t *w1, *w2;           // packed bf16 weights [Et][2I][H], [Et][H][I]
-    uint16_t* h;                       // [rows][I]
+    uint16_t* h;                       // [rows][2][I]: two bf16 parts
     // MXFP8 (xq NULL: bf16)
     const uint8_t *xq, *xs;            // [T][H], operand-layout scales
     const uint8_t *w1q, *s1, *w2q, *s2;

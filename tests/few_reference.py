@@ -2,7 +2,7 @@
 rounds where the library's documentation says it rounds can be from it.
 
 What is rounded: the router's fp32 logits (the oracle's fixed order gives them
-bit for bit) and softmax; bf16 precision rounds h to bf16, MXFP8 quantises x
+bit for bit) and softmax; bf16 precision holds h in two bf16 parts, MXFP8 quantises x
 (exactly defined) and h; every sum is fp32; the output is bf16.  The bound adds
 what each of these can move the output by, element by element:
 
@@ -10,7 +10,7 @@ what each of these can move the output by, element by element:
   the textbook n 2^-24, as a matrix instruction may truncate where it aligns);
 * silu(g) u for errors dg, du: |silu'| <= 1.1, plus 2^-20 relative for exp and
   the division;
-* h to bf16: half a step, 2^-8 relative;
+* h to two bf16 parts, the first cut off: half a step of a step, 2^-15 relative;
 * h to MXFP8: the scale and the code of h +- dh, the farthest of the cases;
 * the gate weight: 2^-19 relative (exp of a difference of logits);
 * the output: half a bf16 step, 2^-8 relative.
@@ -59,7 +59,7 @@ def few_layer(inp, T):
                     err = np.maximum(err, np.abs(_point(b + sg * d, e) - ref))
             h, dh = ref.reshape(h.shape), err.reshape(h.shape)
         else:
-            dh = dh + HALF_BF16 * (np.abs(h) + dh)
+            dh = dh + 2 * HALF_BF16 ** 2 * (np.abs(h) + dh)
         y = h @ Wd
         mag = np.abs(h) @ np.abs(Wd)
         dy = dh @ np.abs(Wd) + I * F32 * (mag + dh @ np.abs(Wd))
