@@ -14,8 +14,8 @@
 // Three launches: the router (logits, top-k, expert row lists), the gate|up
 // product with SwiGLU, and the down product with the weighted sum; past 16
 // tokens the weighted sum has a launch of its own.  One MXFP8 token of H 7168, I
-// 2048, 8 of 32 experts takes 79 us (363 MB of weights: 4.6 TB/s over the call,
-// 5.5 over the gate|up product's 44 us), 64 bf16 tokens of the same sizes 530 us
+// 2048, 8 of 32 experts takes 77 us (363 MB of weights: 4.7 TB/s over the call,
+// 5.5 over the gate|up product's 44 us), 64 bf16 tokens of the same sizes 537 us
 // (2.82 GB, 5.3 TB/s).
 //
 // Two other forms of the products were built and measured on that one token, then

@@ -393,8 +393,9 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t *dy, c
  * moe_prepare_weights buffer serves both) and formula, the same expert choice
  * and weights bit for bit; the outputs differ from moe_layer_fwd's by the
  * rounding of sums taken in another order (here the expert outputs stay fp32
- * until the weighted sum, and bf16 precision keeps h in two bf16 parts).  Runs of one call are bitwise repeatable; a token's
- * sums may be taken in another order beside other tokens.
+ * until the weighted sum, and bf16 precision keeps h in two bf16 parts).  Runs
+ * of one call are bitwise repeatable; a token's sums may be taken in another
+ * order beside other tokens.
  *   x, out [T,H] bf16, 16-byte aligned; they may not overlap;
  *   x_codes, x_scales: MOE_PREC_MXFP8, optional: the MXFP8 form of x as
  *       moe_route or moe_add_rmsnorm_fwd wrote it (codes 16-byte aligned,
