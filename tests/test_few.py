@@ -251,6 +251,26 @@ def test_few_an_infinite_weight_gives_infinity(gpu_lib, T, I):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(3, 8, 2), (12, 2, 2), (16, 40, 2), (20, 4, 1), (40, 2, 2), (64, 48, 2)])
+def test_few_an_infinite_weight_times_an_exact_h(gpu_lib, T, E, k):
+    # h is 1 in its first column, which one bf16 value holds: neither of its parts may be zero
+    w = _wl(T, 128, 64, E, k)
+    inp = make_inputs(w)
+    inp.x[:, 0] = 1
+    for m in (inp.Wg, inp.Wu, inp.Wd):
+        m.zero_()
+    inp.Wg[:, 0, 0], inp.Wu[:, 0, 0] = 64, 1 / 64
+    for e in range(E):
+        inp.Wd[e, 0, e] = float("inf") if e % 2 else float("-inf")
+    few = Few(w, inp)
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    moe.moe_route(few.cfg, few.x, few.Wr, few.bias, idx, torch.empty(T, k, device="cuda"))
+    sign = torch.where(idx % 2 == 1, float("inf"), float("-inf")).bfloat16()
+    want = torch.zeros(T, 128, dtype=torch.bfloat16, device="cuda").scatter_(1, idx.long(), sign)
+    assert torch.equal(few(), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
 @pytest.mark.parametrize("shape", [(1, 448, 64, 256, 16), (6, 64, 64, 8, 3), (11, 2112, 64, 33, 7), (64, 320, 128, 256, 16)],
                          ids=lambda s: "-".join(map(str, s)))
