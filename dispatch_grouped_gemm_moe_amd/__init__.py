@@ -13,6 +13,8 @@ import ctypes
 import dataclasses
 import os
 
+import torch
+
 from .build import lib_path
 
 MOE_OK, MOE_E_INVALID, MOE_E_UNSUPPORTED, MOE_E_WORKSPACE, MOE_E_HIP, MOE_E_DEVICE = range(6)
@@ -212,25 +214,29 @@ def moe_mx_quantize(src, codes, scales, stream=None):
                                                       _stream(stream)))
 
 
+# a tensor's methods as functions: looked up once, not for each of a call's tensors
+_numel, _is_contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
+_get_device, _data_ptr = torch.Tensor.get_device, torch.Tensor.data_ptr
+
+
 def _dense(fn, device, t, dtype, n):
     """The pointer of a dense tensor of `dtype` with at least n elements on `device` (its index, -1 for
     the host); None stays None.  The kernels see pointers only, so what they could not read is refused
     here."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+    if t.dtype is not dtype or _numel(t) < n or not _is_contiguous(t) or _get_device(t) != device:
         raise MoeError(fn, MOE_E_INVALID)
-    return t.data_ptr()
+    return _data_ptr(t)
 
 
 def _call(fn, device, stream, *args):
     """Library function fn(*args, stream) on `device`: the given stream, or that device's current one.  A
     launch goes to the current device's queues, so that one is made current for the call.  Host tensors
     are refused: the kernels would fault on them."""
-    import torch
     if device < 0:
         raise MoeError(fn, MOE_E_INVALID)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         if stream is None:
             s = torch._C._cuda_getCurrentRawStream(device)
         else:
@@ -246,7 +252,6 @@ def _call(fn, device, stream, *args):
 def moe_mx_dequantize(codes, scales, dst, operand_scales=False, stream=None):
     """dst (bf16) = the values of codes [rows, cols] and their scales: [rows, cols/32], or with
     operand_scales the GEMM operand layout [ceil(cols/128), rows, 4]."""
-    import torch
     fn, dev, u8 = "moe_mx_dequantize", codes.get_device(), torch.uint8
     rows, cols = codes.shape
     n_scales = (cols + 127) // 128 * rows * 4 if operand_scales else rows * (cols // 32)
@@ -258,7 +263,6 @@ def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd
                         ck_codes=None, ck_scales=None, stream=None):
     """y = rmsnorm(x + residual) * weight over the rows of x [rows, cols]; see include/moe.h for the
     optional outputs (the sum, 1/rms, the MXFP8 form of y, the 8-bit checkpoint of the sum)."""
-    import torch
     fn, dev, b16, f32, u8 = "moe_add_rmsnorm_fwd", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     rows, cols = x.shape
     n = rows * cols
@@ -278,7 +282,6 @@ def moe_query_add_rmsnorm_bwd(rows, cols) -> int:
 def moe_add_rmsnorm_bwd(dy, weight, rstd, dx, dweight, ws, summed=None, ck_codes=None, ck_scales=None, dsum=None,
                         stream=None):
     """dx and dweight of moe_add_rmsnorm_fwd, from the sum or from its 8-bit checkpoint."""
-    import torch
     fn, dev, b16, f32, u8 = "moe_add_rmsnorm_bwd", dy.get_device(), torch.bfloat16, torch.float32, torch.uint8
     rows, cols = dy.shape
     n = rows * cols
@@ -298,7 +301,6 @@ def moe_query_few(cfg: moe_cfg) -> int:
 def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=None, stream=None):
     """Layer forward for cfg.T <= MOE_FEW_MAX_TOKENS tokens; ws: moe_query_few bytes, the first
     MOE_FEW_COUNTER_BYTES of them zeroed once."""
-    import torch
     fn, dev, b16, f32, u8 = "moe_layer_fwd_few", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     T, H, E = cfg.T, cfg.H, cfg.E
     w = moe_weights(_dense(fn, dev, Wr, f32, H * E), _dense(fn, dev, bias, f32, E), _dense(fn, dev, packed, u8, 0),
