@@ -437,7 +437,7 @@ struct NormBwd {
     float* partial;            // [norm_bwd_parts][cols]
 };
 int norm_bwd_parts(int64_t rows, int cols);
-void launch_norm_bwd(const NormBwd& a, hipStream_t stream);
+void launch_norm_bwd(NormBwd a, hipStream_t stream);
 
 // codes [rows][cols] and scales (layout 0: [rows][cols / 32], 1: operand layout) -> bf16
 void launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int layout, uint16_t* dst,

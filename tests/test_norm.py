@@ -200,7 +200,7 @@ def test_norm_forward_zero_huge_and_spoilt_rows(gpu_lib):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("cols", COLS)
-@pytest.mark.parametrize("rows", [1, 5, 700])
+@pytest.mark.parametrize("rows", [1, 2, 5, 30, 700])
 def test_norm_backward(gpu_lib, rows, cols):
     if rows * cols > 1 << 21:
         rows = 21
