@@ -26,8 +26,14 @@ __device__ __forceinline__ void unpack8(intx4 raw, float (&v)[8]) {
     }
 }
 
+// Two values rounded to nearest even by the conversion instruction.  It gives what
+// f32_to_bf16_rne gives for all 2^32 patterns but the NaN ones (compared one by
+// one), and these stay NaN: adding to a pattern carries a NaN whose payload is all
+// ones, as a gain or 1/rms read from outside may hold, over into a zero.
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{a, b}, bf16x2));
 }
 
 __device__ __forceinline__ intx4 pack8(const float (&v)[8]) {

@@ -416,3 +416,47 @@ def test_block_of_norm_and_few_token_layer(gpu_lib):
             inp.x = o["y"].cpu()
             ref, bound = few_layer(inp, 6)
             assert (np.abs(x.double().cpu().numpy() - ref) <= bound).all()
+
+
+# ------------------------------------------------------------------ NaN of any payload
+
+NAN_BITS = (-1, 0x7FFFFFFF, 0x7FC00000, -0x400000, 0x7FFF8000, -0x8000)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [64, 544, 4128, 16416])
+def test_norm_keeps_a_nan_whatever_its_payload(gpu_lib, cols):
+    rows = 3
+    g, x, r, w = _norm_inputs(rows, cols, 31)
+    dy = _rand(g, rows, cols)
+    ws = torch.empty(moe.moe_query_add_rmsnorm_bwd(rows, cols), dtype=torch.uint8, device="cuda")
+
+    def back(w, rstd):
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        moe.moe_add_rmsnorm_bwd(dy, w, rstd, dx, dw, ws, summed=want["summed"])
+        torch.cuda.synchronize()
+        return dx, dw
+
+    want = _forward(x, w, r)
+    dx, dw = back(w, want["rstd"])
+    for i, b in enumerate(NAN_BITS):
+        # a gain: its column of y, every row of dx (each row's mean has it), no part of dweight
+        bad = w.clone()
+        bad.view(torch.int32)[5 + i] = b
+        o = _forward(x, bad, r)
+        keep = torch.arange(cols, device="cuda") != 5 + i
+        assert torch.isnan(o["y"][:, 5 + i]).all() and torch.equal(o["y"][:, keep], want["y"][:, keep]), hex(b)
+        dx_bad, dw_bad = back(bad, want["rstd"])
+        assert torch.isnan(dx_bad).all() and torch.equal(dw_bad, dw), hex(b)
+        # 1/rms of a row: that row of dx, and all of dweight
+        rstd = want["rstd"].clone()
+        rstd.view(torch.int32)[1] = b
+        dx_bad, dw_bad = back(w, rstd)
+        assert torch.isnan(dx_bad[1]).all() and torch.isnan(dw_bad).all(), hex(b)
+        assert torch.equal(dx_bad[0], dx[0]) and torch.equal(dx_bad[2], dx[2])
+    # a sum: both signs of bf16's own NaN patterns pass through
+    bad = x.clone()
+    bad.view(torch.int16)[1, :4] = torch.tensor([0x7FFF, -1, 0x7F81, -0x7F], dtype=torch.int16, device="cuda")
+    o = _forward(bad, w, r)
+    assert torch.isnan(o["summed"][1, :4]).all() and torch.isnan(o["y"][1]).all()
+    assert torch.equal(o["y"][0], want["y"][0])
