@@ -13,8 +13,6 @@ import ctypes
 import dataclasses
 import os
 
-import torch
-
 from .build import lib_path
 
 MOE_OK, MOE_E_INVALID, MOE_E_UNSUPPORTED, MOE_E_WORKSPACE, MOE_E_HIP, MOE_E_DEVICE = range(6)
@@ -214,9 +212,15 @@ def moe_mx_quantize(src, codes, scales, stream=None):
                                                       _stream(stream)))
 
 
-# a tensor's methods as functions: looked up once, not for each of a call's tensors
-_numel, _is_contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
-_get_device, _data_ptr = torch.Tensor.get_device, torch.Tensor.data_ptr
+torch = None  # until a call is given tensors: building, sizing and validating need none
+
+
+def _use_torch():
+    """torch, and its tensors' methods as functions: looked up once, not for each of a call's tensors."""
+    global torch, _numel, _is_contiguous, _get_device, _data_ptr
+    import torch
+    _numel, _is_contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
+    _get_device, _data_ptr = torch.Tensor.get_device, torch.Tensor.data_ptr
 
 
 def _dense(fn, device, t, dtype, n):
@@ -252,6 +256,8 @@ def _call(fn, device, stream, *args):
 def moe_mx_dequantize(codes, scales, dst, operand_scales=False, stream=None):
     """dst (bf16) = the values of codes [rows, cols] and their scales: [rows, cols/32], or with
     operand_scales the GEMM operand layout [ceil(cols/128), rows, 4]."""
+    if torch is None:
+        _use_torch()
     fn, dev, u8 = "moe_mx_dequantize", codes.get_device(), torch.uint8
     rows, cols = codes.shape
     n_scales = (cols + 127) // 128 * rows * 4 if operand_scales else rows * (cols // 32)
@@ -263,6 +269,8 @@ def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd
                         ck_codes=None, ck_scales=None, stream=None):
     """y = rmsnorm(x + residual) * weight over the rows of x [rows, cols]; see include/moe.h for the
     optional outputs (the sum, 1/rms, the MXFP8 form of y, the 8-bit checkpoint of the sum)."""
+    if torch is None:
+        _use_torch()
     fn, dev, b16, f32, u8 = "moe_add_rmsnorm_fwd", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     rows, cols = x.shape
     n = rows * cols
@@ -282,6 +290,8 @@ def moe_query_add_rmsnorm_bwd(rows, cols) -> int:
 def moe_add_rmsnorm_bwd(dy, weight, rstd, dx, dweight, ws, summed=None, ck_codes=None, ck_scales=None, dsum=None,
                         stream=None):
     """dx and dweight of moe_add_rmsnorm_fwd, from the sum or from its 8-bit checkpoint."""
+    if torch is None:
+        _use_torch()
     fn, dev, b16, f32, u8 = "moe_add_rmsnorm_bwd", dy.get_device(), torch.bfloat16, torch.float32, torch.uint8
     rows, cols = dy.shape
     n = rows * cols
@@ -301,6 +311,8 @@ def moe_query_few(cfg: moe_cfg) -> int:
 def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=None, stream=None):
     """Layer forward for cfg.T <= MOE_FEW_MAX_TOKENS tokens; ws: moe_query_few bytes, the first
     MOE_FEW_COUNTER_BYTES of them zeroed once."""
+    if torch is None:
+        _use_torch()
     fn, dev, b16, f32, u8 = "moe_layer_fwd_few", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     T, H, E = cfg.T, cfg.H, cfg.E
     w = moe_weights(_dense(fn, dev, Wr, f32, H * E), _dense(fn, dev, bias, f32, E), _dense(fn, dev, packed, u8, 0),

@@ -4,6 +4,8 @@ queries behave as documented (no kernel is launched here)."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -175,3 +177,19 @@ def test_misaligned_pointers_are_rejected():
     st = lib.moe_layer_fwd(ctypes.byref(cfg), ctypes.byref(w), ctypes.c_void_p(good + 2),
                            ctypes.c_void_p(good), None, 0, ctypes.c_void_p(good), s.workspace_fwd, None)
     assert st == moe.MOE_E_INVALID
+
+
+def test_sizing_and_validation_need_no_torch():
+    # what a C program's author has at hand: the build, the sizes and the checks of a cfg
+    code = """
+import sys
+sys.modules["torch"] = None  # any import of it fails
+import dispatch_grouped_gemm_moe_amd as moe
+import dispatch_grouped_gemm_moe_amd.build
+cfg = moe.make_cfg(4, 128, 64, 8, 2)
+assert moe.moe_validate_cfg(cfg) == moe.MOE_OK
+assert moe.moe_query_sizes(cfg).packed_weights > 0
+assert moe.moe_query_few(cfg) > 0 and moe.moe_query_add_rmsnorm_bwd(4, 64) > 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
