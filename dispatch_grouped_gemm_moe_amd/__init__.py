@@ -206,8 +206,16 @@ def moe_read_device_status(ws, stream=None):
     return st, code.value, detail.value
 
 
+def _sizes(fn, rows, cols):
+    """rows and cols, refused where the int64 and int32 of the C call cannot hold them: ctypes would pass
+    their low bits on."""
+    if not (-1 << 31 <= cols < 1 << 31 and -1 << 63 <= rows < 1 << 63):
+        raise MoeError(fn, MOE_E_UNSUPPORTED)
+    return rows, cols
+
+
 def moe_mx_quantize(src, codes, scales, stream=None):
-    rows, cols = src.shape
+    rows, cols = _sizes("moe_mx_quantize", *src.shape)
     _check("moe_mx_quantize", _load().moe_mx_quantize(_ptr(src), rows, cols, _ptr(codes), _ptr(scales),
                                                       _stream(stream)))
 
@@ -259,7 +267,7 @@ def moe_mx_dequantize(codes, scales, dst, operand_scales=False, stream=None):
     if torch is None:
         _use_torch()
     fn, dev, u8 = "moe_mx_dequantize", codes.get_device(), torch.uint8
-    rows, cols = codes.shape
+    rows, cols = _sizes(fn, *codes.shape)
     n_scales = (cols + 127) // 128 * rows * 4 if operand_scales else rows * (cols // 32)
     _call(fn, dev, stream, _dense(fn, dev, codes, u8, 0), _dense(fn, dev, scales, u8, n_scales), rows, cols,
           1 if operand_scales else 0, _dense(fn, dev, dst, torch.bfloat16, rows * cols))
@@ -272,7 +280,7 @@ def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd
     if torch is None:
         _use_torch()
     fn, dev, b16, f32, u8 = "moe_add_rmsnorm_fwd", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
-    rows, cols = x.shape
+    rows, cols = _sizes(fn, *x.shape)
     n = rows * cols
     _call(fn, dev, stream, rows, cols, _dense(fn, dev, x, b16, n), _dense(fn, dev, residual, b16, n),
           _dense(fn, dev, weight, f32, cols), eps, _dense(fn, dev, summed, b16, n), _dense(fn, dev, y, b16, n),
@@ -282,8 +290,8 @@ def moe_add_rmsnorm_fwd(x, weight, y, eps=1e-6, residual=None, summed=None, rstd
 
 
 def moe_query_add_rmsnorm_bwd(rows, cols) -> int:
-    n = ctypes.c_size_t()
-    _check("moe_query_add_rmsnorm_bwd", _load().moe_query_add_rmsnorm_bwd(rows, cols, ctypes.byref(n)))
+    fn, n = "moe_query_add_rmsnorm_bwd", ctypes.c_size_t()
+    _check(fn, _load().moe_query_add_rmsnorm_bwd(*_sizes(fn, rows, cols), ctypes.byref(n)))
     return n.value
 
 
@@ -293,7 +301,7 @@ def moe_add_rmsnorm_bwd(dy, weight, rstd, dx, dweight, ws, summed=None, ck_codes
     if torch is None:
         _use_torch()
     fn, dev, b16, f32, u8 = "moe_add_rmsnorm_bwd", dy.get_device(), torch.bfloat16, torch.float32, torch.uint8
-    rows, cols = dy.shape
+    rows, cols = _sizes(fn, *dy.shape)
     n = rows * cols
     _call(fn, dev, stream, rows, cols, _dense(fn, dev, dy, b16, n), _dense(fn, dev, dsum, b16, n),
           _dense(fn, dev, summed, b16, n), _dense(fn, dev, ck_codes, u8, n),

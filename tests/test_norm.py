@@ -93,6 +93,29 @@ def test_norm_binding_refuses_tensors_the_kernels_cannot_read():
         assert e.value.status == moe.MOE_E_INVALID
 
 
+@pytest.mark.parametrize("rows,cols", [(4, (1 << 32) + 64), (4, 1 << 31), ((1 << 64) + 4, 64), (1 << 63, 64)])
+def test_sizes_that_the_c_types_cannot_hold(rows, cols):
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_query_add_rmsnorm_bwd(rows, cols)
+    assert e.value.status == moe.MOE_E_UNSUPPORTED
+
+
+def test_tensors_of_more_columns_than_the_c_types_hold():
+    # (meta tensors hold no memory; of any other size they are refused as not on a GPU)
+    n = (1 << 32) + 64  # as an int32: 64
+    big = lambda dtype: torch.empty(1, n, dtype=dtype, device="meta")
+    b16, u8, gain = big(torch.bfloat16), big(torch.uint8), torch.empty(n, device="meta")
+    one = torch.empty(1, device="meta")
+    calls = [lambda: moe.moe_add_rmsnorm_fwd(b16, gain, b16, stream=0),
+             lambda: moe.moe_add_rmsnorm_bwd(b16, gain, one, b16, gain, u8, summed=b16, stream=0),
+             lambda: moe.moe_mx_dequantize(u8, u8, b16, stream=0),
+             lambda: moe.moe_mx_quantize(b16, u8, u8, stream=0)]
+    for call in calls:
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == moe.MOE_E_UNSUPPORTED
+
+
 # ------------------------------------------------------------------ GPU
 
 COLS = [32, 64, 96, 128, 224, 512, 544, 1024, 1056, 2080, 4096, 4128, 7168, 8192, 8224, 16384, 32768]
