@@ -935,7 +935,7 @@ moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
     if (!codes || !scales || !dst || rows < 1 || cols < 32 || cols % 32) return MOE_E_INVALID;
     if (operand_scales != 0 && operand_scales != 1) return MOE_E_INVALID;
     if (!aligned(codes, 16) || !aligned(dst, 16)) return MOE_E_INVALID;
-    if (rows >= (1ll << 35) / cols) return MOE_E_UNSUPPORTED;  // one thread per 16 codes, a 32-bit grid
+    if (rows > ((1ll << 35) - 1) / cols) return MOE_E_UNSUPPORTED;  // one thread per 16 codes, a 32-bit grid
     launch_mx_dequant(codes, scales, rows, cols, operand_scales, dst, (hipStream_t)stream);
     return check_launch();
 }

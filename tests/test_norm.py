@@ -116,6 +116,15 @@ def test_tensors_of_more_columns_than_the_c_types_hold():
         assert e.value.status == moe.MOE_E_UNSUPPORTED
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the sizes that are not refused would be launched")
+@pytest.mark.parametrize("cols", [32, 96, 7168, 32800])
+def test_dequantize_refuses_2_to_the_35_codes_and_no_fewer(cols):
+    most = ((1 << 35) - 1) // cols
+    call = lambda rows: moe.lib().moe_mx_dequantize(FAKE, FAKE, rows, cols, 0, FAKE, None)
+    assert call(most) == moe.MOE_E_HIP  # past every check; there is no GPU
+    assert call(most + 1) == moe.MOE_E_UNSUPPORTED
+
+
 # ------------------------------------------------------------------ GPU
 
 COLS = [32, 64, 96, 128, 224, 512, 544, 1024, 1056, 2080, 4096, 4128, 7168, 8192, 8224, 16384, 32768]
