@@ -242,6 +242,13 @@ def _dense(fn, device, t, dtype, n):
     return _data_ptr(t)
 
 
+def _buffer(fn, device, t):
+    """The pointer and the bytes of a dense buffer on `device`, a tensor of any type."""
+    if not _is_contiguous(t) or _get_device(t) != device:
+        raise MoeError(fn, MOE_E_INVALID)
+    return _data_ptr(t), t.nbytes
+
+
 def _call(fn, device, stream, *args):
     """Library function fn(*args, stream) on `device`: the given stream, or that device's current one.  A
     launch goes to the current device's queues, so that one is made current for the call.  Host tensors
@@ -307,7 +314,7 @@ def moe_add_rmsnorm_bwd(dy, weight, rstd, dx, dweight, ws, summed=None, ck_codes
           _dense(fn, dev, summed, b16, n), _dense(fn, dev, ck_codes, u8, n),
           _dense(fn, dev, ck_scales, u8, rows * (cols // 32)), _dense(fn, dev, weight, f32, cols),
           _dense(fn, dev, rstd, f32, rows), _dense(fn, dev, dx, b16, n), _dense(fn, dev, dweight, f32, cols),
-          _dense(fn, dev, ws, u8, 0), ws.numel())
+          *_buffer(fn, dev, ws))
 
 
 def moe_query_few(cfg: moe_cfg) -> int:
@@ -323,11 +330,10 @@ def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=
         _use_torch()
     fn, dev, b16, f32, u8 = "moe_layer_fwd_few", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     T, H, E = cfg.T, cfg.H, cfg.E
-    w = moe_weights(_dense(fn, dev, Wr, f32, H * E), _dense(fn, dev, bias, f32, E), _dense(fn, dev, packed, u8, 0),
-                    packed.numel())
+    w = moe_weights(_dense(fn, dev, Wr, f32, H * E), _dense(fn, dev, bias, f32, E), *_buffer(fn, dev, packed))
     _call(fn, dev, stream, ctypes.byref(cfg), ctypes.byref(w), _dense(fn, dev, x, b16, T * H),
           _dense(fn, dev, x_codes, u8, T * H), _dense(fn, dev, x_scales, u8, (H + 127) // 128 * T * 4),
-          _dense(fn, dev, out, b16, T * H), _dense(fn, dev, ws, u8, 0), ws.numel())
+          _dense(fn, dev, out, b16, T * H), *_buffer(fn, dev, ws))
 
 
 def moe_diag_mfma_loop(kind, operands, blocks, iters, clocks, sink, stream=None):

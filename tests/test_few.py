@@ -412,3 +412,24 @@ def test_few_weights_past_32_bits(gpu_lib, T, prec):
         del packed
     assert got[0].abs().max() > 0.01 and torch.isfinite(got[0]).all()
     assert torch.equal(got[0], got[1])
+
+
+@pytest.mark.gpu
+def test_few_buffers_of_any_type(gpu_lib):
+    # moe_prepare_weights and moe_layer_fwd take packed weights and a workspace of any type, by their bytes
+    few = Few(_wl(5, 128, 64, 8, 2, prec="mxfp8"))
+    want = few()
+
+    def call(packed, ws):
+        out = torch.zeros_like(few.x)
+        moe.moe_layer_fwd_few(few.cfg, few.Wr, few.bias, packed, few.x, out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    for dtype in (torch.int8, torch.bfloat16, torch.int64):
+        packed, ws = few.packed.view(dtype), few.ws.view(dtype)
+        assert torch.equal(call(packed, ws), want)
+        for short in ((packed[:-1], ws), (packed, ws[:-1])):
+            with pytest.raises(moe.MoeError) as e:
+                call(*short)
+            assert e.value.status == moe.MOE_E_WORKSPACE

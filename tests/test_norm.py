@@ -492,3 +492,16 @@ def test_norm_keeps_a_nan_whatever_its_payload(gpu_lib, cols):
     o = _forward(bad, w, r)
     assert torch.isnan(o["summed"][1, :4]).all() and torch.isnan(o["y"][1]).all()
     assert torch.equal(o["y"][0], want["y"][0])
+
+
+@pytest.mark.gpu
+def test_norm_backward_workspace_of_any_type(gpu_lib):
+    x, w = torch.ones(40, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, device="cuda")
+    got = []
+    for dtype in (torch.uint8, torch.float32):
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = torch.empty(moe.moe_query_add_rmsnorm_bwd(40, 64), dtype=torch.uint8, device="cuda").view(dtype)
+        moe.moe_add_rmsnorm_bwd(x, w, torch.ones(40, device="cuda"), dx, dw, ws, summed=x)
+        torch.cuda.synchronize()
+        got.append((dx, dw))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
