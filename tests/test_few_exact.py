@@ -12,13 +12,15 @@ are few such values within 2^20 of each other, rounded once to bf16.
 """
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import dispatch_grouped_gemm_moe_amd as moe
-from few_reference import few_layer
-from moe_inputs import LayerInputs, Workload
-from test_few import Few
+import oracle as O
+from few_reference import HALF_BF16, few_layer
+from moe_inputs import LayerInputs, Workload, make_inputs
+from test_few import Few, test_few_routes_as_the_router_does as routes_as_the_router_does
 
 G = 64  # columns that a token reads at a time
 
@@ -177,6 +179,23 @@ def test_a_column_left_out_changes_the_formulas_outputs(by, shape, prec, shared)
             m.copy_(old)
 
 
+@pytest.mark.parametrize("E,k", [(8, 3), (7, 2)])
+def test_the_routers_second_slab_decides(E, k):
+    # the inputs of the GPU test below: without the columns past 8192 every token's weights are others
+    inp = _slab_inputs(5, 8256, E, k)
+    x = inp.x.float().numpy()
+    _, idx, gw = O.route(x, inp.Wr, None, k)
+    x[:, 8192:] = 0
+    _, idx2, gw2 = O.route(x, inp.Wr, None, k)
+    assert ((idx != idx2).any(1) | (np.abs(gw - gw2).max(1) > 0.01)).all()
+
+
+def _slab_inputs(T, H, E, k):
+    inp = make_inputs(Workload("slab_%d_%d_%d_%d" % (T, H, E, k), T=T, H=H, I=64, E=E, k=k, stream=9800 + E))
+    inp.Wr[H // 8192 * 8192:] *= 10  # the 64 columns of the last slab weigh as much as all the others
+    return inp
+
+
 # ------------------------------------------------------------------ GPU
 
 def _splits(name, *args):
@@ -217,3 +236,29 @@ def test_few_takes_every_column_once(gpu_lib, by, shape, prec, shared):
         wrong = (got != want).nonzero()
         assert len(wrong) == 0, "round %d: %d outputs, the first at %s: %s for %s" % (
             r, len(wrong), wrong[0].tolist(), got[tuple(wrong[0])].item(), want[tuple(wrong[0])].item())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("shape", [(5, 8256, 64, 8, 3), (6, 16448, 64, 7, 2), (3, 8256, 64, 67, 5), (9, 16448, 64, 12, 4)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_few_routes_as_the_router_does_past_a_slab(gpu_lib, shape, prec):
+    routes_as_the_router_does(gpu_lib, shape, prec)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,E,k", [(5, 8256, 8, 3), (5, 8256, 7, 2), (6, 16448, 12, 4), (3, 16448, 67, 5)])
+def test_few_router_by_its_last_slab(gpu_lib, T, H, E, k):
+    # expert e's output is 1 in column e (silu(64) / 64 is 1): the layer's are the routing weights
+    inp = _slab_inputs(T, H, E, k)
+    inp.x[:, 0] = 1
+    for m in (inp.Wg, inp.Wu, inp.Wd):
+        m.zero_()
+    inp.Wg[:, 0, 0], inp.Wu[:, 0, 0] = 64, 1 / 64
+    for e in range(E):
+        inp.Wd[e, 0, e] = 1
+    _, idx, gw = O.route(inp.x.float().numpy(), inp.Wr, None, k)
+    few = Few(inp.w, inp)
+    want = torch.zeros(T, H).scatter_(1, torch.from_numpy(idx.astype(np.int64)), torch.from_numpy(gw.astype(np.float32)))
+    # (the softmax's exp is the device's: 2^-19 relative, besides bf16's half step)
+    assert ((few().cpu().float() - want).abs() <= want * (HALF_BF16 + 2.0 ** -19)).all()
