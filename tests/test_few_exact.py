@@ -262,3 +262,33 @@ def test_few_router_by_its_last_slab(gpu_lib, T, H, E, k):
     want = torch.zeros(T, H).scatter_(1, torch.from_numpy(idx.astype(np.int64)), torch.from_numpy(gw.astype(np.float32)))
     # (the softmax's exp is the device's: 2^-19 relative, besides bf16's half step)
     assert ((few().cpu().float() - want).abs() <= want * (HALF_BF16 + 2.0 ** -19)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 9, 20, 40])
+@pytest.mark.parametrize("I", [64, 192, 1984])
+def test_few_mxfp8_down_product_keeps_what_the_matrix_instruction_keeps(gpu_lib, T, I):
+    """The scaled matrix instruction adds up eight neighbouring products on one exponent: what lies
+    below 2^-13 of the largest is cut off.  Everything else is fp32.  So a sum is off by at most 7 2^-13
+    of the sum of the groups' largest magnitudes, and n 2^-23 of the whole.  Here each group has a large
+    product, which the next group's takes away again, and seven of 2^-14 to 2^-11 of it."""
+    w = _workload(T, 128, I, 2, 2, "mxfp8", False)
+    x, Wg, Wu = torch.zeros(T, 128), torch.zeros(2, 128, I), torch.zeros(2, 128, I)
+    x[:, 0] = 1
+    x[:, 1] = 2.0 ** (torch.arange(T) % 3)
+    Wg[:, 0] = 64
+    i = torch.arange(I)
+    Wu[:, 1] = torch.where(i % 8 == 0, 1.0, 2.0 ** -6)  # h: 64 or 1, times the token's
+    c = torch.arange(128)[None, :]
+    small = 2.0 ** -(5 + c % 4).float() * torch.where((i[:, None] + c) % 5 < 3, 1.0, -1.0)
+    Wd = torch.where(i[:, None] % 8 == 0, torch.where(i[:, None] % 16 == 0, 1.0, -1.0), small).expand(2, I, 128)
+    inp = LayerInputs(w, x.bfloat16(), torch.zeros(128, 2), None, *(m.bfloat16().contiguous() for m in (Wg, Wu, Wd)))
+    h = (64 * inp.x[:, 1:2].double()) * inp.Wu[0, 1].double()
+    W = inp.Wd[0].double()
+    # MXFP8 holds h (64 or 1 of a block's scale) and the weights (1 to 2^-8) exactly
+    want = h @ W
+    mag = h.abs() @ W.abs()
+    largest = (h[:, ::8].abs() @ W[::8].abs())
+    got = Few(w, inp)().double().cpu()
+    bound = 7 * 2.0 ** -13 * largest + I * 2.0 ** -23 * mag
+    assert ((got - want).abs() <= bound + HALF_BF16 * (want.abs() + bound)).all()
