@@ -408,8 +408,10 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t *dy, c
  *       leaves them zero).  One call at a time: calls that overlap on two
  *       streams take a workspace each.
  * cfg->minibatch, ring_slots, comm_cus and the flags other than
- * MOE_F_SHARED_EXPERT have no effect.  MOE_E_UNSUPPORTED for more tokens and
- * in identity-expert mode; MOE_E_INVALID for x_codes with MOE_PREC_BF16.
+ * MOE_F_SHARED_EXPERT have no effect.  A cfg that moe_validate_cfg refuses is
+ * refused alike, its limits on padded rows too (no call makes packed weights for
+ * such a cfg); MOE_E_UNSUPPORTED for more tokens and in identity-expert mode;
+ * MOE_E_INVALID for x_codes with MOE_PREC_BF16.
  * Inputs must be finite: a NaN reaches its own token's output only.
  */
 #define MOE_FEW_MAX_TOKENS 64

@@ -28,6 +28,17 @@ def test_few_refuses_configurations(kw, want):
     assert e.value.status == want
 
 
+@pytest.mark.parametrize("kw", [dict(T=1, E=256, H=32704), dict(T=1, E=256, H=32768), dict(T=1, E=256, I=16384),
+                                dict(T=1, E=128, H=32768, I=8128), dict(T=1, E=2, H=32768, I=32768),
+                                dict(T=1, E=8, H=1 << 20, I=960), dict(T=64, E=8, H=1 << 20, I=1024), dict(minibatch=-1),
+                                dict(T=1, E=240, H=32768, flags=moe.MOE_F_SHARED_EXPERT)])
+@pytest.mark.parametrize("prec", [moe.MOE_PREC_BF16, moe.MOE_PREC_MXFP8])
+def test_few_takes_the_configurations_that_the_weights_can_be_packed_for(kw, prec):
+    cfg = _cfg(prec=prec, **kw)
+    n = ctypes.c_size_t()
+    assert moe.lib().moe_query_few(ctypes.byref(cfg), ctypes.byref(n)) == moe.moe_validate_cfg(cfg)
+
+
 def test_few_workspace_depends_on_the_layer_only():
     base = moe.moe_query_few(_cfg())
     assert base % 256 == 0 and base >= 8 * 2 * 128 * 4
