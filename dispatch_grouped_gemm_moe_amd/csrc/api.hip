@@ -940,7 +940,7 @@ moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
     return check_launch();
 }
 
-// Limits of the norm's sizes (a row in a workgroup's registers, a 32-bit grid).
+// Limits of the norm's sizes (kNormMaxCols: a workgroup's registers; rows: a 32-bit grid).
 static moe_status check_norm(int64_t rows, int32_t cols) {
     if (rows < 1 || cols < 32 || cols % 32) return MOE_E_INVALID;
     if (cols > kNormMaxCols || rows > (1 << 21)) return MOE_E_UNSUPPORTED;

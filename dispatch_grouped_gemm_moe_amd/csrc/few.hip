@@ -9,7 +9,7 @@
 // HBM once (3 H I values per expert), not arithmetic.  The tiles of the layer
 // kernel spend 128 padded rows per expert; here the weight rows are the M side
 // of 16-wide MFMAs and the expert's tokens the N side, so 16 tokens ride on
-// every weight fragment and nothing is padded past 16 rows.
+// every weight fragment and an expert's rows are padded to 16, 32 or 64 only.
 //
 // Three launches: the router (logits, top-k, expert row lists), the gate|up
 // product with SwiGLU, and the down product with the weighted sum; past 16
@@ -18,12 +18,13 @@
 // 5.5 over the gate|up product's 44 us), 64 bf16 tokens of the same sizes 537 us
 // (2.82 GB, 5.3 TB/s).
 //
-// Two other forms of the products were built and measured on that one token, then
-// 85 us: all three in one launch with tiles handed out by a ticket, down tiles
-// waiting on counters, took 159 us (atomics on one cache line complete one per
-// 30 ns); workgroups that stay and ask for their next tile's weights before they
-// reduce the present one, 82 us, and 343 us against 301 us for 16 tokens with the
-// shared expert, by register spills.
+// Two other forms of the products were built and measured on that one token,
+// then 85 us: all three in one launch with tiles handed out by a ticket, down
+// tiles waiting on counters, took 159 us (the ticket and the counters shared a
+// cache line, on which atomics complete one per 30 ns; with a line each, as the
+// counters have now, it was not built again); workgroups that stay and ask for
+// their next tile's weights before they reduce the present one, 82 us, and 343
+// us against 301 us for 16 tokens with the shared expert, by register spills.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "mxfp8.hpp"

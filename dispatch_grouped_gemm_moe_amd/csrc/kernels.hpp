@@ -403,7 +403,8 @@ void launch_few_combine(const FewGemm& a, int k, int shared, uint16_t* out, hipS
 
 // ---- residual addition and root-mean-square norm (norm.hip) ----
 
-constexpr int kNormMaxCols = 32768;  // a row stays in a workgroup's registers
+// sixteen waves of four vectors a lane: the row (forward) or dw's sums (backward) in registers
+constexpr int kNormMaxCols = 32768;
 
 struct NormFwd {
     int64_t rows;

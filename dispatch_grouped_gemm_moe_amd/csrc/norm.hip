@@ -4,10 +4,11 @@
 //   dx = dsum + rstd * (dy w - xhat mean(dy w xhat)),  xhat = s * rstd
 //   dw = sum over rows of dy * xhat
 //
-// All of it is bound by memory: a few operations per value.  A row is read
-// once and kept in registers between its sum and its output.  A thread holds
-// vectors of eight consecutive values (16 bytes of bf16), so an MXFP8 block of
-// 32 is four neighbouring lanes.
+// All of it is bound by memory: a few operations per value.  A row is read once
+// and kept in registers between its sum and its output; only the backward of
+// rows past 16384 columns reads them twice.  A thread holds vectors of eight
+// consecutive values (16 bytes of bf16), so an MXFP8 block of 32 is four
+// neighbouring lanes.
 #include "common.hpp"
 #include "kernels.hpp"
 #include "mxfp8.hpp"
@@ -81,8 +82,9 @@ __device__ __forceinline__ uint64_t block_codes(const float (&v)[8], uint8_t& sc
 }
 
 // A row per group of kWaves waves, kNV vectors per thread, or (kWaves = 1) of
-// kLanes lanes, 256 / kLanes rows in a workgroup: 262144 rows of 128 take 42 us
-// (6.4 TB/s) with 16 lanes a row and 92 us with 64.
+// kLanes lanes, 256 / kLanes rows in a workgroup: 262144 rows of 128 with the
+// residual and its sum take 48 us (5.5 TB/s) with 16 lanes a row.  On inputs that the
+// last cache held in part it was 42 us, against 92 with 64 lanes.
 template <int kWaves, int kNV, int kLanes>
 __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_fwd_kernel(NormFwd a) {
     __shared__ float s_sum[kWaves];
@@ -311,9 +313,10 @@ __global__ __launch_bounds__(kBwdWaves * kWave) void norm_bwd_kernel(NormBwd a) 
 
 // The same for rows past 16384, sixteen waves and up to four vectors a lane: 128
 // registers a lane hold dw's sums but not the row, which is read again after its
-// sum (from the L2 or the cache behind it): 2048 rows of 32768 170 us (3.2 TB/s).
-// Eight waves of eight vectors that keep it spill, and so do sixteen of four:
-// 324 and 265 us.
+// sum (from the L2 or the cache behind it): 2048 rows of 32768 149 us (3.6 TB/s of
+// what has to move).  Eight waves of eight vectors that keep the row as fp32 xhat,
+// g and dsum (24 registers a vector) spill, and so do sixteen of four: 324 and 265
+// us.  A row kept as it lies in memory (8 a vector) has not been built.
 template <bool kCk>
 __global__ __launch_bounds__(kWideWaves * kWave) void norm_bwd_wide_kernel(NormBwd a) {
     constexpr int kNV = 4, kThreads = kWideWaves * kWave;
@@ -390,13 +393,14 @@ __global__ __launch_bounds__(kWideWaves * kWave) void norm_bwd_wide_kernel(NormB
     }
 }
 
-// The same for rows that one wave holds: kLanes lanes a row, 256 / kLanes rows of
-// a workgroup side by side, so that narrow rows (a head's) fill their lanes and
-// no barrier stands in the loop.  The rows' sums of dw meet in LDS at the end.
-// Against a workgroup a row: 262144 rows of 128 377 -> 47 us (5.7 TB/s), 65536 of
-// 512 103 -> 45 us, 16384 of 1024 37 -> 26 us.  Rows of 2048 would need four
-// vectors a lane and 256 registers: 4096 of them from the checkpoint take 21 us
-// that way and 18 us with a workgroup each.
+// The same for rows that one wave holds: kLanes lanes a row, 256 / kLanes rows
+// of a workgroup side by side, so that narrow rows (a head's) fill their lanes
+// and no barrier stands in the loop.  The rows' sums of dw meet in LDS at the
+// end. Against a workgroup a row, on inputs that the last cache holds in part:
+// 262144 rows of 128 377 -> 47 us, 65536 of 512 103 -> 45 us, 16384 of 1024 37
+// -> 26 us; on three such inputs in turn the first two take 52 us (5.1 TB/s).
+// Rows of 2048 would need four vectors a lane and 256 registers: 4096 of them
+// from the checkpoint take 21 us that way and 18 us with a workgroup each.
 template <int kLanes, int kNV, bool kCk>
 __global__ __launch_bounds__(256) void norm_bwd_narrow_kernel(NormBwd a) {
     constexpr int kRows = 256 / kLanes;

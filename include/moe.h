@@ -218,6 +218,8 @@ moe_status moe_dispatch_layout(const moe_cfg *cfg, const int32_t *topk_idx, int3
  * reused as soon as combine has sent a batch's results, with no CPU round trip).
  *   out[t] = sum_j topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t])  (+ shared FFN(x[t]))
  *   FFN_e(v) = (silu(v Wg[e]) * (v Wu[e])) Wd[e],  silu(z) = z / (1 + exp(-z))
+ * For up to MOE_FEW_MAX_TOKENS tokens without a backward moe_layer_fwd_few is
+ * the faster call (1.6 to 8 times, measured at two layer sizes).
  *   x [T,H] bf16, out [T,H] bf16.
  *   saved: NULL, or at least moe_sizes.saved bytes that moe_layer_bwd will read.
  *       It starts with the routing of every token: topk_idx [T,k] int32 at
