@@ -444,3 +444,18 @@ def test_few_buffers_of_any_type(gpu_lib):
             with pytest.raises(moe.MoeError) as e:
                 call(*short)
             assert e.value.status == moe.MOE_E_WORKSPACE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 20])
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+def test_few_a_nan_of_any_payload_spoils_its_token(gpu_lib, prec, T):
+    w = _wl(T, 256, 64, 4, 4, prec=prec, shared=True)  # every expert: the others' sums keep their order
+    few = Few(w)
+    want = few()
+    keep = torch.arange(T, device="cuda") != 3
+    for bits in (0x7FFF, -1, 0x7F81, -0x7F, 0x7FC0):
+        x = few.x.clone()
+        x.view(torch.int16)[3, 17] = bits
+        got = few(x)
+        assert torch.isnan(got[3]).all() and torch.equal(got[keep], want[keep]), hex(bits)
