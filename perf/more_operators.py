@@ -259,7 +259,7 @@ def prepare(case, seed):
         st["max_norm"] = 0.01 + 1e-4 * (seed % 7)
         if own:
             import dispatch_grouped_gemm_moe_amd as moe
-            st["ws"] = torch.empty(moe.moe_query_grad_norm(len(st["grads"])), dtype=torch.uint8, device="cuda")
+            st["ws"] = torch.zeros(moe.moe_query_grad_norm(len(st["grads"])), dtype=torch.uint8, device="cuda")
     return st
 
 
