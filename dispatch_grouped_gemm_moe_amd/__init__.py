@@ -30,7 +30,9 @@ EXPORTS = ("moe_status_string", "moe_abi_version", "moe_validate_cfg", "moe_quer
            "moe_layer_bwd", "moe_read_device_status", "moe_mx_quantize", "moe_timing_enable",
            "moe_timing_read", "moe_diag_mfma_loop", "moe_layer_fwd_static", "moe_mx_dequantize",
            "moe_add_rmsnorm_fwd", "moe_add_rmsnorm_bwd", "moe_query_add_rmsnorm_bwd", "moe_layer_fwd_few",
-           "moe_query_few")
+           "moe_query_few", "moe_dispatch_rows", "moe_combine_rows", "moe_combine_rows_bwd", "moe_block_quantize",
+           "moe_block_quantize_weights", "moe_block_dequantize", "moe_block_gemm", "moe_query_block_swiglu",
+           "moe_block_gemm_swiglu", "moe_query_grad_norm", "moe_grad_norm", "moe_clip_grads")
 MOE_STATIC_WORKSPACE_BYTES = 256 << 20
 MOE_FEW_MAX_TOKENS, MOE_FEW_COUNTER_BYTES = 64, 36864
 KERNEL_KINDS = ("route", "layout", "gemm_gate_up", "gemm_down", "combine", "gather", "other", "wgrad",
@@ -77,7 +79,7 @@ def _load():
             raise ImportError("HIP library %s is missing: build it with "
                               "`python -m dispatch_grouped_gemm_moe_amd.build`" % path)
         lib = ctypes.CDLL(path)
-        P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         cfgp = ctypes.POINTER(moe_cfg)
         sig = {
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -103,6 +105,18 @@ def _load():
             "moe_add_rmsnorm_bwd": (ctypes.c_int, [ctypes.c_int64, I32, P, P, P, P, P, P, P, P, P, P, SZ, P]),
             "moe_layer_fwd_few": (ctypes.c_int, [cfgp, ctypes.POINTER(moe_weights), P, P, P, P, P, SZ, P]),
             "moe_query_few": (ctypes.c_int, [cfgp, ctypes.POINTER(SZ)]),
+            "moe_dispatch_rows": (ctypes.c_int, [I64, I32, I32, I64, P, P, P, P, P, P]),
+            "moe_combine_rows": (ctypes.c_int, [I64, I32, I32, I64, P, P, P, P, P, P]),
+            "moe_combine_rows_bwd": (ctypes.c_int, [I64, I32, I32, I64, P, P, P, P, P, P, P, P, P]),
+            "moe_block_quantize": (ctypes.c_int, [I64, I32, P, P, P, P]),
+            "moe_block_quantize_weights": (ctypes.c_int, [I32, I32, I32, P, I32, P, P, P]),
+            "moe_block_dequantize": (ctypes.c_int, [I64, I32, I32, P, P, P, P]),
+            "moe_block_gemm": (ctypes.c_int, [I64, I32, I32, I32, P, P, P, P, P, P, P]),
+            "moe_query_block_swiglu": (ctypes.c_int, [I64, I32, I32, I32, ctypes.POINTER(SZ)]),
+            "moe_block_gemm_swiglu": (ctypes.c_int, [I64, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "moe_query_grad_norm": (ctypes.c_int, [I32, ctypes.POINTER(SZ)]),
+            "moe_grad_norm": (ctypes.c_int, [I32, P, P, P, P, P, SZ, P]),
+            "moe_clip_grads": (ctypes.c_int, [I32, P, P, P, P, ctypes.c_float, P, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -334,6 +348,191 @@ def moe_layer_fwd_few(cfg, Wr, bias, packed, x, out, ws, x_codes=None, x_scales=
     _call(fn, dev, stream, ctypes.byref(cfg), ctypes.byref(w), _dense(fn, dev, x, b16, T * H),
           _dense(fn, dev, x_codes, u8, T * H), _dense(fn, dev, x_scales, u8, (H + 127) // 128 * T * 4),
           _dense(fn, dev, out, b16, T * H), *_buffer(fn, dev, ws))
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def moe_dispatch_rows(x, tok_row, dst=None, codes=None, scales=None, stream=None):
+    """Row tok_row[t, j] = x[t] for each of the k choices j: of dst (bf16), and / or of codes and scales
+    (moe_block_quantize's); rows outside theirs are no rows."""
+    if torch is None:
+        _use_torch()
+    fn, dev, b16, f32, u8 = "moe_dispatch_rows", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
+    T, cols = _sizes(fn, *x.shape)
+    k = tok_row.shape[1]
+    R = (codes if dst is None else dst).shape[0] if dst is not None or codes is not None else 0
+    _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, x, b16, 0), _dense(fn, dev, tok_row, torch.int32, T * k),
+          _dense(fn, dev, dst, b16, R * cols), _dense(fn, dev, codes, u8, R * cols),
+          _dense(fn, dev, scales, f32, _blocks(cols) * R))
+
+
+def moe_combine_rows(src, tok_row, out, topk_w=None, add=None, stream=None):
+    """out[t] = add[t] + sum over j of topk_w[t, j] src[tok_row[t, j]]; without topk_w the weights are 1,
+    which is the gradient of moe_dispatch_rows."""
+    if torch is None:
+        _use_torch()
+    fn, dev, b16, f32 = "moe_combine_rows", src.get_device(), torch.bfloat16, torch.float32
+    R, cols = _sizes(fn, *src.shape)
+    T, k = tok_row.shape
+    _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, src, b16, 0), _dense(fn, dev, tok_row, torch.int32, 0),
+          _dense(fn, dev, topk_w, f32, T * k), _dense(fn, dev, add, b16, T * cols), _dense(fn, dev, out, b16, T * cols))
+
+
+def moe_combine_rows_bwd(dout, tok_row, src=None, topk_w=None, dsrc=None, dw=None, codes=None, scales=None,
+                         stream=None):
+    """dsrc[tok_row[t, j]] = topk_w[t, j] dout[t] (bf16, and / or its codes and scales) and
+    dw[t, j] = <src[tok_row[t, j]], dout[t]>."""
+    if torch is None:
+        _use_torch()
+    fn, dev, b16, f32, u8 = "moe_combine_rows_bwd", dout.get_device(), torch.bfloat16, torch.float32, torch.uint8
+    T, cols = _sizes(fn, *dout.shape)
+    k = tok_row.shape[1]
+    rows = [t.shape[0] for t in (src, dsrc, codes) if t is not None]
+    R = min(rows) if rows else 0
+    _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, dout, b16, 0), _dense(fn, dev, src, b16, R * cols),
+          _dense(fn, dev, tok_row, torch.int32, T * k), _dense(fn, dev, topk_w, f32, T * k),
+          _dense(fn, dev, dsrc, b16, R * cols), _dense(fn, dev, codes, u8, R * cols),
+          _dense(fn, dev, scales, f32, _blocks(cols) * R), _dense(fn, dev, dw, f32, T * k))
+
+
+def moe_block_quantize(src, codes, scales, stream=None):
+    """codes [rows, cols] and scales [ceil(cols / 128), rows] of src (bf16) in blocks of 1 x 128."""
+    if torch is None:
+        _use_torch()
+    fn, dev = "moe_block_quantize", src.get_device()
+    rows, cols = _sizes(fn, *src.shape)
+    _call(fn, dev, stream, rows, cols, _dense(fn, dev, src, torch.bfloat16, 0),
+          _dense(fn, dev, codes, torch.uint8, rows * cols),
+          _dense(fn, dev, scales, torch.float32, _blocks(cols) * rows))
+
+
+def moe_block_quantize_weights(src, codes, scales, transposed=False, stream=None):
+    """codes [groups, n, k] and scales [groups, ceil(n / 128), ceil(k / 128)] in blocks of 128 x 128 of src
+    (bf16) [groups, n, k], or with transposed [groups, k, n]."""
+    if torch is None:
+        _use_torch()
+    fn, dev = "moe_block_quantize_weights", src.get_device()
+    groups, n, k = codes.shape
+    if max(groups, n, k) >= 1 << 31:
+        raise MoeError(fn, MOE_E_UNSUPPORTED)
+    _call(fn, dev, stream, groups, n, k, _dense(fn, dev, src, torch.bfloat16, groups * n * k), 1 if transposed else 0,
+          _dense(fn, dev, codes, torch.uint8, 0),
+          _dense(fn, dev, scales, torch.float32, groups * _blocks(n) * _blocks(k)))
+
+
+def moe_block_dequantize(codes, scales, dst, weights=False, stream=None):
+    """dst (bf16) = the values of codes [rows, cols] and their scales, or with weights of codes [groups, n, k]."""
+    if torch is None:
+        _use_torch()
+    fn, dev = "moe_block_dequantize", codes.get_device()
+    n = codes.shape[-2] if weights else 0
+    rows, cols = _sizes(fn, codes.shape[0] * n if weights else codes.shape[0], codes.shape[-1])
+    n_scales = codes.shape[0] * _blocks(n) * _blocks(cols) if weights else _blocks(cols) * rows
+    if n >= 1 << 31:
+        raise MoeError(fn, MOE_E_UNSUPPORTED)
+    _call(fn, dev, stream, rows, cols, n, _dense(fn, dev, codes, torch.uint8, rows * cols),
+          _dense(fn, dev, scales, torch.float32, n_scales), _dense(fn, dev, dst, torch.bfloat16, rows * cols))
+
+
+def _block_operands(fn, dev, a, a_scales, offsets, w):
+    """The sizes of a product and the pointers of its rows: (rows, n, k, groups), (a, a_scales, offsets)."""
+    rows, k = _sizes(fn, *a.shape)
+    groups, n, kw = w.shape
+    if kw != k:
+        raise MoeError(fn, MOE_E_INVALID)
+    if max(groups, n) >= 1 << 31:
+        raise MoeError(fn, MOE_E_UNSUPPORTED)
+    return (rows, n, k, groups), (_dense(fn, dev, a, torch.uint8, 0),
+                                  _dense(fn, dev, a_scales, torch.float32, _blocks(k) * rows),
+                                  _dense(fn, dev, offsets, torch.int32, groups + 1))
+
+
+def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None):
+    """out [rows, n] (bf16) = rows of a [rows, k] times their group's matrix w [groups, n, k], both codes in
+    blocks of 128 with their scales; group g's rows are offsets[g] .. offsets[g + 1] - 1."""
+    if torch is None:
+        _use_torch()
+    fn, dev = "moe_block_gemm", a.get_device()
+    (rows, n, k, groups), ptrs = _block_operands(fn, dev, a, a_scales, offsets, w)
+    _call(fn, dev, stream, rows, n, k, groups, *ptrs, _dense(fn, dev, w, torch.uint8, 0),
+          _dense(fn, dev, w_scales, torch.float32, groups * _blocks(n) * _blocks(k)),
+          _dense(fn, dev, out, torch.bfloat16, rows * n))
+
+
+def moe_query_block_swiglu(rows, n, k, groups) -> int:
+    fn, size = "moe_query_block_swiglu", ctypes.c_size_t()
+    if max(n, k, groups) >= 1 << 31 or rows >= 1 << 63:
+        raise MoeError(fn, MOE_E_UNSUPPORTED)
+    _check(fn, _load().moe_query_block_swiglu(rows, n, k, groups, ctypes.byref(size)))
+    return size.value
+
+
+def moe_block_gemm_swiglu(a, a_scales, wg, wg_scales, wu, wu_scales, h_codes, h_scales, ws, h=None, offsets=None,
+                          stream=None):
+    """h = silu(a wg) * (a wu), each as moe_block_gemm's product, in codes h_codes [rows, n] and scales h_scales
+    [ceil(n / 128), rows], and in bf16 where h is given; ws: moe_query_block_swiglu bytes."""
+    if torch is None:
+        _use_torch()
+    fn, dev, f32, u8 = "moe_block_gemm_swiglu", a.get_device(), torch.float32, torch.uint8
+    (rows, n, k, groups), ptrs = _block_operands(fn, dev, a, a_scales, offsets, wg)
+    n_w, n_s = groups * n * k, groups * _blocks(n) * _blocks(k)
+    _call(fn, dev, stream, rows, n, k, groups, *ptrs, _dense(fn, dev, wg, u8, 0), _dense(fn, dev, wg_scales, f32, n_s),
+          _dense(fn, dev, wu, u8, n_w), _dense(fn, dev, wu_scales, f32, n_s), _dense(fn, dev, h_codes, u8, rows * n),
+          _dense(fn, dev, h_scales, f32, _blocks(n) * rows), _dense(fn, dev, h, torch.bfloat16, rows * n),
+          *_buffer(fn, dev, ws))
+
+
+def moe_query_grad_norm(tensors) -> int:
+    """Bytes of moe_grad_norm's workspace for so many tensors; its first 256 are zeroed once by the caller."""
+    fn, n = "moe_query_grad_norm", ctypes.c_size_t()
+    if not 0 <= tensors < 1 << 31:
+        raise MoeError(fn, MOE_E_INVALID)
+    _check(fn, _load().moe_query_grad_norm(tensors, ctypes.byref(n)))
+    return n.value
+
+
+def _grad_arrays(fn, dev, grads, like=None):
+    """C arrays of the tensors' pointers, and (without `like`, whose sizes and types they must have) of their
+    element counts and types."""
+    n = len(grads)
+    ptrs = (ctypes.c_void_p * n)()
+    counts, kinds = (ctypes.c_int64 * n)(), (ctypes.c_uint8 * n)()
+    for i, t in enumerate(grads):
+        if t.dtype is torch.bfloat16:
+            kinds[i] = 1
+        elif t.dtype is not torch.float32:
+            raise MoeError(fn, MOE_E_INVALID)
+        if not _is_contiguous(t) or _get_device(t) != dev:
+            raise MoeError(fn, MOE_E_INVALID)
+        if like is not None and (t.dtype is not like[i].dtype or _numel(t) != _numel(like[i])):
+            raise MoeError(fn, MOE_E_INVALID)
+        ptrs[i], counts[i] = _data_ptr(t), _numel(t)
+    return ptrs, counts, kinds
+
+
+def moe_grad_norm(grads, norm, ws, stream=None):
+    """norm (one fp32 element) = the norm of all tensors' (fp32 or bf16) elements together; ws:
+    moe_query_grad_norm bytes, the first 256 of them zeroed once."""
+    if torch is None:
+        _use_torch()
+    fn, dev = "moe_grad_norm", norm.get_device()
+    ptrs, counts, kinds = _grad_arrays(fn, dev, grads)
+    _call(fn, dev, stream, len(grads), ptrs, counts, kinds, _dense(fn, dev, norm, torch.float32, 1),
+          *_buffer(fn, dev, ws))
+
+
+def moe_clip_grads(grads, norm, max_norm, out=None, stream=None):
+    """out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), in place without out; norm as moe_grad_norm wrote it."""
+    if torch is None:
+        _use_torch()
+    fn, dev = "moe_clip_grads", norm.get_device()
+    ptrs, counts, kinds = _grad_arrays(fn, dev, grads)
+    if out is not None and len(out) != len(grads):
+        raise MoeError(fn, MOE_E_INVALID)
+    outs = ptrs if out is None else _grad_arrays(fn, dev, out, grads)[0]
+    _call(fn, dev, stream, len(grads), ptrs, counts, kinds, _dense(fn, dev, norm, torch.float32, 1), max_norm, outs)
 
 
 def moe_diag_mfma_loop(kind, operands, blocks, iters, clocks, sink, stream=None):

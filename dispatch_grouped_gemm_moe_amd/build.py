@@ -16,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "libmoe_mi355x.so"
 SOURCES = ["api.hip", "route.hip", "gemm.hip", "bwd.hip", "mx.hip", "mega.hip", "few.hip", "norm.hip",
+           "rows.hip", "block.hip", "grad.hip",
            "diag.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

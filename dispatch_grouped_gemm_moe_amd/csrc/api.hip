@@ -995,6 +995,222 @@ moe_status moe_add_rmsnorm_bwd(int64_t rows, int32_t cols, const uint16_t* dy, c
     return check_launch();
 }
 
+// ---- rows by expert and back ----
+
+static moe_status check_rows(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint8_t* codes,
+                             const float* scales, const int32_t* tok_row) {
+    if (tokens < 1 || k < 1 || cols < 8 || rows < 1 || cols % (codes ? 16 : 8)) return MOE_E_INVALID;
+    if (k > kMaxTopK || cols > (1 << 20) || tokens > (1 << 30) / k || rows > (1 << 30)) return MOE_E_UNSUPPORTED;
+    if (!codes != !scales || !tok_row || !aligned(tok_row, 4) || !aligned(codes, 16) || !aligned(scales, 4))
+        return MOE_E_INVALID;
+    return MOE_OK;
+}
+
+moe_status moe_dispatch_rows(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint16_t* x,
+                             const int32_t* tok_row, uint16_t* dst, uint8_t* codes, float* scales, void* stream) {
+    moe_status st = check_rows(tokens, k, cols, rows, codes, scales, tok_row);
+    if (st != MOE_OK) return st;
+    if (!x || (!dst && !codes) || !aligned(x, 16) || !aligned(dst, 16)) return MOE_E_INVALID;
+    RowsDispatch a{};
+    a.tokens = tokens; a.rows = rows; a.cols = cols; a.k = k; a.x = x; a.tok_row = tok_row; a.dst = dst;
+    a.codes = codes; a.scales = scales;
+    TIMED(MOE_K_GATHER, (hipStream_t)stream, launch_rows_dispatch(a, (hipStream_t)stream));
+    return check_launch();
+}
+
+moe_status moe_combine_rows(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint16_t* src,
+                            const int32_t* tok_row, const float* w, const uint16_t* add, uint16_t* out, void* stream) {
+    moe_status st = check_rows(tokens, k, cols, rows, nullptr, nullptr, tok_row);
+    if (st != MOE_OK) return st;
+    if (!src || !out || !aligned(src, 16) || !aligned(w, 4) || !aligned(add, 16) || !aligned(out, 16))
+        return MOE_E_INVALID;
+    RowsCombine a{};
+    a.tokens = tokens; a.rows = rows; a.cols = cols; a.k = k; a.src = src; a.tok_row = tok_row; a.w = w; a.add = add;
+    a.out = out;
+    TIMED(MOE_K_COMBINE, (hipStream_t)stream, launch_rows_combine(a, (hipStream_t)stream));
+    return check_launch();
+}
+
+moe_status moe_combine_rows_bwd(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint16_t* dout,
+                                const uint16_t* src, const int32_t* tok_row, const float* w, uint16_t* dsrc,
+                                uint8_t* codes, float* scales, float* dw, void* stream) {
+    moe_status st = check_rows(tokens, k, cols, rows, codes, scales, tok_row);
+    if (st != MOE_OK) return st;
+    if (!dout || (!dsrc && !codes && !dw) || (dw && !src)) return MOE_E_INVALID;
+    if (!aligned(dout, 16) || !aligned(src, 16) || !aligned(w, 4) || !aligned(dsrc, 16) || !aligned(dw, 4))
+        return MOE_E_INVALID;
+    RowsCombineBwd a{};
+    a.tokens = tokens; a.rows = rows; a.cols = cols; a.k = k; a.dout = dout; a.src = src; a.tok_row = tok_row; a.w = w;
+    a.dsrc = dsrc; a.codes = codes; a.scales = scales; a.dw = dw;
+    TIMED(MOE_K_COMBINE, (hipStream_t)stream, launch_rows_combine_bwd(a, (hipStream_t)stream));
+    return check_launch();
+}
+
+// ---- blocks of 128 ----
+
+moe_status moe_block_quantize(int64_t rows, int32_t cols, const uint16_t* src, uint8_t* codes, float* scales,
+                              void* stream) {
+    if (rows < 1 || cols < 16 || cols % 16 || !src || !codes || !scales) return MOE_E_INVALID;
+    if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_E_INVALID;
+    if (rows > (1 << 30) || cols > (1 << 20)) return MOE_E_UNSUPPORTED;
+    RowsDispatch a{};
+    a.tokens = rows; a.rows = rows; a.cols = cols; a.k = 1; a.x = src; a.codes = codes; a.scales = scales;
+    TIMED(MOE_K_GATHER, (hipStream_t)stream, launch_rows_dispatch(a, (hipStream_t)stream));
+    return check_launch();
+}
+
+moe_status moe_block_quantize_weights(int32_t groups, int32_t n, int32_t k, const uint16_t* src, int32_t transposed,
+                                      uint8_t* codes, float* scales, void* stream) {
+    if (groups < 1 || n < 1 || k < 16 || k % 16 || (transposed != 0 && transposed != 1)) return MOE_E_INVALID;
+    if ((transposed && n % 8) || !src || !codes || !scales) return MOE_E_INVALID;
+    if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_E_INVALID;
+    if ((int64_t)groups * n > (1 << 30) || (int64_t)n * k >= (1ll << 31)) return MOE_E_UNSUPPORTED;
+    TIMED(MOE_K_OTHER, (hipStream_t)stream,
+          launch_block_quant_weights(src, groups, n, k, transposed, codes, scales, (hipStream_t)stream));
+    return check_launch();
+}
+
+moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uint8_t* codes, const float* scales,
+                                uint16_t* dst, void* stream) {
+    if (rows < 1 || cols < 16 || cols % 16 || n < 0 || (n && rows % n) || !codes || !scales || !dst)
+        return MOE_E_INVALID;
+    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(dst, 16)) return MOE_E_INVALID;
+    if (rows > (1 << 30) || (n == 0 && cols > (1 << 20)) || (int64_t)n * cols >= (1ll << 31)) return MOE_E_UNSUPPORTED;
+    TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_block_dequant(codes, scales, rows, cols, n, dst, (hipStream_t)stream));
+    return check_launch();
+}
+
+static moe_status check_block(int64_t rows, int32_t n, int32_t k, int32_t groups, int n_step) {
+    if (rows < 1 || n < 1 || n % n_step || k < 16 || k % 16 || groups < 1) return MOE_E_INVALID;
+    if (rows > (1 << 24) || groups > (1 << 16) || n > (1 << 20) || k > (1 << 20) || (int64_t)n * k >= (1ll << 31))
+        return MOE_E_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status moe_block_gemm(int64_t rows, int32_t n, int32_t k, int32_t groups, const uint8_t* a, const float* a_scales,
+                          const int32_t* offsets, const uint8_t* w, const float* w_scales, uint16_t* out,
+                          void* stream) {
+    moe_status st = check_block(rows, n, k, groups, 8);
+    if (st != MOE_OK) return st;
+    if (!a || !a_scales || !w || !w_scales || !out || (!offsets && groups > 1)) return MOE_E_INVALID;
+    if (!aligned(a, 16) || !aligned(a_scales, 4) || !aligned(offsets, 4) || !aligned(w, 16) || !aligned(w_scales, 4) ||
+        !aligned(out, 16))
+        return MOE_E_INVALID;
+    BlockGemm g{};
+    g.rows = (int)rows; g.n = n; g.k = k; g.groups = groups; g.a = a; g.sa = a_scales; g.offsets = offsets; g.w = w;
+    g.sw = w_scales; g.out = out;
+    TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_block_gemm_few(g, (hipStream_t)stream));
+    return check_launch();
+}
+
+moe_status moe_query_block_swiglu(int64_t rows, int32_t n, int32_t k, int32_t groups, size_t* workspace) {
+    if (!workspace) return MOE_E_INVALID;
+    moe_status st = check_block(rows, n, k, groups, 16);
+    if (st != MOE_OK) return st;
+    *workspace = align_up((size_t)rows * n * 4);
+    return MOE_OK;
+}
+
+moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t groups, const uint8_t* a,
+                                 const float* a_scales, const int32_t* offsets, const uint8_t* wg,
+                                 const float* wg_scales, const uint8_t* wu, const float* wu_scales, uint8_t* h_codes,
+                                 float* h_scales, uint16_t* h, void* ws, size_t ws_bytes, void* stream) {
+    size_t need = 0;
+    moe_status st = moe_query_block_swiglu(rows, n, k, groups, &need);
+    if (st != MOE_OK) return st;
+    if (!a || !a_scales || !wg || !wg_scales || !wu || !wu_scales || !h_codes || !h_scales || !ws ||
+        (!offsets && groups > 1))
+        return MOE_E_INVALID;
+    if (!aligned(a, 16) || !aligned(a_scales, 4) || !aligned(offsets, 4) || !aligned(wg, 16) || !aligned(wg_scales, 4) ||
+        !aligned(wu, 16) || !aligned(wu_scales, 4) || !aligned(h_codes, 16) || !aligned(h_scales, 4) ||
+        !aligned(h, 16) || !aligned(ws, 16))
+        return MOE_E_INVALID;
+    if (ws_bytes < need) return MOE_E_WORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    BlockGemm g{};
+    g.rows = (int)rows; g.n = n; g.k = k; g.groups = groups; g.a = a; g.sa = a_scales; g.offsets = offsets; g.w = wg;
+    g.sw = wg_scales; g.wu = wu; g.swu = wu_scales; g.h = (float*)ws;
+    TIMED(MOE_K_OTHER, s, launch_block_gemm_few(g, s));
+    RowsDispatch q{};
+    q.tokens = rows; q.rows = rows; q.cols = n; q.k = 1; q.xf = (const float*)ws; q.codes = h_codes; q.scales = h_scales;
+    q.dst = h; q.offsets = offsets; q.groups = groups;
+    TIMED(MOE_K_GATHER, s, launch_rows_dispatch(q, s));
+    return check_launch();
+}
+
+// ---- gradient norm and clipping ----
+
+constexpr size_t kGradCounterBytes = 256;
+
+moe_status moe_query_grad_norm(int32_t tensors, size_t* workspace) {
+    if (!workspace || tensors < 1) return MOE_E_INVALID;
+    if (tensors > (1 << 20)) return MOE_E_UNSUPPORTED;
+    const size_t launches = ((size_t)tensors + kGradTensors - 1) / kGradTensors;
+    *workspace = kGradCounterBytes + launches * kGradSlots * sizeof(double);
+    return MOE_OK;
+}
+
+// Whether the tensors of one call can be read (and written to out, where out is given).
+static moe_status check_grads(int32_t tensors, const void* const* grads, const int64_t* counts, const uint8_t* is_bf16,
+                              void* const* out, bool with_out) {
+    if (tensors < 1 || !grads || !counts || (with_out && !out)) return MOE_E_INVALID;
+    if (tensors > (1 << 20)) return MOE_E_UNSUPPORTED;
+    for (int32_t i = 0; i < tensors; ++i) {
+        if (counts[i] < 0) return MOE_E_INVALID;
+        if (counts[i] > (1ll << 48)) return MOE_E_UNSUPPORTED;
+        if (counts[i] == 0) continue;
+        const size_t size = is_bf16 && is_bf16[i] ? 2 : 4;
+        if (!grads[i] || !aligned(grads[i], size)) return MOE_E_INVALID;
+        if (with_out && (!out[i] || !aligned(out[i], size))) return MOE_E_INVALID;
+    }
+    return MOE_OK;
+}
+
+// Tensors i .. of a call, as many as one launch holds.
+static GradList grad_list(int32_t tensors, const void* const* grads, const int64_t* counts, const uint8_t* is_bf16,
+                          void* const* out, int32_t i) {
+    GradList a{};
+    a.n = std::min(tensors - i, kGradTensors);
+    for (int j = 0; j < a.n; ++j) {
+        a.src[j] = grads[i + j];
+        a.dst[j] = out ? out[i + j] : nullptr;
+        a.count[j] = (uint64_t)counts[i + j] | (is_bf16 && is_bf16[i + j] ? kGradBf16 : 0);
+    }
+    return a;
+}
+
+moe_status moe_grad_norm(int32_t tensors, const void* const* grads, const int64_t* counts, const uint8_t* is_bf16,
+                         float* norm, void* ws, size_t ws_bytes, void* stream) {
+    moe_status st = check_grads(tensors, grads, counts, is_bf16, nullptr, false);
+    if (st != MOE_OK) return st;
+    if (!norm || !ws || !aligned(norm, 4) || !aligned(ws, 16)) return MOE_E_INVALID;
+    size_t need = 0;
+    moe_query_grad_norm(tensors, &need);
+    if (ws_bytes < need) return MOE_E_WORKSPACE;
+    int* counter = (int*)ws;
+    double* partial = (double*)((uint8_t*)ws + kGradCounterBytes);
+    int slots = 0;
+    for (int32_t i = 0; i < tensors; i += kGradTensors) {
+        const GradList a = grad_list(tensors, grads, counts, is_bf16, nullptr, i);
+        const bool last = i + kGradTensors >= tensors;
+        TIMED(MOE_K_OTHER, (hipStream_t)stream,
+              slots = launch_grad_norm(a, partial, slots, last, counter, norm, (hipStream_t)stream));
+    }
+    return check_launch();
+}
+
+moe_status moe_clip_grads(int32_t tensors, const void* const* grads, const int64_t* counts, const uint8_t* is_bf16,
+                          const float* norm, float max_norm, void* const* out, void* stream) {
+    moe_status st = check_grads(tensors, grads, counts, is_bf16, out, true);
+    if (st != MOE_OK) return st;
+    if (!norm || !aligned(norm, 4) || !(max_norm > 0.0f)) return MOE_E_INVALID;
+    for (int32_t i = 0; i < tensors; i += kGradTensors) {
+        const GradList a = grad_list(tensors, grads, counts, is_bf16, out, i);
+        TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_grad_clip(a, norm, max_norm, (hipStream_t)stream));
+    }
+    return check_launch();
+}
+
 // Workspace of moe_layer_fwd_few (byte offsets).
 struct FewPlan {
     size_t counter, partial, logits, sel_e, sel_w, n_act, act_e, act_off, row_token, row_w, slot_row;

@@ -444,4 +444,86 @@ void launch_norm_bwd(NormBwd a, hipStream_t stream);
 void launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int layout, uint16_t* dst,
                        hipStream_t stream);
 
+// ---- rows by expert and back, blocks of 128 (rows.hip) ----
+
+struct RowsDispatch {
+    int64_t tokens, rows;      // rows: of dst, or of the codes
+    int cols, k;
+    const uint16_t* x;         // [tokens][cols]
+    const float* xf;           // or fp32 values in its place (codes only)
+    const int32_t* tok_row;    // [tokens][k]; NULL: token t is row t, k = 1
+    const int32_t* offsets;    // or NULL; else only tokens offsets[0] .. offsets[groups] - 1
+    int groups;
+    uint16_t* dst;             // or NULL
+    uint8_t* codes;            // [rows][cols] and their scales [blk_count(cols)][rows], or NULL
+    float* scales;
+};
+void launch_rows_dispatch(const RowsDispatch& a, hipStream_t stream);
+
+struct RowsCombine {
+    int64_t tokens, rows;
+    int cols, k;
+    const uint16_t* src;       // [rows][cols]
+    const int32_t* tok_row;
+    const float* w;            // [tokens][k], or NULL: 1
+    const uint16_t* add;       // [tokens][cols], or NULL
+    uint16_t* out;
+};
+void launch_rows_combine(const RowsCombine& a, hipStream_t stream);
+
+struct RowsCombineBwd {
+    int64_t tokens, rows;
+    int cols, k;
+    const uint16_t* dout;      // [tokens][cols]
+    const uint16_t* src;       // [rows][cols], where dw is wanted
+    const int32_t* tok_row;
+    const float* w;            // or NULL: 1
+    uint16_t* dsrc;            // or NULL
+    uint8_t* codes;            // dsrc's codes and scales, or NULL
+    float* scales;
+    float* dw;                 // [tokens][k], or NULL
+};
+void launch_rows_combine_bwd(const RowsCombineBwd& a, hipStream_t stream);
+
+// src [groups][n][k] ([groups][k][n] transposed) -> codes [groups][n][k], scales [groups][n / 128][k / 128]
+void launch_block_quant_weights(const uint16_t* src, int groups, int n, int k, int transposed, uint8_t* codes,
+                                float* scales, hipStream_t stream);
+// n = 0: scales [blk_count(cols)][rows]; else rows are those of matrices of n rows in blocks of 128 x 128
+void launch_block_dequant(const uint8_t* codes, const float* scales, int64_t rows, int cols, int n, uint16_t* dst,
+                          hipStream_t stream);
+
+// ---- gradient norm and clipping (grad.hip) ----
+
+constexpr int kGradTensors = 96;   // of one launch: what the kernel's arguments (4 KB) hold
+constexpr int kGradSlots = 2048;   // partial sums of one launch
+constexpr uint64_t kGradBf16 = 1ull << 63;  // in a count: the tensor is bf16
+struct GradList {
+    int n, chunk;                     // tensors; elements of a workgroup's step
+    const void* src[kGradTensors];
+    void* dst[kGradTensors];
+    uint64_t count[kGradTensors];
+    int64_t first[kGradTensors + 1];  // chunks before each tensor
+};
+static_assert(sizeof(GradList) + 64 <= 4096, "the kernel's arguments");
+// Returns the slots used up to and with this launch; the last launch of a call joins them all.
+int launch_grad_norm(GradList a, double* partial, int slot0, bool last, int* counter, float* norm, hipStream_t stream);
+void launch_grad_clip(GradList a, const float* norm, float max_norm, hipStream_t stream);
+
+// ---- products in blocks of 128 (block.hip) ----
+
+// out[r][j] = sum over blocks b of sa[b][r] sw[g][j / 128][b] sum over b's values of
+// a[r][.] w[g][j][.], g the group that row r lies in; or with wu (the up matrix; w the
+// gate) h = silu(gate) up.
+struct BlockGemm {
+    int rows, n, k, groups;
+    const uint8_t* a;          // [rows][k]
+    const float* sa;           // [blk_count(k)][rows]
+    const int32_t* offsets;    // [groups + 1] first row of each group, or NULL: one group of all rows
+    const uint8_t *w, *wu;     // [groups][n][k]
+    const float *sw, *swu;     // [groups][blk_count(n)][blk_count(k)]
+    uint16_t* out;             // [rows][n]
+    float* h;                  // [rows][n] fp32 (wu)
+};
+void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream);
+
 }  // namespace moe

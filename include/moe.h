@@ -426,6 +426,146 @@ moe_status moe_layer_fwd_few(const moe_cfg *cfg, const moe_weights *w, const uin
 moe_status moe_query_few(const moe_cfg *cfg, size_t *workspace);
 
 /*
+ * Rows by expert and back: the layer's dispatch and combine for callers who run
+ * the experts' products themselves (with moe_block_gemm, or their own), and the
+ * gradients.  r(t,j) = tok_row[t,j] is the row of token t's choice j, as
+ * moe_dispatch_layout writes it; a value outside [0, rows) is no row (a dropped
+ * choice).  No row may stand in the table twice: what it holds afterwards would
+ * be unspecified.
+ *
+ * moe_dispatch_rows:      row r(t,j) = x[t]
+ *   x bf16 [tokens, cols]; tok_row int32 [tokens, k];
+ *   dst bf16 [rows, cols], or NULL; and / or
+ *   codes uint8 [rows, cols], scales fp32 [ceil(cols/128)][rows]: the row as
+ *       moe_block_quantize holds it; both or neither.
+ * moe_combine_rows:       out[t] = add[t] + sum_j w[t,j] src[r(t,j)]
+ *   src bf16 [rows, cols]; w fp32 [tokens, k], or NULL: 1 (which is the gradient
+ *   of moe_dispatch_rows: src the rows' gradients, out that of x); add bf16
+ *   [tokens, cols], or NULL: 0; out bf16 [tokens, cols], which may be add itself.
+ *   The sum is fp32, in ascending j, rounded once; a token without rows gets
+ *   add[t], or zeros.  w of a choice without a row is not used.
+ * moe_combine_rows_bwd:   dsrc[r(t,j)] = w[t,j] dout[t],  dw[t,j] = <src[r(t,j)], dout[t]>
+ *   dout bf16 [tokens, cols]; src, tok_row, w as above (src may be NULL without
+ *   dw); dsrc bf16 [rows, cols], or NULL; codes, scales of the rounded dsrc as
+ *   moe_block_quantize holds it, both or neither; dw fp32 [tokens, k], or NULL (0
+ *   for a choice without a row).  The gradient of add is dout.
+ *
+ * Rows that the table does not name are left as they were.  All pointers 16-byte
+ * aligned (tok_row, w, dw and scales 4).  MOE_E_INVALID for null or misaligned
+ * pointers, no output, tokens, k or rows < 1, cols not a positive multiple of 8
+ * (of 16 with codes); MOE_E_UNSUPPORTED for k > 16, cols > 2^20, tokens * k or
+ * rows > 2^30.  Sums have a fixed order, so results are bitwise repeatable.
+ */
+moe_status moe_dispatch_rows(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint16_t *x,
+                             const int32_t *tok_row, uint16_t *dst, uint8_t *codes, float *scales, void *stream);
+moe_status moe_combine_rows(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint16_t *src,
+                            const int32_t *tok_row, const float *w, const uint16_t *add, uint16_t *out,
+                            void *stream);
+moe_status moe_combine_rows_bwd(int64_t tokens, int32_t k, int32_t cols, int64_t rows, const uint16_t *dout,
+                                const uint16_t *src, const int32_t *tok_row, const float *w, uint16_t *dsrc,
+                                uint8_t *codes, float *scales, float *dw, void *stream);
+
+/*
+ * 8-bit floating point with a scale for each block of 128, the form in which many
+ * checkpoints hold their experts: OCP E4M3 codes; one fp32 scale for every 128
+ * consecutive values of a row of activations, and for every 128 x 128 values of a
+ * weight matrix.  A value is code * scale.  A block past the last full 128 is
+ * shorter.
+ * The quantisers' scale is 2^e for the smallest e with amax <= 448 * 2^e (at least
+ * 2^-126; 1 for a block of zeros), and a code is x / 2^e rounded to nearest even:
+ * the rule of moe_mx_quantize.  The products take any positive finite scales
+ * whose products are normal fp32 numbers.
+ *
+ * moe_block_quantize: src bf16 [rows, cols] -> codes [rows, cols], scales
+ *   [ceil(cols/128)][rows].
+ * moe_block_quantize_weights: codes [groups, n, k], scales
+ *   [groups][ceil(n/128)][ceil(k/128)] of src bf16 [groups, n, k], or with
+ *   transposed = 1 [groups, k, n] (the layout of moe_prepare_weights' inputs: Wg
+ *   [E, H, I] is n = I, k = H).  With transposed = 0 a matrix [E, H, I] gives the
+ *   operand of its input gradient: n = H, k = I, the same blocks turned.
+ * moe_block_dequantize: dst bf16 of codes [rows, cols] and their scales: those of
+ *   activations (n = 0), or of weights (n > 0: rows = groups * n).
+ * A NaN or an infinity gives a NaN code (other codes and the scale of its block
+ * are unspecified where it is an infinity).  All pointers 16-byte aligned (scales 4).
+ * MOE_E_INVALID for null or misaligned pointers, sizes < 1, cols and k not
+ * multiples of 16, n not a multiple of 8 with transposed = 1, n not a divisor of
+ * rows or an unknown transposed; MOE_E_UNSUPPORTED for rows (groups * n) > 2^30,
+ * cols > 2^20 or n * k >= 2^31.
+ */
+moe_status moe_block_quantize(int64_t rows, int32_t cols, const uint16_t *src, uint8_t *codes, float *scales,
+                              void *stream);
+moe_status moe_block_quantize_weights(int32_t groups, int32_t n, int32_t k, const uint16_t *src, int32_t transposed,
+                                      uint8_t *codes, float *scales, void *stream);
+moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uint8_t *codes, const float *scales,
+                                uint16_t *dst, void *stream);
+
+/*
+ * Grouped product of rows sorted by expert with their expert's matrix, both in
+ * that form.  For row r of group g:
+ *   out[r,j] = bf16(sum_i A[r,i] W[g,j,i])
+ *   a uint8 [rows, k], a_scales fp32 [ceil(k/128)][rows];
+ *   offsets int32 [groups + 1]: group g's rows are offsets[g] .. offsets[g+1]-1,
+ *       ascending from 0, as moe_dispatch_layout writes it; NULL with groups = 1:
+ *       every row.  A group may be empty; bounds outside the rows are cut off, and
+ *       rows of no group are left as they were;
+ *   w uint8 [groups, n, k], w_scales fp32 [groups][ceil(n/128)][ceil(k/128)];
+ *   out bf16 [rows, n].
+ * moe_block_gemm_swiglu is the gate and up products with SwiGLU behind them:
+ *   h[r,j] = silu(g) u,  g = sum_i A[r,i] Wg[g,j,i],  u = sum_i A[r,i] Wu[g,j,i]
+ *   h_codes uint8 [rows, n], h_scales fp32 [ceil(n/128)][rows]: h as the next
+ *       product takes it, quantised from fp32 by the rule above;
+ *   h bf16 [rows, n], or NULL: h itself as well;
+ *   ws: moe_query_block_swiglu bytes (host-only query; its refusals of sizes are
+ *       those below), 16-byte aligned, of any content; calls that overlap on two
+ *       streams take one each.
+ * The product of a gradient is the same call: dA = dOut W takes dOut's codes and the
+ * turned weights.  Each block's products are summed by the matrix instruction (which
+ * cuts off what lies below 2^-13 of the largest of eight neighbouring products),
+ * scaled and added up in fp32.  Runs of one call are bitwise repeatable.
+ * All pointers 16-byte aligned (scales and offsets 4).  MOE_E_INVALID for null or
+ * misaligned pointers, sizes < 1, k not a multiple of 16, n not of 8 (of 16 with
+ * SwiGLU), or no offsets with groups > 1; MOE_E_WORKSPACE for a smaller workspace;
+ * MOE_E_UNSUPPORTED for rows > 2^24, groups > 65536, n or k > 2^20 or n * k >= 2^31.
+ */
+moe_status moe_block_gemm(int64_t rows, int32_t n, int32_t k, int32_t groups, const uint8_t *a, const float *a_scales,
+                          const int32_t *offsets, const uint8_t *w, const float *w_scales, uint16_t *out,
+                          void *stream);
+moe_status moe_query_block_swiglu(int64_t rows, int32_t n, int32_t k, int32_t groups, size_t *workspace);
+moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t groups, const uint8_t *a,
+                                 const float *a_scales, const int32_t *offsets, const uint8_t *wg,
+                                 const float *wg_scales, const uint8_t *wu, const float *wu_scales, uint8_t *h_codes,
+                                 float *h_scales, uint16_t *h, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The global norm of many gradient tensors, and their clipping by it: what stands
+ * between moe_layer_bwd and an optimizer.
+ *   norm = sqrt(sum of all squares)                         (moe_grad_norm)
+ *   out_i = grads_i * min(1, max_norm / (norm + 1e-6))      (moe_clip_grads)
+ *   grads, out: host arrays of `tensors` device pointers, read during the call;
+ *       out[i] may be grads[i] itself (in place: written only where the factor is
+ *       less than 1), and overlaps no other tensor;
+ *   counts: host array of their element counts (0: an empty tensor, whose pointer
+ *       is not used); is_bf16: host array, non-zero where the tensor is bf16, else
+ *       it is fp32; NULL: all fp32;
+ *   norm: device fp32.  Summed in 64 bits, so no fp32 square overflows;
+ *   ws: moe_query_grad_norm bytes, 16-byte aligned; zero its first 256 bytes once
+ *       when it is allocated (every call leaves them zero).  One call at a time:
+ *       calls that overlap on two streams take a workspace each.
+ * max_norm must be positive; a NaN norm makes every gradient NaN, an infinite one
+ * zero (an infinite gradient NaN).  Tensors need the alignment of their type only;
+ * those that are not 16-byte aligned are read element by element.
+ * Sums have a fixed order, so results are bitwise repeatable.  MOE_E_INVALID for
+ * null or misaligned pointers, tensors < 1, a negative count or max_norm not above
+ * 0 (infinity is: it scales by 1); MOE_E_WORKSPACE for a smaller workspace;
+ * MOE_E_UNSUPPORTED for more than 2^20 tensors or 2^48 elements in one.
+ */
+moe_status moe_query_grad_norm(int32_t tensors, size_t *workspace);
+moe_status moe_grad_norm(int32_t tensors, const void *const *grads, const int64_t *counts, const uint8_t *is_bf16,
+                         float *norm, void *ws, size_t ws_bytes, void *stream);
+moe_status moe_clip_grads(int32_t tensors, const void *const *grads, const int64_t *counts, const uint8_t *is_bf16,
+                          const float *norm, float max_norm, void *const *out, void *stream);
+
+/*
  * Kernel timing (diagnostics, for benchmarks).  While enabled, every kernel
  * the library launches is bracketed by a pair of HIP events recorded on the
  * stream it is launched on; moe_timing_read waits for those events and
