@@ -1099,7 +1099,7 @@ moe_status moe_block_gemm(int64_t rows, int32_t n, int32_t k, int32_t groups, co
     BlockGemm g{};
     g.rows = (int)rows; g.n = n; g.k = k; g.groups = groups; g.a = a; g.sa = a_scales; g.offsets = offsets; g.w = w;
     g.sw = w_scales; g.out = out;
-    TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_block_gemm_few(g, (hipStream_t)stream));
+    TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_block_gemm(g, (hipStream_t)stream));
     return check_launch();
 }
 
@@ -1107,7 +1107,8 @@ moe_status moe_query_block_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gr
     if (!workspace) return MOE_E_INVALID;
     moe_status st = check_block(rows, n, k, groups, 16);
     if (st != MOE_OK) return st;
-    *workspace = align_up((size_t)rows * n * 4);
+    // the small tiles' h in fp32; the large ones quantise it themselves
+    *workspace = block_gemm_large(rows, n, k, groups) ? kAlign : align_up((size_t)rows * n * 4);
     return MOE_OK;
 }
 
@@ -1130,7 +1131,9 @@ moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gro
     BlockGemm g{};
     g.rows = (int)rows; g.n = n; g.k = k; g.groups = groups; g.a = a; g.sa = a_scales; g.offsets = offsets; g.w = wg;
     g.sw = wg_scales; g.wu = wu; g.swu = wu_scales; g.h = (float*)ws;
-    TIMED(MOE_K_OTHER, s, launch_block_gemm_few(g, s));
+    g.hq = h_codes; g.hs = h_scales; g.h16 = h;
+    TIMED(MOE_K_OTHER, s, launch_block_gemm(g, s));
+    if (block_gemm_large(rows, n, k, groups)) return check_launch();
     RowsDispatch q{};
     q.tokens = rows; q.rows = rows; q.cols = n; q.k = 1; q.xf = (const float*)ws; q.codes = h_codes; q.scales = h_scales;
     q.dst = h; q.offsets = offsets; q.groups = groups;

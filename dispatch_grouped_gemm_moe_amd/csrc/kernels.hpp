@@ -522,8 +522,13 @@ struct BlockGemm {
     const uint8_t *w, *wu;     // [groups][n][k]
     const float *sw, *swu;     // [groups][blk_count(n)][blk_count(k)]
     uint16_t* out;             // [rows][n]
-    float* h;                  // [rows][n] fp32 (wu)
+    float* h;                  // wu, small tiles: h [rows][n] in fp32
+    uint8_t* hq;               // wu, large tiles: its codes and scales [blk_count(n)][rows], and bf16 or NULL
+    float* hs;
+    uint16_t* h16;
 };
-void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream);
+// Whether a product runs in the large tiles, which write h's codes themselves.
+bool block_gemm_large(int64_t rows, int n, int k, int groups);
+void launch_block_gemm(const BlockGemm& a, hipStream_t stream);
 
 }  // namespace moe
