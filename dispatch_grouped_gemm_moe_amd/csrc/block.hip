@@ -25,6 +25,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t blk_rsrc(const void* p, uint32
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
 }
 
+__device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
+
 // Part `slot` of the rows: groups in ascending order, each in parts of kRows rows (the
 // last one shorter).  False past the last part.  Offsets outside the rows are cut off,
 // so whatever the table holds, no row outside them is named.  Uniform in the wave.
@@ -38,18 +40,12 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int groups, in
         return count > 0;
     }
     const int lane = threadIdx.x & 63, per = (groups + kWave - 1) / kWave;
-    auto bounds = [&](int e, int& lo, int& hi) {
-        lo = min(max(offsets[e], 0), rows);
-        hi = min(max(offsets[e + 1], lo), rows);
-    };
-    int mine = 0;
+    int lo = 0, hi = 0, mine = 0;  // of the lane's groups: the last one's bounds, their parts
     for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e < groups) {
-            int lo, hi;
-            bounds(e, lo, hi);
-            mine += (hi - lo + kRows - 1) / kRows;
-        }
+        const int e = min(lane * per + i, groups);
+        lo = min(max(offsets[e], 0), rows);
+        hi = min(max(offsets[min(e + 1, groups)], lo), rows);  // past the last group: none
+        mine += (hi - lo + kRows - 1) / kRows;
     }
     int upto = mine;  // inclusive sum over the lanes
 #pragma unroll
@@ -61,18 +57,24 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int groups, in
     if (!past) return false;
     const int l = __builtin_ctzll(past);
     int left = slot - __builtin_amdgcn_readlane(upto - mine, l);
-    for (int e = l * per;; ++e) {  // ends: lane l's groups hold the part
-        int lo, hi;
-        bounds(e, lo, hi);
-        const int parts = (hi - lo + kRows - 1) / kRows;
-        if (left < parts || e == groups - 1) {
-            g = __builtin_amdgcn_readfirstlane(e);
-            row0 = __builtin_amdgcn_readfirstlane(lo + left * kRows);
-            count = __builtin_amdgcn_readfirstlane(min(hi - lo - left * kRows, kRows));
-            return true;
+    g = l * per;
+    if (per == 1) {
+        lo = __builtin_amdgcn_readlane(lo, l);
+        hi = __builtin_amdgcn_readlane(hi, l);
+    } else {
+        for (;; ++g) {  // ends: the part is one of lane l's groups'
+            lo = min(max(offsets[g], 0), rows);
+            hi = min(max(offsets[g + 1], lo), rows);
+            const int parts = (hi - lo + kRows - 1) / kRows;
+            if (left < parts || g == groups - 1) break;
+            left -= parts;
         }
-        left -= parts;
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        hi = __builtin_amdgcn_readfirstlane(hi);
     }
+    row0 = lo + left * kRows;
+    count = min(hi - row0, kRows);
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -80,111 +82,168 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int groups, in
 // ---------------------------------------------------------------------------
 
 constexpr int kBfWaves = 4;
+constexpr int kBfRows = 64;           // most rows of a part
+constexpr int kBfSlot = 4 * 16 * kBlk;  // a wave's weights of a step: four fragments of 16 rows by a block
 
-// 16 kTF rows by 16 kNF columns a workgroup, the K blocks dealt to its four waves and
-// their sums joined in LDS in a fixed order.  Weight rows are the M side of 16-wide
-// MFMAs, rows of a the N side, so a lane ends with four neighbouring columns of a row.
-template <int kNF, int kTF, bool kGlu, int kDepth>
-__global__ __launch_bounds__(kBfWaves * kWave) void block_few_kernel(BlockGemm a) {
+// kFrags fragments of 16 weight rows from LDS, fragment f at byte 2048 f: this lane's
+// pieces at p0 and p1 of its row.  In one block with its wait: the compiler would wait
+// for the loads into the other slot too.
+template <int kFrags>
+__device__ __forceinline__ void few_frags(uint32_t p0, uint32_t p1, intx8 (&w)[kFrags]) {
+    intx4 f[2 * kFrags];
+    if constexpr (kFrags == 4) {
+        asm volatile(
+            "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\t"
+            "ds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
+            "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %9 offset:4096\n\t"
+            "ds_read_b128 %6, %8 offset:6144\n\tds_read_b128 %7, %9 offset:6144\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(f[4]), "=&v"(f[5]), "=&v"(f[6]), "=&v"(f[7])
+            : "v"(p0), "v"(p1)
+            : "memory");
+    } else if constexpr (kFrags == 2) {
+        asm volatile(
+            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
+            "ds_read_b128 %2, %4 offset:2048\n\tds_read_b128 %3, %5 offset:2048\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+            : "v"(p0), "v"(p1)
+            : "memory");
+    } else {
+        static_assert(kFrags == 1, "");
+        asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(f[0]), "=&v"(f[1])
+                     : "v"(p0), "v"(p1)
+                     : "memory");
+    }
+#pragma unroll
+    for (int x = 0; x < kFrags; ++x) w[x] = __builtin_shufflevector(f[2 * x], f[2 * x + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Rows row0 .. row0 + count - 1 (at most 16 kTF) of group g by columns n0 .. n0 + 16 kNF -
+// 1, the K blocks dealt to the workgroup's four waves and their sums joined in LDS in a
+// fixed order.  Weight rows are the M side of 16-wide MFMAs, rows of a the N side, so a
+// lane ends with four neighbouring columns of a row.
+//
+// A wave's step is kU blocks of K.  Its weights come straight into one of the wave's own
+// two LDS slots in whole lines, eight rows an instruction, asked for a step ahead; the
+// rows of a, which every workgroup of the group reads, come from the cache into registers.
+template <int kNF, int kTF, bool kGlu>
+__device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int row0, int count, int n0,
+                                               uint8_t (*s_w)[2][kBfSlot]) {
     constexpr int kW = kGlu ? 2 * kNF : kNF;  // weight fragments: the gate's, then the up matrix's
-    __shared__ floatx4 s_part[kBfWaves][kW * kTF][kWave];
+    constexpr int kU = 4 / (kW > kTF ? kW : kTF);
+    constexpr int kFrags = kW * kU;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lq = lane >> 4;
-    const int n0 = blockIdx.x * 16 * kNF;
-    int g, row0, count;
-    for (int slot = blockIdx.y; find_part<16 * kTF>(a.offsets, a.groups, a.rows, slot, g, row0, count);
-         slot += gridDim.y) {
-        const int kb_n = blk_count(a.k), nb = blk_count(a.n);
-        const int64_t wat = (int64_t)g * a.n * a.k;
-        const uint32_t wbytes = (uint32_t)a.n * (uint32_t)a.k;
-        const __amdgpu_buffer_rsrc_t rw = blk_rsrc(a.w + wat, wbytes), ru = blk_rsrc((kGlu ? a.wu : a.w) + wat, wbytes);
-        const __amdgpu_buffer_rsrc_t ra = blk_rsrc(a.a + (int64_t)row0 * a.k, (uint32_t)count * (uint32_t)a.k);
-        uint32_t woff[kNF];
-        const float *swf[kNF], *suf[kNF];
+    const int kb_n = blk_count(a.k), nb = blk_count(a.n);
+    const int64_t wat = ((int64_t)g * a.n + n0) * a.k;
+    const uint32_t wbytes = (uint32_t)(a.n - n0) * (uint32_t)a.k;  // columns past the last read as zero
+    const __amdgpu_buffer_rsrc_t rw = blk_rsrc(a.w + wat, wbytes), ru = blk_rsrc((kGlu ? a.wu : a.w) + wat, wbytes);
+    const __amdgpu_buffer_rsrc_t ra = blk_rsrc(a.a + (int64_t)row0 * a.k, (uint32_t)count * (uint32_t)a.k);
+    const uint32_t off16 = 16u * (uint32_t)a.k;
+    const float *swf[kNF], *suf[kNF];
 #pragma unroll
-        for (int f = 0; f < kNF; ++f) {
-            const int col = n0 + 16 * f + lr;
-            woff[f] = col < a.n ? (uint32_t)col * (uint32_t)a.k + lq * 16 : kNowhere;
-            const int64_t sat = ((int64_t)g * nb + min(n0 + 16 * f, a.n - 1) / kBlk) * kb_n;
-            swf[f] = a.sw + sat;
-            suf[f] = (kGlu ? a.swu : a.sw) + sat;
+    for (int f = 0; f < kNF; ++f) {
+        const int64_t at = ((int64_t)g * nb + min(n0 + 16 * f, a.n - 1) / kBlk) * kb_n;
+        swf[f] = a.sw + at;
+        suf[f] = (kGlu ? a.swu : a.sw) + at;
+    }
+    // Load q of a step: rows 8 (q % 2) .. + 7 of fragment q / 2; lane l row l / 8, chunk l % 8 in
+    // LDS, which holds the row's chunk (l % 8) ^ swz8(row).
+    auto issue = [&](int s, int slot) {
+        uint8_t* dst = s_w[wave][slot];
+#pragma unroll
+        for (int q = 0; q < 2 * kFrags; ++q) {
+            const int f = q / 2 % kW, row = 8 * (q & 1) + (lane >> 3);
+            const int at = ((s * kBfWaves + wave) * kU + q / 2 / kW) * kBlk + ((lane & 7) ^ (4 * (q & 1) | (lane >> 4))) * 16;
+            // k is a multiple of 16: a piece is inside the row or not
+            const uint32_t o = at < a.k ? (uint32_t)row * (uint32_t)a.k + at + f % kNF * off16 : kNowhere;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(f < kNF ? rw : ru, (lds_void*)(dst + q * 1024), 16, o, 0, 0, 0);
         }
-        uint32_t aoff[kTF];
-        const float* saf[kTF];
+    };
+    struct Rows {
+        intx4 x[kU][kTF][2];
+        float sa[kU][kTF];
+    };
+    constexpr int kRowLoads = 3 * kU * kTF;
+    auto load = [&](int s, Rows& r) {
 #pragma unroll
-        for (int t = 0; t < kTF; ++t) {
-            const int r = 16 * t + lr;
-            aoff[t] = r < count ? (uint32_t)r * (uint32_t)a.k + lq * 16 : kNowhere;
-            saf[t] = a.sa + row0 + min(r, count - 1);
-        }
-        struct Step {
-            intx4 w[kW][2], x[kTF][2];
-            float sw[kW], sa[kTF];
-        };
-        auto load = [&](Step& s, int kb) {
-            const uint32_t at = (uint32_t)kb * kBlk + lq * 16;
+        for (int u = 0; u < kU; ++u) {
+            const int kb = (s * kBfWaves + wave) * kU + u;
+            const __amdgpu_buffer_rsrc_t rs = blk_rsrc(a.sa + (int64_t)min(kb, kb_n - 1) * a.rows + row0, count * 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool in = at + 64 * h < (uint32_t)a.k;  // k is a multiple of 16: a piece is inside or not
+            for (int t = 0; t < kTF; ++t) {
 #pragma unroll
-                for (int f = 0; f < kW; ++f) {
-                    const uint32_t o = woff[f % kNF];
-                    s.w[f][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                        f < kNF ? rw : ru, in && o != kNowhere ? o + kb * kBlk + 64 * h : kNowhere, 0, 0);
+                for (int h = 0; h < 2; ++h) {
+                    const int at = kb * kBlk + 64 * h + lq * 16;
+                    const uint32_t o = at < a.k ? (uint32_t)lr * (uint32_t)a.k + at : kNowhere;
+                    r.x[u][t][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, o + t * off16, 0, 0);
                 }
-#pragma unroll
-                for (int t = 0; t < kTF; ++t)
-                    s.x[t][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                        ra, in && aoff[t] != kNowhere ? aoff[t] + kb * kBlk + 64 * h : kNowhere, 0, 0);
+                r.sa[u][t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (16 * t + lr) * 4, 0, 0));
             }
-            const int ks = min(kb, kb_n - 1);
+        }
+    };
+    floatx4 acc[kW][kTF] = {};
+    const uint32_t p_row = lds_at(s_w[wave][0]) + lr * kBlk;
+    const uint32_t p0 = p_row + ((lq ^ swz8(lr)) << 4), p1 = p_row + (((4 + lq) ^ swz8(lr)) << 4);
+    auto step = [&](int s, int slot, const Rows& cur, Rows& next) {
+        load(s + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(s + 1, slot ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        // this step's loads, all older than those, have arrived (scalar loads are not counted)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kRowLoads + 2 * kFrags) : "memory");
+        intx8 w[kFrags];
+        few_frags<kFrags>(p0 + slot * kBfSlot, p1 + slot * kBfSlot, w);
 #pragma unroll
-            for (int f = 0; f < kW; ++f) s.sw[f] = (f < kNF ? swf[f % kNF] : suf[f % kNF])[ks];
-#pragma unroll
-            for (int t = 0; t < kTF; ++t) s.sa[t] = saf[t][(int64_t)ks * a.rows];
-        };
-        floatx4 acc[kW][kTF] = {};
-        auto multiply = [&](const Step& s) {
+        for (int u = 0; u < kU; ++u) {
+            const int ks = min((s * kBfWaves + wave) * kU + u, kb_n - 1);
 #pragma unroll
             for (int f = 0; f < kW; ++f) {
-                const intx8 w = __builtin_shufflevector(s.w[f][0], s.w[f][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                const float sw = (f < kNF ? swf[f % kNF] : suf[f % kNF])[ks];
 #pragma unroll
                 for (int t = 0; t < kTF; ++t) {
-                    const intx8 x = __builtin_shufflevector(s.x[t][0], s.x[t][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    const floatx4 p =
-                        __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, floatx4{}, 0, 0, 0, 0, 0, 0);
-                    const float sc = s.sw[f] * s.sa[t];
+                    const intx8 x = __builtin_shufflevector(cur.x[u][t][0], cur.x[u][t][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    const floatx4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[u * kW + f], x, floatx4{}, 0, 0,
+                                                                                       0, 0, 0, 0);
+                    const float sc = sw * cur.sa[u][t];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[f][t][i] = __builtin_fmaf(p[i], sc, acc[f][t][i]);
                 }
             }
-        };
-        Step st[kDepth];
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) load(st[d], wave + kBfWaves * d);
-        for (int kb = wave; kb < kb_n; kb += kBfWaves * kDepth) {
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                multiply(st[d]);  // past the last block: zeros
-                load(st[d], kb + kBfWaves * (kDepth + d));
-            }
         }
+    };
+    // (a wave's blocks past the last are zeros)
+    const int steps = (kb_n + kBfWaves * kU - 1) / (kBfWaves * kU);
+    Rows r0, r1;
+    load(0, r0);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(0, 0);
+    for (int s = 0; s < steps; s += 2) {
+        step(s, 0, r0, r1);
+        if (s + 1 < steps) step(s + 1, 1, r1, r0);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the slots are free
+    __syncthreads();
+    // the sums go through the slots' memory, one fragment of rows at a time
+    floatx4 (*s_part)[kW][kWave] = (floatx4(*)[kW][kWave])s_w;
 #pragma unroll
-        for (int f = 0; f < kW; ++f)
+    for (int t = 0; t < kTF; ++t) {
 #pragma unroll
-            for (int t = 0; t < kTF; ++t) s_part[wave][f * kTF + t][lane] = acc[f][t];
+        for (int f = 0; f < kW; ++f) s_part[wave][f][lane] = acc[f][t];
         __syncthreads();
-        auto joined = [&](int i) {
-            floatx4 v = s_part[0][i][lane];
+        auto joined = [&](int f) {
+            floatx4 v = s_part[0][f][lane];
 #pragma unroll
-            for (int x = 1; x < kBfWaves; ++x) v += s_part[x][i][lane];
+            for (int x = 1; x < kBfWaves; ++x) v += s_part[x][f][lane];
             return v;
         };
-        for (int i = wave; i < kNF * kTF; i += kBfWaves) {
-            const int f = i / kTF, t = i % kTF, r = 16 * t + lr, col = n0 + 16 * f + 4 * lq;
-            floatx4 v = joined(i);
+        for (int f = wave; f < kNF; f += kBfWaves) {
+            const int r = 16 * t + lr, col = n0 + 16 * f + 4 * lq;
+            floatx4 v = joined(f);
             if constexpr (kGlu) {
-                const floatx4 u = joined(kNF * kTF + i);
+                const floatx4 u = joined(kNF + f);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) v[x] = v[x] / (1.0f + __expf(-v[x])) * u[x];
             }
@@ -195,7 +254,20 @@ __global__ __launch_bounds__(kBfWaves * kWave) void block_few_kernel(BlockGemm a
             else
                 *(uint2*)(a.out + at) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         }
-        __syncthreads();  // the sums are read
+        __syncthreads();
+    }
+}
+
+template <int kNF, bool kGlu>
+__global__ __launch_bounds__(kBfWaves * kWave, 2) void block_few_kernel(BlockGemm a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_w[kBfWaves][2][kBfSlot];
+    int g, row0, count;
+    for (int slot = blockIdx.y; find_part<kBfRows>(a.offsets, a.groups, a.rows, slot, g, row0, count);
+         slot += gridDim.y) {
+        const int n0 = blockIdx.x * 16 * kNF;
+        if (count <= 16) block_few_part<kNF, 1, kGlu>(a, g, row0, count, n0, s_w);
+        else if (count <= 32) block_few_part<kNF, 2, kGlu>(a, g, row0, count, n0, s_w);
+        else block_few_part<kNF, 4, kGlu>(a, g, row0, count, n0, s_w);
     }
 }
 
@@ -236,7 +308,6 @@ struct BgTile {
 
 // LDS accesses of the epilogue, in asm: the compiler would wait for the next tile's
 // loads into the ring too.
-__device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void lds_put(uint32_t at, uint32_t v) {
@@ -603,16 +674,19 @@ bool block_gemm_large(int64_t rows, int n, int k, int groups) {
 }
 
 static void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream) {
-#define BLOCK_FEW(NF, TF, D)                                                                                          \
-    do {                                                                                                              \
-        const dim3 grid((a.n + 16 * NF - 1) / (16 * NF), std::min(most_parts(a.rows, a.groups, 16 * TF), 65535));                      \
-        if (a.wu)                                                                                                     \
-            hipLaunchKernelGGL((block_few_kernel<NF, TF, true, D>), grid, dim3(kBfWaves * kWave), 0, stream, a);      \
-        else                                                                                                          \
-            hipLaunchKernelGGL((block_few_kernel<NF, TF, false, D>), grid, dim3(kBfWaves * kWave), 0, stream, a);     \
-    } while (0)
-    if (a.rows <= 16 * a.groups) BLOCK_FEW(1, 1, 2);
-    else BLOCK_FEW(2, 4, 1);
+#define BLOCK_FEW(NF, GLU)                                                                                      \
+    hipLaunchKernelGGL((block_few_kernel<NF, GLU>),                                                             \
+                       dim3((a.n + 16 * NF - 1) / (16 * NF), std::min(most_parts(a.rows, a.groups, kBfRows), 65535)), \
+                       dim3(kBfWaves * kWave), 0, stream, a)
+    const int64_t strips = (int64_t)((a.n + 15) / 16) * std::min(a.rows, a.groups);
+    if (a.wu) {
+        if (strips >= 2 * 512) BLOCK_FEW(2, true);
+        else BLOCK_FEW(1, true);
+    } else {
+        if (strips >= 4 * 512) BLOCK_FEW(4, false);
+        else if (strips >= 2 * 512) BLOCK_FEW(2, false);
+        else BLOCK_FEW(1, false);
+    }
 #undef BLOCK_FEW
 }
 
