@@ -6,7 +6,10 @@
 // and, with a gate and an up matrix, h = silu(gate product) * (up product).  A block
 // is as deep as one or two matrix instructions, so P_b comes from a zero accumulator
 // and one fused multiply-add per element takes it, scaled, into the fp32 sum.
+#include <math.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "block8.hpp"
 #include "common.hpp"
@@ -187,13 +190,19 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
     floatx4 acc[kW][kTF] = {};
     const uint32_t p_row = lds_at(s_w[wave][0]) + lr * kBlk;
     const uint32_t p0 = p_row + ((lq ^ swz8(lr)) << 4), p1 = p_row + (((4 + lq) ^ swz8(lr)) << 4);
-    auto step = [&](int s, int slot, const Rows& cur, Rows& next) {
-        load(s + 1, next);
-        __builtin_amdgcn_sched_barrier(0);
-        issue(s + 1, slot ^ 1);
-        __builtin_amdgcn_sched_barrier(0);
-        // this step's loads, all older than those, have arrived (scalar loads are not counted)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kRowLoads + 2 * kFrags) : "memory");
+    auto step = [&](auto last, int s, int slot, const Rows& cur, Rows& next) {
+        if constexpr (decltype(last)::value) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+            load(s + 1, next);
+            __builtin_amdgcn_sched_barrier(0);
+            issue(s + 1, slot ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+            // This step's loads, all older than those, have arrived (scalar loads are not
+            // counted).  The count holds because a step that is not the last uses every value it
+            // loads in the next one: none is dropped.
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kRowLoads + 2 * kFrags) : "memory");
+        }
         intx8 w[kFrags];
         few_frags<kFrags>(p0 + slot * kBfSlot, p1 + slot * kBfSlot, w);
 #pragma unroll
@@ -201,7 +210,8 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
             const int ks = min((s * kBfWaves + wave) * kU + u, kb_n - 1);
 #pragma unroll
             for (int f = 0; f < kW; ++f) {
-                const float sw = (f < kNF ? swf[f % kNF] : suf[f % kNF])[ks];
+                // a scalar load: waiting for a vector one would wait for the weights asked for before it
+                const float sw = *(const __attribute__((address_space(4))) float*)((f < kNF ? swf[f % kNF] : suf[f % kNF]) + ks);
 #pragma unroll
                 for (int t = 0; t < kTF; ++t) {
                     const intx8 x = __builtin_shufflevector(cur.x[u][t][0], cur.x[u][t][1], 0, 1, 2, 3, 4, 5, 6, 7);
@@ -220,12 +230,20 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
     load(0, r0);
     __builtin_amdgcn_sched_barrier(0);
     issue(0, 0);
-    for (int s = 0; s < steps; s += 2) {
-        step(s, 0, r0, r1);
-        if (s + 1 < steps) step(s + 1, 1, r1, r0);
+    constexpr std::integral_constant<bool, false> more{};
+    constexpr std::integral_constant<bool, true> last{};
+    int s = 0;
+    for (; s + 2 < steps; s += 2) {
+        step(more, s, 0, r0, r1);
+        step(more, s + 1, 1, r1, r0);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the slots are free
-    __syncthreads();
+    if (s + 1 < steps) {
+        step(more, s, 0, r0, r1);
+        step(last, s + 1, 1, r1, r0);
+    } else {
+        step(last, s, 0, r0, r1);
+    }
+    __syncthreads();  // the slots are free
     // the sums go through the slots' memory, one fragment of rows at a time
     floatx4 (*s_part)[kW][kWave] = (floatx4(*)[kW][kWave])s_w;
 #pragma unroll
@@ -272,30 +290,35 @@ __global__ __launch_bounds__(kBfWaves * kWave, 2) void block_few_kernel(BlockGem
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 256 x 256 tiles
+// Many rows: tiles of up to 256 x 256
 // ---------------------------------------------------------------------------
 
-// Eight waves, two per SIMD, each 64 x 128 of the tile as 2 x 4 fragments of 32 x 32.
-// A stage is one block of K: A and B codes as 128-byte rows, the A rows' scales and
-// the tile's two weight scales; two stages make the ring.  All of it comes by loads
-// straight into LDS through buffer descriptors: what lies past the group's last row,
-// the matrix's last row or the row's end reads as zero and moves no memory, so no
-// size needs a tile of its own, and a lane's offsets are the same for every tile.
-constexpr int kBgStageB = BM * kBlk;
-constexpr int kBgStageSA = kBgStageB + BN * kBlk;
-constexpr int kBgStageSW = kBgStageSA + BM * 4;       // the first two of four areas that a wave's load fills
-constexpr int kBgStage = kBgStageSW + 4 * kWave * 4;
-constexpr int kBgRing = 2 * kBgStage;
-constexpr int kBgStgPitch = 512;                      // staged bf16 output: 32 rows of 512 bytes
-constexpr int kBgMax = kBgRing + 32 * kBgStgPitch;    // SwiGLU: largest |h| of each row's two halves
-constexpr int kBgTables = kBgMax + BM * 8;
-constexpr int kBgGroups = 512;                        // groups whose tables fit beside them
-constexpr int kBgSmem = kBgTables + (3 * kBgGroups + 1) * 4;
-static_assert(kBgSmem <= 160 * 1024, "the LDS");
+// A tile of eight waves, kWM down and kWN across, each with kFI x kFJ fragments of 32 x
+// 32.  A stage is one block of K: A and B codes as 128-byte rows, the A rows' scales and
+// the tile's weight scales; kS stages make the ring.  All of it comes by loads straight
+// into LDS through buffer descriptors: what lies past the group's last row, the matrix's
+// last row or the row's end reads as zero and moves no memory, so no size needs a tile of
+// its own, and a lane's offsets are the same for every tile.
 constexpr int kBgThreads = 512;
+constexpr int kBgGroups = 512;  // groups whose tables fit beside the ring
+template <int kWM_, int kWN_, int kFI_, int kFJ_, int kS_>
+struct BgShape {
+    static constexpr int kWM = kWM_, kWN = kWN_, kFI = kFI_, kFJ = kFJ_, kS = kS_;
+    static_assert(kWM * kWN == 8 && kFJ % 2 == 0 && kS >= 2, "eight waves; B fragments alternate between two registers");
+    static constexpr int kM = kWM * kFI * 32, kN = kWN * kFJ * 32;
+    static constexpr int kStageB = kM * kBlk;
+    static constexpr int kStageS = kStageB + kN * kBlk;  // scales: an area of 64 for each wave's load
+    static constexpr int kStage = kStageS + 8 * kWave * 4;
+    static constexpr int kRing = kS * kStage;
+    static constexpr int kMax = kRing + 32 * kN * 2;     // behind 32 staged rows; SwiGLU: largest |h| by row and wave
+    static constexpr int kTables = kMax + kM * kWN * 4;
+    static constexpr int kSmem = kTables + (3 * kBgGroups + 1) * 4;
+    static_assert(kSmem <= 160 * 1024, "the LDS");
+    static constexpr int kLoads = (kM + kN) / 64 + 1;    // of a wave and stage
+};
 
 // What a tile's loads start from, uniform in a wave: codes of this wave's A and B
-// rows, the scales of its 64 A rows (waves 0 .. 3), one weight scale (waves 4 and 5).
+// rows, and the scales of 64 A rows (the first kM / 64 waves) or one weight scale.
 struct BgSource {
     const uint8_t *a, *b;
     const float* s;
@@ -303,7 +326,7 @@ struct BgSource {
 };
 
 struct BgTile {
-    int g, row0, count, n0;  // n0: first output column; count: rows, at most BM; 0: no tile
+    int g, row0, count, n0;  // n0: first output column; count: rows, at most kM; 0: no tile
 };
 
 // LDS accesses of the epilogue, in asm: the compiler would wait for the next tile's
@@ -316,28 +339,28 @@ __device__ __forceinline__ void lds_put(uint32_t at, uint32_t v) {
 __device__ __forceinline__ void lds_put2(uint32_t at, u32x2 v) {
     asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(v) : "memory");
 }
+__device__ __forceinline__ void lds_get4(uint32_t at, u32x4& d) {
+    asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(d) : "v"(at) : "memory");
+}
 __device__ __forceinline__ void lds_get4x2(uint32_t at0, uint32_t at1, u32x4& d0, u32x4& d1) {
     asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
                  : "=&v"(d0), "=&v"(d1)
                  : "v"(at0), "v"(at1)
                  : "memory");
 }
-__device__ __forceinline__ u32x2 lds_get2(uint32_t at) {
-    u32x2 d;
-    asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(d) : "v"(at) : "memory");
-    return d;
-}
 
-template <bool kGlu>
-__global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) {
-    constexpr int kCols = kGlu ? BN / 2 : BN;  // output columns of a tile
+template <class C, bool kGlu>
+__device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
+    constexpr int kFI = C::kFI, kFJ = C::kFJ, kWM = C::kWM, kWN = C::kWN;
+    constexpr int kCols = kGlu ? C::kN / 2 : C::kN;  // output columns of a tile
+    static_assert(!kGlu || kCols == kBlk, "a block of h is a tile's columns");
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-    int32_t* s_first = (int32_t*)(smem + kBgTables);  // [groups + 1] M tiles before each group
-    int32_t* s_lo = s_first + p.groups + 1;           // [groups] its rows
+    int32_t* s_first = (int32_t*)(smem + C::kTables);  // [groups + 1] M tiles before each group
+    int32_t* s_lo = s_first + p.groups + 1;            // [groups] its rows
     int32_t* s_hi = s_lo + p.groups;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / kWN, wn = wave % kWN;
     const int KB = blk_count(p.k), NB = blk_count(p.n), NT = (p.n + kCols - 1) / kCols;
 
     if (wave == 0) {
@@ -349,7 +372,7 @@ __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) 
                 lo = p.offsets ? min(max(p.offsets[e], 0), p.rows) : 0;
                 hi = p.offsets ? min(max(p.offsets[e + 1], lo), p.rows) : p.rows;
             }
-            const int tiles = (hi - lo + BM - 1) / BM;
+            const int tiles = (hi - lo + C::kM - 1) / C::kM;
             int upto = tiles;
 #pragma unroll
             for (int s = 1; s < kWave; s *= 2) {
@@ -385,40 +408,44 @@ __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) 
         const int f0 = __builtin_amdgcn_readfirstlane(s_first[e]), f1 = __builtin_amdgcn_readfirstlane(s_first[e + 1]);
         const int in = t - f0 * NT, col = in / (f1 - f0);
         r.n0 = col * kCols;
-        r.row0 = __builtin_amdgcn_readfirstlane(s_lo[e]) + (in - col * (f1 - f0)) * BM;
-        r.count = min(__builtin_amdgcn_readfirstlane(s_hi[e]) - r.row0, BM);
+        r.row0 = __builtin_amdgcn_readfirstlane(s_lo[e]) + (in - col * (f1 - f0)) * C::kM;
+        r.count = min(__builtin_amdgcn_readfirstlane(s_hi[e]) - r.row0, C::kM);
         return r;
     };
+    constexpr int kRowsA = C::kM / 8, kRowsB = C::kN / 8;  // rows of a stage that a wave loads
+    constexpr int kScaleWaves = C::kM / 64;                // waves that load A scales
+    constexpr int kScalesW = kGlu ? 2 : C::kN / kBlk;      // weight scales of a stage
     auto source_of = [&](const BgTile& t) {
         BgSource s{};
         if (t.count == 0) return s;
-        s.a = p.a + (int64_t)(t.row0 + wave * 32) * p.k;
-        s.a_bytes = (uint32_t)max(t.count - wave * 32, 0) * (uint32_t)p.k;
-        // B rows 32 wave .. + 31 of the stage: columns n0 + 32 wave; with SwiGLU, for the column
-        // half wn = wave / 4 and fragment j = wave % 4, columns n0 + 64 wn + 32 (j % 2) of the
-        // gate's (j < 2) or the up matrix, so that a wave ends with both of its columns
-        const bool up = kGlu && (wave & 2);
-        const int br = t.n0 + (kGlu ? (wave >> 2) * 64 + (wave & 1) * 32 : wave * 32);
+        s.a = p.a + (int64_t)(t.row0 + wave * kRowsA) * p.k;
+        s.a_bytes = (uint32_t)max(t.count - wave * kRowsA, 0) * (uint32_t)p.k;
+        // B rows of the stage are columns n0 ..; with SwiGLU, of a wave's kFJ fragments the
+        // first half are columns of the gate's, the second the same of the up matrix, so that
+        // a wave ends with both (a wave then loads just one fragment's rows)
+        static_assert(!kGlu || kRowsB == 32, "");
+        const bool up = kGlu && wave % kFJ >= kFJ / 2;
+        const int br = t.n0 + (kGlu ? wave / kFJ * (kFJ * 16) + wave % (kFJ / 2) * 32 : wave * kRowsB);
         s.b = (up ? p.wu : p.w) + ((int64_t)t.g * p.n + br) * p.k;
         s.b_bytes = (uint32_t)max(p.n - br, 0) * (uint32_t)p.k;
-        if (wave < 4) {
+        if (wave < kScaleWaves) {
             s.s = p.sa + t.row0 + wave * 64;
             s.s_bytes = (uint32_t)max(t.count - wave * 64, 0) * 4;
-        } else {  // the tile's first column block (the gate's), and its second (the up matrix's)
-            const int nb = t.n0 / kBlk + (kGlu ? 0 : wave & 1);
-            s.s = (kGlu && (wave & 1) ? p.swu : p.sw) + ((int64_t)t.g * NB + nb) * KB;
-            s.s_bytes = wave < 6 && nb < NB ? 4 : 0;
+        } else {  // the tile's column blocks, or the gate's and the up matrix's
+            const int x = wave - kScaleWaves, nb = t.n0 / kBlk + (kGlu ? 0 : x);
+            s.s = (kGlu && x == 1 ? p.swu : p.sw) + ((int64_t)t.g * NB + min(nb, NB - 1)) * KB;
+            s.s_bytes = x < kScalesW && nb < NB ? 4 : 0;
         }
         return s;
     };
-    const int64_t s_step = wave < 4 ? p.rows : 1;  // scales from block to block of K
+    const int64_t s_step = wave < kScaleWaves ? p.rows : 1;  // scales from block to block of K
 
-    // Load i of a stage fills rows 32 wave + 8 i .. + 7: lane l row l / 8, chunk l % 8 in LDS,
-    // which holds the row's chunk (l % 8) ^ swz8(row).
+    // A load fills eight rows of a stage: lane l row l / 8, chunk l % 8 in LDS, which holds the
+    // row's chunk (l % 8) ^ swz8(row), that is with bit 2 turned for every other eight rows.
     const int c_even = (lane & 7) ^ (lane >> 4), c_odd = c_even ^ 4;
     const uint32_t v_even = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_even * 16;
-    const uint32_t v_odd = (uint32_t)((lane >> 3) + 8) * (uint32_t)p.k + c_odd * 16;
-    const uint32_t v_two = 16u * (uint32_t)p.k;
+    const uint32_t v_odd = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_odd * 16;
+    const uint32_t v_eight = 8u * (uint32_t)p.k;
     BgSource src, nxt;
     // Stage s of this tile, or past its last the next tile's; past the last tile's last
     // nothing is read and the slot, which no wave reads any more, is filled with zeros.
@@ -427,30 +454,37 @@ __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) 
         const BgSource q = beyond ? nxt : src;
         const int s = beyond ? s_ - KB : s_;
         const int left = q.a ? p.k - s * kBlk : 0;  // bytes of a row from this stage on
-        uint8_t* st = smem + slot * kBgStage;
-        uint8_t* base = st + wave * 32 * kBlk;
+        uint8_t* st = smem + slot * C::kStage;
         const __amdgpu_buffer_rsrc_t ra = blk_rsrc(q.a, q.a_bytes), rb = blk_rsrc(q.b, q.b_bytes);
         const bool in_e = c_even * 16 < left, in_o = c_odd * 16 < left;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = (i & 1 ? v_odd : v_even) + (i >> 1) * v_two + s * kBlk;
-            const uint32_t o = (i & 1 ? in_o : in_e) ? v : kNowhere;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + i * 1024), 16, o, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + kBgStageB + i * 1024), 16, o, 0, 0, 0);
+        for (int i = 0; i < (kRowsA > kRowsB ? kRowsA : kRowsB) / 8; ++i) {
+            // (fewer than sixteen rows to a wave: the wave's own place tells which)
+            auto at = [&](int rows) {
+                const bool odd = rows >= 16 ? (i & 1) : (wave & 1);
+                const uint32_t v = (odd ? v_odd : v_even) + i * v_eight + s * kBlk;
+                return (odd ? in_o : in_e) ? v : kNowhere;
+            };
+            if (i < kRowsA / 8)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + wave * kRowsA * kBlk + i * 1024), 16,
+                                                         at(kRowsA), 0, 0, 0);
+            if (i < kRowsB / 8)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rb, (lds_void*)(st + C::kStageB + wave * kRowsB * kBlk + i * 1024), 16, at(kRowsB), 0, 0, 0);
         }
         // (a wave without scales fills its area with zeros: a branch here would let the
         // compiler move every addition of the stage past it)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(blk_rsrc(q.s + s * s_step, left > 0 ? q.s_bytes : 0),
-                                                 (lds_void*)(st + kBgStageSA + wave * 256), 4, lane * 4, 0, 0, 0);
+                                                 (lds_void*)(st + C::kStageS + wave * 256), 4, lane * 4, 0, 0, 0);
     };
 
     const int fr = lane & 31, half = lane >> 5;
     const int fsw = swz8(fr);  // a fragment's rows differ from fr by multiples of 32
-    const int arow = (wm * 32 + fr) * kBlk, brow = kBgStageB + (wn * 128 + fr) * kBlk;
+    const int arow = (wm * 32 + fr) * kBlk, brow = C::kStageB + (wn * kFJ * 32 + fr) * kBlk;
     // The two operands' parts of a K block fall to the lanes alike: K step ks takes chunks
     // 4 ks + half and 4 ks + 2 + half.
     auto read_frag = [&](int slot, int row, intx8 (&f)[2]) {
-        const uint8_t* st = smem + slot * kBgStage + row;
+        const uint8_t* st = smem + slot * C::kStage + row;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             const intx4 lo = *(const intx4*)(st + (((4 * ks + half) ^ fsw) * 16));
@@ -458,36 +492,36 @@ __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) 
             f[ks] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     };
-    intx8 fa[2][2], fb[2][2];
-    float sa[2], sw[kGlu ? 2 : 1], sa_n[2], sw_n[kGlu ? 2 : 1];
+    intx8 fa[kFI][2], fb[2][2];
+    constexpr int kSW = kGlu ? 2 : 1;  // weight scales of a wave
+    float sa[kFI], sw[kSW], sa_n[kFI], sw_n[kSW];
     auto read_scales = [&](int slot) {
-        const float* st = (const float*)(smem + slot * kBgStage + kBgStageSA);
+        const float* st = (const float*)(smem + slot * C::kStage + C::kStageS);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sa_n[i] = st[i * 128 + wm * 32 + fr];
-        const float* w = (const float*)(smem + slot * kBgStage + kBgStageSW);
-        if constexpr (kGlu) {
-            sw_n[0] = w[0];
-            sw_n[1] = w[kWave];
-        } else {
-            sw_n[0] = w[wn * kWave];
-        }
+        for (int i = 0; i < kFI; ++i) sa_n[i] = st[(i * kWM + wm) * 32 + fr];
+        const float* w = st + kScaleWaves * kWave;
+        sw_n[0] = kGlu ? w[0] : w[wn * kFJ * 32 / kBlk * kWave];
+        if constexpr (kGlu) sw_n[1] = w[kWave];
     };
-    floatx16 acc[2][4];
-    // Fragment f = 2 j + i of a stage: both K steps from a zero accumulator, then scaled into
+    floatx16 acc[kFI][kFJ];
+    // Fragment f = j kFI + i of a stage: both K steps from a zero accumulator, then scaled into
     // the sum.  B is the first operand, so element 4 q + s of lane l is column 8 q + 4 (l / 32) +
     // s of row l % 32: a lane has one row of A, and its scale is one register.  A fragment is
     // added while the next one multiplies, the last one of a stage in the next stage; the
     // order is fixed here, since the compiler's own keeps six products at once and spills.
+    constexpr int kF = kFI * kFJ;
     floatx16 v[2];
     float sc[2];
-    auto multiply = [&](int i, int j, const intx8 (&b)[2]) {
-        v[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[0], fa[i][0], floatx16{}, 0, 0, 0, 0, 0, 0);
-        v[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[1], fa[i][1], v[i], 0, 0, 0, 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);  // then the additions: the product they take is done by now
+    auto multiply = [&](int f) {
+        const int i = f % kFI, j = f / kFI;
+        v[f & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j & 1][0], fa[i][0], floatx16{}, 0, 0, 0, 0, 0, 0);
+        v[f & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j & 1][1], fa[i][1], v[f & 1], 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);  // then an addition: the product that it takes is done by now
     };
-    auto add = [&](int i, int j) {
+    auto add = [&](int f) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) acc[i][j][c] = __builtin_fmaf(v[i][c], sc[i], acc[i][j][c]);
+        for (int c = 0; c < 16; ++c)
+            acc[f % kFI][f / kFI][c] = __builtin_fmaf(v[f & 1][c], sc[f & 1], acc[f % kFI][f / kFI][c]);
     };
     auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
 
@@ -495,183 +529,233 @@ __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) 
     BgTile tile = tile_at(t);
     if (tile.count == 0) return;
     src = source_of(tile);
-    nxt = BgSource{};
-    issue(0, 0);
-    issue(1, 1);  // KB is at least 2
+    t += step;
+    BgTile next = tile_at(t);
+    nxt = source_of(next);
+    // (KB is at least kS, so a tile's loads reach no further than the next tile)
+#pragma unroll
+    for (int s = 0; s < C::kS; ++s) issue(s, s);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     int slot = 0;
-    read_frag(0, arow, fa[0]);
-    read_frag(0, arow + 128 * kBlk, fa[1]);
+#pragma unroll
+    for (int i = 0; i < kFI; ++i) read_frag(0, arow + i * kWM * 32 * kBlk, fa[i]);
     read_frag(0, brow, fb[0]);
     read_scales(0);
     for (;;) {
-        t += step;
-        const BgTile next = tile_at(t);
-        nxt = source_of(next);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kFI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = floatx16{};
-        v[1] = floatx16{};
-        sc[1] = 0.0f;
+            for (int j = 0; j < kFJ; ++j) acc[i][j] = floatx16{};
+        v[(kF - 1) & 1] = floatx16{};
+        sc[(kF - 1) & 1] = 0.0f;
         for (int s = 0; s < KB; ++s) {
-            pin();
-            read_frag(slot, brow + 1 * 32 * kBlk, fb[1]);
-            multiply(0, 0, fb[0]);
-            add(1, 3);  // of the stage before
 #pragma unroll
-            for (int i = 0; i < 2; ++i) sa[i] = sa_n[i];
+            for (int f = 0; f < kF; ++f) {
+                const int i = f % kFI, j = f / kFI;
+                pin();
+                if (i == 0 && j < kFJ - 1) read_frag(slot, brow + (j + 1) * 32 * kBlk, fb[(j + 1) & 1]);
+                if (i == 0 && j == kFJ - 1) {
+                    // stage s + 1 has landed, and no wave reads stage s any more
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((C::kS - 2) * C::kLoads) : "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    issue(s + C::kS, slot);
+                    slot = slot == C::kS - 1 ? 0 : slot + 1;
+                    pin();
+                    read_frag(slot, brow, fb[(j + 1) & 1]);
+                    read_scales(slot);
+                }
+                multiply(f);
+                if (f == 0) {
+                    add(kF - 1);  // of the stage before
 #pragma unroll
-            for (int x = 0; x < (kGlu ? 2 : 1); ++x) sw[x] = sw_n[x];
-            sc[0] = sa[0] * sw[0];
-            sc[1] = sa[1] * sw[0];
-            pin();
-            multiply(1, 0, fb[0]);
-            add(0, 0);
-            pin();
-            read_frag(slot, brow + 2 * 32 * kBlk, fb[0]);
-            multiply(0, 1, fb[1]);
-            add(1, 0);
-            pin();
-            multiply(1, 1, fb[1]);
-            add(0, 1);
-            if constexpr (kGlu) sc[0] = sa[0] * sw[1];
-            pin();
-            read_frag(slot, brow + 3 * 32 * kBlk, fb[1]);
-            multiply(0, 2, fb[0]);
-            add(1, 1);
-            if constexpr (kGlu) sc[1] = sa[1] * sw[1];
-            pin();
-            multiply(1, 2, fb[0]);
-            add(0, 2);
-            pin();
-            // stage s + 1 has landed, and no wave reads stage s any more
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            issue(s + 2, slot);
-            slot ^= 1;
-            pin();
-            read_frag(slot, brow, fb[0]);
-            read_scales(slot);
-            multiply(0, 3, fb[1]);
-            add(1, 2);
-            pin();
-            read_frag(slot, arow, fa[0]);
-            multiply(1, 3, fb[1]);
-            add(0, 3);
-            pin();
-            read_frag(slot, arow + 128 * kBlk, fa[1]);
+                    for (int x = 0; x < kFI; ++x) sa[x] = sa_n[x];
+#pragma unroll
+                    for (int x = 0; x < kSW; ++x) sw[x] = sw_n[x];
+                } else {
+                    add(f - 1);
+                }
+                sc[f & 1] = sa[i] * sw[kGlu ? j / (kFJ / 2) : 0];
+                pin();
+                if (j == kFJ - 1) read_frag(slot, arow + i * kWM * 32 * kBlk, fa[i]);  // of the next stage
+            }
         }
-        add(1, 3);
+        add(kF - 1);
 
-        const uint32_t stg = lds_at(smem) + kBgRing;
+        const uint32_t stg = lds_at(smem) + C::kRing;
         int tid = threadIdx.x;  // opaque: the lane addresses are formed here, not kept live
         asm volatile("" : "+v"(tid));
         if constexpr (!kGlu) {
             // 32 rows at a time through LDS, chunk c of row r at c ^ r, out in whole lines
-            const int rs = tid & 31, r0 = tid >> 5, ch = tid & 31;
-            const uint32_t wrow = stg + rs * kBgStgPitch + 8 * ((tid >> 5) & 1);
-            const int wc0 = ((tid >> 6) & 1) * 16;
+            constexpr int kCh = C::kN / 8, kPitch = kCh * 16;  // chunks and bytes of a row
+            const int rs = tid & 31, r0 = tid / kCh, ch = tid % kCh;
+            const uint32_t wrow = stg + rs * kPitch + 8 * ((tid >> 5) & 1);
             const bool col_in = ch * 8 < p.n - tile.n0;  // n is a multiple of 8
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {  // tile rows 32 b ..: fragment b / 4 of the waves with wm = b % 4
+            for (int b = 0; b < C::kM / 32; ++b) {  // tile rows 32 b ..: fragment b / kWM of the waves with wm = b % kWM
                 if (b * 32 >= tile.count) break;
-                if (wm == (b & 3)) {
+                if (wm == b % kWM) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < kFJ; ++j)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const floatx16& v = acc[b >> 2][j];
-                            lds_put2(wrow + (((wc0 + 4 * j + q) ^ rs) << 4),
-                                     u32x2{pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3])});
+                            const floatx16& x = acc[b / kWM][j];
+                            lds_put2(wrow + (((wn * kFJ * 4 + 4 * j + q) ^ (rs & (kCh - 1))) << 4),
+                                     u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])});
                         }
                 }
                 lds_barrier();
-                u32x4 d0, d1;
-                lds_get4x2(stg + r0 * kBgStgPitch + ((ch ^ r0) << 4),
-                           stg + (r0 + 16) * kBgStgPitch + ((ch ^ (r0 + 16)) << 4), d0, d1);
+                constexpr int kStep = kBgThreads / kCh;  // rows that the threads take at once: 16 or 32
+                auto from = [&](int r) { return stg + r * kPitch + ((ch ^ (r & (kCh - 1))) << 4); };
                 const int row = b * 32 + r0;
                 uint16_t* dst = p.out + (int64_t)(tile.row0 + row) * p.n + tile.n0 + ch * 8;
+                u32x4 d0, d1;
+                if constexpr (kStep == 16) {
+                    lds_get4x2(from(r0), from(r0 + 16), d0, d1);
+                    if (col_in && row + 16 < tile.count) *(u32x4*)(dst + 16 * (int64_t)p.n) = d1;
+                } else {
+                    static_assert(kStep == 32, "");
+                    lds_get4(from(r0), d0);
+                }
                 if (col_in && row < tile.count) *(u32x4*)dst = d0;
-                if (col_in && row + 16 < tile.count) *(u32x4*)(dst + 16 * (int64_t)p.n) = d1;
                 lds_barrier();
             }
         } else {
-            // h in place of the gate's fragments; a row's block of 128 is two waves' columns
-            const int cl = tile.n0 + wn * 64 + 4 * half;
-            float m[2] = {0.0f, 0.0f};
+            // h in place of the gate's fragments; a row's block of 128 is kWN waves' columns
+            constexpr int kJ = kFJ / 2;
+            const int c0 = wn * kJ * 32 + 4 * half;  // this lane's first column of the tile
+            const int rl = wm * 32 + (tid & 31);
+            const uint32_t mx = lds_at(smem) + C::kMax;
+            float m[kFI];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kFI; ++i) {
+                m[i] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kJ; ++j)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float g = acc[i][j][c];
-                        float v = g / (1.0f + __expf(-g)) * acc[i][2 + j][c];
-                        if (cl + 32 * j + 8 * (c >> 2) >= p.n) v = 0.0f;  // n is a multiple of 16
-                        acc[i][j][c] = v;
-                        m[i] = fmaxf(m[i], fabsf(v));
+                        float h = g / (1.0f + __expf(-g)) * acc[i][kJ + j][c];
+                        if (tile.n0 + c0 + 32 * j + 8 * (c >> 2) >= p.n) h = 0.0f;  // n is a multiple of 16
+                        acc[i][j][c] = h;
+                        m[i] = fmaxf(m[i], fabsf(h));
                     }
-            const uint32_t mx = lds_at(smem) + kBgMax;
-            const int rl = wm * 32 + (tid & 31);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
                 m[i] = fmaxf(m[i], __shfl_xor(m[i], 32, kWave));
-                if (half == 0) lds_put(mx + ((128 * i + rl) * 2 + wn) * 4, __builtin_bit_cast(uint32_t, m[i]));
+                const float mi = m[i];  // (a cast of the array's element would be of its first one)
+                if (half == 0)
+                    lds_put(mx + ((i * kWM * 32 + rl) * kWN + wn) * 4, __builtin_bit_cast(uint32_t, mi));
             }
             lds_barrier();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (128 * i >= tile.count) break;
-                const u32x2 both = lds_get2(mx + (128 * i + rl) * 8);
-                // (of values: a cast of the vector's element itself takes its first one)
-                const uint32_t m0 = both[0], m1 = both[1];
-                const int e = blk_exp(fmaxf(__builtin_bit_cast(float, m0), __builtin_bit_cast(float, m1)));
-                const int row = tile.row0 + 128 * i + rl;
-                const bool row_in = 128 * i + rl < tile.count;
+            for (int i = 0; i < kFI; ++i) {
+                if (i * kWM * 32 >= tile.count) break;
+                u32x4 all;  // the row's maxima (with two waves across, the next row's behind them)
+                lds_get4(mx + (i * kWM * 32 + rl) * kWN * 4 / 16 * 16, all);
+                const uint32_t a0 = all[0], a1 = all[1], a2 = all[2], a3 = all[3];
+                auto f32 = [](uint32_t x) { return __builtin_bit_cast(float, x); };
+                const float lo = fmaxf(f32(a0), f32(a1)), hi = fmaxf(f32(a2), f32(a3));
+                const int e = blk_exp(kWN == 4 ? fmaxf(lo, hi) : (rl & 1 ? hi : lo));
+                const int row = tile.row0 + i * kWM * 32 + rl;
+                const bool row_in = i * kWM * 32 + rl < tile.count;
                 if (wn == 0 && half == 0 && row_in) p.hs[(int64_t)(tile.n0 / kBlk) * p.rows + row] = pow2f(e);
                 const float inv = pow2f(-e);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kJ; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const floatx16& v = acc[i][j];
-                        const int col = wn * 64 + 32 * j + 8 * q + 4 * half;
+                        const floatx16& x = acc[i][j];
+                        const int col = c0 + 32 * j + 8 * q;
                         lds_put(stg + rl * kBlk + (((col >> 4) ^ swz8(rl)) << 4) + (col & 15),
-                                fp8x4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv));
-                        if (p.h16 && row_in && cl + 32 * j + 8 * q < p.n)
+                                fp8x4(x[4 * q] * inv, x[4 * q + 1] * inv, x[4 * q + 2] * inv, x[4 * q + 3] * inv));
+                        if (p.h16 && row_in && tile.n0 + col < p.n)
                             *(u32x2*)(p.h16 + (int64_t)row * p.n + tile.n0 + col) =
-                                u32x2{pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3])};
+                                u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])};
                     }
                 lds_barrier();
-                const int r0 = tid >> 3, ch = tid & 7;  // rows r0 and r0 + 64 of these 128
-                u32x4 d0, d1;
-                lds_get4x2(stg + r0 * kBlk + ((ch ^ swz8(r0)) << 4), stg + (r0 + 64) * kBlk + ((ch ^ swz8(r0 + 64)) << 4),
-                           d0, d1);
-                uint8_t* dst = p.hq + (int64_t)(tile.row0 + 128 * i + r0) * p.n + tile.n0 + ch * 16;
+                // kWM x 32 rows of eight chunks: 64 rows at once
+                const int r0 = tid >> 3, ch = tid & 7;
                 const bool col_in = tile.n0 + ch * 16 < p.n;
-                if (col_in && 128 * i + r0 < tile.count) *(u32x4*)dst = d0;
-                if (col_in && 128 * i + r0 + 64 < tile.count) *(u32x4*)(dst + 64 * (int64_t)p.n) = d1;
+                auto from = [&](int r) { return stg + r * kBlk + ((ch ^ swz8(r)) << 4); };
+                uint8_t* dst = p.hq + (int64_t)(tile.row0 + i * kWM * 32 + r0) * p.n + tile.n0 + ch * 16;
+                u32x4 d0, d1;
+                if constexpr (kWM == 4) {
+                    lds_get4x2(from(r0), from(r0 + 64), d0, d1);
+                    if (col_in && i * kWM * 32 + r0 + 64 < tile.count) *(u32x4*)(dst + 64 * (int64_t)p.n) = d1;
+                } else {
+                    static_assert(kWM == 2, "");
+                    lds_get4(from(r0), d0);
+                }
+                if (col_in && i * kWM * 32 + r0 < tile.count) *(u32x4*)dst = d0;
                 lds_barrier();
             }
         }
         if (next.count == 0) break;
         tile = next;
         src = nxt;
+        t += step;
+        next = tile_at(t);
+        nxt = source_of(next);
     }
     // zeros may still be on their way into the ring
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+template <class C, bool kGlu>
+__global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) {
+    block_gemm_tiles<C, kGlu>(p);
+}
+
 // Parts of at most `part` rows that `rows` rows of `groups` groups can fall into.
 static int most_parts(int rows, int groups, int part) { return rows / part + (groups < rows ? groups : rows); }
 
-// Whether the large tiles are the better ones.
-bool block_gemm_large(int64_t rows, int n, int k, int groups) {
-    return groups <= kBgGroups && k > kBlk && rows > 64 * groups;
+using Bg256x256 = BgShape<4, 2, 2, 4, 2>;
+using Bg128x256 = BgShape<4, 2, 1, 4, 2>;
+using Bg128x128 = BgShape<4, 2, 1, 2, 4>;
+using Bg64x256 = BgShape<2, 4, 1, 2, 3>;
+
+enum BlockForm { kFormFew, kForm256x256, kForm128x256, kForm128x128, kForm64x256 };
+
+// The form with the least expected time, in us.  A tile takes a block of K in `low` us
+// where it is one of few and in `full` us where every CU has one, and `end` us for its
+// epilogue (fitted to products of [4096, 4096] with 256 to 4096 rows and of 32 x [7168,
+// 2048] with 1024 to 131072); tiles run in rounds of one to a CU.  Larger tiles need
+// less of everything for each element, smaller ones fill the CUs sooner and pad a
+// group's rows less.  Measured, us, tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 256 and
+// the few-row form: 1 row x [2048, 1024] -, -, 8.2, 9.2, 3.7; 64 x [4096, 4096] -, -,
+// 21, 26, 13; 256: 54, 35, 23, 27, 39; 2048: 57, 43, 52, 58, 268; 4096: 68, 86, 103, 104,
+// 531; 32 groups of [7168, 2048]: 64 rows -, -, 80, 75, 79; 1024: 121, 105, 99, 93, 116;
+// 8192: 202, 212, 220, 227, 957; 131072: 2107, 2573, 2821, 2984, 14243.
+static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
+    const double r = (double)rows, kb = blk_count(k);
+    const double active = std::min(r, groups * (1.0 - exp(-r / groups)));  // groups with rows, routed evenly
+    auto parts = [&](int m) {  // of m rows: half a part of padding to a group
+        return groups == 1 ? ceil(r / m) : std::max(active, r / m + active / 2);
+    };
+    const double per_group = r / active;
+    const double strips = ((n + 15) / 16) * parts(kBfRows) / 256;
+    BlockForm best = kFormFew;
+    double least = 3.5 + kb * 0.14 * (glu ? 2 : 1) * (per_group <= 16 ? 1.0 : per_group <= 32 ? 1.4 : 2.0) *
+                             std::max(1.0, strips);
+    if (groups > kBgGroups) return best;
+    const struct { BlockForm form; int m, n, stages; double low, full, end; } tiles[] = {
+        {kForm256x256, 256, 256, Bg256x256::kS, 1.55, 2.3, 4}, {kForm128x256, 128, 256, Bg128x256::kS, 1.0, 1.41, 3},
+        {kForm128x128, 128, 128, Bg128x128::kS, 0.62, 0.78, 2}, {kForm64x256, 64, 256, Bg64x256::kS, 0.72, 0.83, 2}};
+    for (const auto& t : tiles) {
+        if (kb < t.stages || (glu && t.n != 256)) continue;  // a block of h is half of 256 columns
+        const int cols = glu ? t.n / 2 : t.n;
+        const double rounds = parts(t.m) * ((n + cols - 1) / cols) / 256;
+        const double us = 4 + (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds) *
+                                  (kb * (rounds <= 1 ? t.low : t.full) + t.end);
+        if (us < least) {
+            least = us;
+            best = t.form;
+        }
+    }
+    return best;
 }
+
+bool block_gemm_large(int64_t rows, int n, int k, int groups) { return block_form(rows, n, k, groups, true) != kFormFew; }
 
 static void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream) {
 #define BLOCK_FEW(NF, GLU)                                                                                      \
@@ -690,18 +774,32 @@ static void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream) {
 #undef BLOCK_FEW
 }
 
-void launch_block_gemm(const BlockGemm& a, hipStream_t stream) {
-    if (!block_gemm_large(a.rows, a.n, a.k, a.groups)) {
-        launch_block_gemm_few(a, stream);
-        return;
-    }
-    const int cols = a.wu ? BN / 2 : BN;
-    const int64_t tiles = (int64_t)most_parts(a.rows, a.groups, BM) * ((a.n + cols - 1) / cols);
+template <class C, bool kGlu>
+static void launch_block_gemm_tiles(const BlockGemm& a, hipStream_t stream) {
+    const int cols = kGlu ? C::kN / 2 : C::kN;
+    const int64_t tiles = (int64_t)most_parts(a.rows, a.groups, C::kM) * ((a.n + cols - 1) / cols);
     const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256);  // a multiple of the XCDs
-    if (a.wu)
-        hipLaunchKernelGGL(block_gemm_kernel<true>, dim3(grid), dim3(kBgThreads), kBgSmem, stream, a);
-    else
-        hipLaunchKernelGGL(block_gemm_kernel<false>, dim3(grid), dim3(kBgThreads), kBgSmem, stream, a);
+    hipLaunchKernelGGL((block_gemm_kernel<C, kGlu>), dim3(grid), dim3(kBgThreads), C::kSmem, stream, a);
+}
+
+void launch_block_gemm(const BlockGemm& a, hipStream_t stream) {
+    const bool glu = a.wu != nullptr;
+    switch (block_form(a.rows, a.n, a.k, a.groups, glu)) {
+        case kFormFew: launch_block_gemm_few(a, stream); return;
+        case kForm256x256:
+            if (glu) launch_block_gemm_tiles<Bg256x256, true>(a, stream);
+            else launch_block_gemm_tiles<Bg256x256, false>(a, stream);
+            return;
+        case kForm128x256:
+            if (glu) launch_block_gemm_tiles<Bg128x256, true>(a, stream);
+            else launch_block_gemm_tiles<Bg128x256, false>(a, stream);
+            return;
+        case kForm128x128: launch_block_gemm_tiles<Bg128x128, false>(a, stream); return;
+        case kForm64x256:
+            if (glu) launch_block_gemm_tiles<Bg64x256, true>(a, stream);
+            else launch_block_gemm_tiles<Bg64x256, false>(a, stream);
+            return;
+    }
 }
 
 }  // namespace moe
