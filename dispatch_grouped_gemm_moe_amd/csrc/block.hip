@@ -30,6 +30,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t blk_rsrc(const void* p, uint32
 
 __device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 
+// silu(g) * u with the hardware's reciprocal (1 ulp) for the division
+__device__ __forceinline__ float blk_swiglu(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
 // Part `slot` of the rows: groups in ascending order, each in parts of kRows rows (the
 // last one shorter).  False past the last part.  Offsets outside the rows are cut off,
 // so whatever the table holds, no row outside them is named.  Uniform in the wave.
@@ -263,7 +268,7 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
             if constexpr (kGlu) {
                 const floatx4 u = joined(kNF + f);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = v[x] / (1.0f + __expf(-v[x])) * u[x];
+                for (int x = 0; x < 4; ++x) v[x] = blk_swiglu(v[x], u[x]);
             }
             if (r >= count || col >= a.n) continue;  // n is a multiple of 8: four columns are inside or not
             const int64_t at = (int64_t)(row0 + r) * a.n + col;
@@ -301,6 +306,7 @@ __global__ __launch_bounds__(kBfWaves * kWave, 2) void block_few_kernel(BlockGem
 // its own, and a lane's offsets are the same for every tile.
 constexpr int kBgThreads = 512;
 constexpr int kBgGroups = 512;  // groups whose tables fit beside the ring
+constexpr int kBgStg = 2048;    // a wave's staged output
 template <int kWM_, int kWN_, int kFI_, int kFJ_, int kS_>
 struct BgShape {
     static constexpr int kWM = kWM_, kWN = kWN_, kFI = kFI_, kFJ = kFJ_, kS = kS_;
@@ -310,7 +316,7 @@ struct BgShape {
     static constexpr int kStageS = kStageB + kN * kBlk;  // scales: an area of 64 for each wave's load
     static constexpr int kStage = kStageS + 8 * kWave * 4;
     static constexpr int kRing = kS * kStage;
-    static constexpr int kMax = kRing + 32 * kN * 2;     // behind 32 staged rows; SwiGLU: largest |h| by row and wave
+    static constexpr int kMax = kRing + 8 * kBgStg;      // behind the staged output; SwiGLU: largest |h| by row and wave
     static constexpr int kTables = kMax + kM * kWN * 4;
     static constexpr int kSmem = kTables + (3 * kBgGroups + 1) * 4;
     static_assert(kSmem <= 160 * 1024, "the LDS");
@@ -344,6 +350,14 @@ __device__ __forceinline__ void lds_get4(uint32_t at, u32x4& d) {
 }
 __device__ __forceinline__ void lds_get4x2(uint32_t at0, uint32_t at1, u32x4& d0, u32x4& d1) {
     asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(d0), "=&v"(d1)
+                 : "v"(at0), "v"(at1)
+                 : "memory");
+}
+
+// The wave's own writes, then two reads: LDS serves a wave in order.
+__device__ __forceinline__ void lds_put_get(uint32_t at0, uint32_t at1, u32x4& d0, u32x4& d1) {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\tds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
                  : "=&v"(d0), "=&v"(d1)
                  : "v"(at0), "v"(at1)
                  : "memory");
@@ -587,40 +601,40 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         int tid = threadIdx.x;  // opaque: the lane addresses are formed here, not kept live
         asm volatile("" : "+v"(tid));
         if constexpr (!kGlu) {
-            // 32 rows at a time through LDS, chunk c of row r at c ^ r, out in whole lines
-            constexpr int kCh = C::kN / 8, kPitch = kCh * 16;  // chunks and bytes of a row
-            const int rs = tid & 31, r0 = tid / kCh, ch = tid % kCh;
-            const uint32_t wrow = stg + rs * kPitch + 8 * ((tid >> 5) & 1);
-            const bool col_in = ch * 8 < p.n - tile.n0;  // n is a multiple of 8
+            // 16 rows of 64 columns at a time through the wave's own block of LDS (chunk c of row r
+            // at c ^ swz8(r)) and out in whole lines; no barrier, so the waves part here.  (32 rows of
+            // all columns at a time by the whole workgroup, with two barriers each: 6.8 us a tile of
+            // 256 x 256.)
+            const uint32_t blk = stg + wave * kBgStg;
+            const int l = tid & 63, r16 = l & 15, h2 = (l >> 5) & 1, r0 = l >> 3, ch = l & 7;
+            const uint32_t put = blk + r16 * kBlk + 8 * h2;
+            const uint32_t g0 = blk + r0 * kBlk + ((ch ^ swz8(r0)) << 4), g1 = blk + (r0 + 8) * kBlk + ((ch ^ swz8(r0 + 8)) << 4);
 #pragma unroll
-            for (int b = 0; b < C::kM / 32; ++b) {  // tile rows 32 b ..: fragment b / kWM of the waves with wm = b % kWM
-                if (b * 32 >= tile.count) break;
-                if (wm == b % kWM) {
+            for (int i = 0; i < kFI; ++i)
 #pragma unroll
-                    for (int j = 0; j < kFJ; ++j)
+                for (int h = 0; h < 2; ++h) {
+                    const int row = (i * kWM + wm) * 32 + 16 * h;
+                    if (row >= tile.count) break;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const floatx16& x = acc[b / kWM][j];
-                            lds_put2(wrow + (((wn * kFJ * 4 + 4 * j + q) ^ (rs & (kCh - 1))) << 4),
-                                     u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])});
+                    for (int jp = 0; jp < kFJ / 2; ++jp) {
+                        if (((l >> 4) & 1) == h) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const floatx16& x = acc[i][2 * jp + (c >> 2)];
+                                const int q = c & 3;
+                                lds_put2(put + ((c ^ swz8(r16)) << 4),
+                                         u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])});
+                            }
                         }
+                        u32x4 d0, d1;
+                        lds_put_get(g0, g1, d0, d1);
+                        const int col = tile.n0 + (wn * kFJ + 2 * jp) * 32 + ch * 8;
+                        uint16_t* dst = p.out + (int64_t)(tile.row0 + row + r0) * p.n + col;
+                        const bool col_in = col < p.n;  // n is a multiple of 8
+                        if (col_in && row + r0 < tile.count) *(u32x4*)dst = d0;
+                        if (col_in && row + r0 + 8 < tile.count) *(u32x4*)(dst + 8 * (int64_t)p.n) = d1;
+                    }
                 }
-                lds_barrier();
-                constexpr int kStep = kBgThreads / kCh;  // rows that the threads take at once: 16 or 32
-                auto from = [&](int r) { return stg + r * kPitch + ((ch ^ (r & (kCh - 1))) << 4); };
-                const int row = b * 32 + r0;
-                uint16_t* dst = p.out + (int64_t)(tile.row0 + row) * p.n + tile.n0 + ch * 8;
-                u32x4 d0, d1;
-                if constexpr (kStep == 16) {
-                    lds_get4x2(from(r0), from(r0 + 16), d0, d1);
-                    if (col_in && row + 16 < tile.count) *(u32x4*)(dst + 16 * (int64_t)p.n) = d1;
-                } else {
-                    static_assert(kStep == 32, "");
-                    lds_get4(from(r0), d0);
-                }
-                if (col_in && row < tile.count) *(u32x4*)dst = d0;
-                lds_barrier();
-            }
         } else {
             // h in place of the gate's fragments; a row's block of 128 is kWN waves' columns
             constexpr int kJ = kFJ / 2;
@@ -636,7 +650,7 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float g = acc[i][j][c];
-                        float h = g / (1.0f + __expf(-g)) * acc[i][kJ + j][c];
+                        float h = blk_swiglu(g, acc[i][kJ + j][c]);
                         if (tile.n0 + c0 + 32 * j + 8 * (c >> 2) >= p.n) h = 0.0f;  // n is a multiple of 16
                         acc[i][j][c] = h;
                         m[i] = fmaxf(m[i], fabsf(h));
