@@ -32,21 +32,34 @@ static int row_lanes_log(int cols) {
     return s;
 }
 
-// Slices of 8 << log columns that a row falls into.
-static unsigned row_slices(int cols, int log) { return (unsigned)((cols / kRowVec + (1 << log) - 1) >> log); }
-
 static unsigned row_grid(int64_t units) { return (unsigned)(units < (1 << 22) ? units : (1 << 22)); }
+
+// Workgroups that share a token's columns: one where the tokens alone fill the CUs,
+// which then reads the token's table once.
+static unsigned row_slices(int64_t groups, int cols, int log) {
+    const int slices = (cols / kRowVec + (1 << log) - 1) >> log;
+    return (unsigned)(groups >= 2048 ? 1 : slices);
+}
+
+// An entry of a table that no kernel changes while it is read, of a token that is the
+// same in the whole wave: a scalar load.
+template <class T>
+__device__ __forceinline__ T ld_uniform(const T* p) {
+    return *(const __attribute__((address_space(4))) T*)p;
+}
 
 // ---------------------------------------------------------------------------
 // Dispatch, and the quantiser (a dispatch of every row to itself)
 // ---------------------------------------------------------------------------
 
-// A workgroup takes kRowThreads >> log tokens at a time, 8 << log of their columns.
-template <bool kCodes>
+// A workgroup takes kRowThreads >> log tokens at a time.  kWide: one wave's lanes share
+// a token (rows of more than 256 columns).
+template <bool kCodes, bool kWide>
 __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch a, int log) {
     const int lanes = 1 << log, per = kRowThreads >> log;
-    const int lid = threadIdx.x & (lanes - 1), sub = threadIdx.x >> log;
-    const int nv = a.cols / kRowVec, p = blockIdx.y * lanes + lid;
+    const int lid = threadIdx.x & (lanes - 1);
+    const int sub = kWide ? __builtin_amdgcn_readfirstlane(threadIdx.x >> log) : threadIdx.x >> log;
+    const int nv = a.cols / kRowVec;
     int64_t t_lo = 0, t_hi = a.tokens;
     if (a.offsets) {
         t_lo = max(a.offsets[0], 0);
@@ -54,39 +67,44 @@ __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch
     }
     for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < t_hi; t0 += (int64_t)gridDim.x * per) {
         const int64_t t = t0 + sub;
-        const bool live = t >= t_lo && t < t_hi && p < nv;
-        intx4 raw = {0, 0, 0, 0};
-        float v[8];
-        if (live) {
-            if (a.xf) {
-                const floatx4* s = (const floatx4*)(a.xf + t * a.cols + (int64_t)p * kRowVec);
-                const floatx4 f0 = s[0], f1 = s[1];
+        const bool tok = t >= t_lo && t < t_hi;
+        // (whole groups of 16 lanes: they share a block's maximum)
+        for (int p = blockIdx.y * lanes + lid; (p & ~15) < nv; p += gridDim.y * lanes) {
+            const bool live = tok && p < nv;
+            intx4 raw = {0, 0, 0, 0};
+            float v[8];
+            if (live) {
+                if (kCodes && a.xf) {
+                    const floatx4* s = (const floatx4*)(a.xf + t * a.cols + (int64_t)p * kRowVec);
+                    const floatx4 f0 = s[0], f1 = s[1];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] = c < 4 ? f0[c] : f1[c - 4];
-            } else {
-                raw = *(const intx4*)(a.x + t * a.cols + (int64_t)p * kRowVec);
+                    for (int c = 0; c < 8; ++c) v[c] = c < 4 ? f0[c] : f1[c - 4];
+                } else {
+                    raw = *(const intx4*)(a.x + t * a.cols + (int64_t)p * kRowVec);
+                }
             }
-        }
-        uint64_t q = 0;
-        float scale = 0.0f;
-        if constexpr (kCodes) {
-            if (!a.xf) unpack_bf16x8(raw, v);
-            float m = live ? abs_max8(v) : 0.0f;  // past the row's end: zeros
-#pragma unroll
-            for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s, kWave));
-            const int e = blk_exp(m);
-            scale = pow2f(e);
-            q = blk_codes8(v, e);
-            if (a.xf) raw = pack_bf16x8(v);
-        }
-        if (!live) continue;
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t r = a.tok_row ? (int64_t)a.tok_row[t * a.k + j] : t;
-            if (r < 0 || r >= a.rows) continue;  // no row
-            if (a.dst) *(intx4*)(a.dst + r * a.cols + (int64_t)p * kRowVec) = raw;
+            uint64_t q = 0;
+            float scale = 0.0f;
             if constexpr (kCodes) {
-                *(uint64_t*)(a.codes + r * a.cols + (int64_t)p * kRowVec) = q;
-                if ((p & 15) == 0) a.scales[(int64_t)(p >> 4) * a.rows + r] = scale;
+                if (!a.xf) unpack_bf16x8(raw, v);
+                float m = live ? abs_max8(v) : 0.0f;  // past the row's end: zeros
+#pragma unroll
+                for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s, kWave));
+                const int e = blk_exp(m);
+                scale = pow2f(e);
+                q = blk_codes8(v, e);
+                if (a.xf) raw = pack_bf16x8(v);
+            }
+            if (!live) continue;
+            for (int j = 0; j < a.k; ++j) {
+                const int32_t* at = a.tok_row + t * a.k + j;
+                const int64_t r = !a.tok_row ? t : kWide ? ld_uniform(at) : *at;
+                if (r < 0 || r >= a.rows) continue;  // no row
+                if (a.dst) *(intx4*)(a.dst + r * a.cols + (int64_t)p * kRowVec) = raw;
+                if constexpr (kCodes) {
+                    *(uint64_t*)(a.codes + r * a.cols + (int64_t)p * kRowVec) = q;
+                    if ((p & 15) == 0) a.scales[(int64_t)(p >> 4) * a.rows + r] = scale;
+                }
             }
         }
     }
@@ -94,11 +112,18 @@ __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch
 
 void launch_rows_dispatch(const RowsDispatch& a, hipStream_t stream) {
     const int log = row_lanes_log(a.cols), per = kRowThreads >> log;
-    const dim3 grid(row_grid((a.tokens + per - 1) / per), row_slices(a.cols, log));
-    if (a.codes)
-        hipLaunchKernelGGL(rows_dispatch_kernel<true>, grid, dim3(kRowThreads), 0, stream, a, log);
-    else
-        hipLaunchKernelGGL(rows_dispatch_kernel<false>, grid, dim3(kRowThreads), 0, stream, a, log);
+    const int64_t groups = (a.tokens + per - 1) / per;
+    const dim3 grid(row_grid(groups), row_slices(groups, a.cols, log));
+#define ROWS_DISPATCH(CODES, WIDE) \
+    hipLaunchKernelGGL((rows_dispatch_kernel<CODES, WIDE>), grid, dim3(kRowThreads), 0, stream, a, log)
+    if (a.codes) {
+        if (log >= 6) ROWS_DISPATCH(true, true);
+        else ROWS_DISPATCH(true, false);
+    } else {
+        if (log >= 6) ROWS_DISPATCH(false, true);
+        else ROWS_DISPATCH(false, false);
+    }
+#undef ROWS_DISPATCH
 }
 
 // ---------------------------------------------------------------------------
@@ -107,47 +132,54 @@ void launch_rows_dispatch(const RowsDispatch& a, hipStream_t stream) {
 
 // The sum over a token's rows in fp32, choice by choice in ascending order, rounded
 // once.  Eight rows' loads are in flight at a time.
+template <bool kWide>
 __global__ __launch_bounds__(kRowThreads) void rows_combine_kernel(RowsCombine a, int log) {
     const int lanes = 1 << log, per = kRowThreads >> log;
-    const int lid = threadIdx.x & (lanes - 1), sub = threadIdx.x >> log;
-    const int p = blockIdx.y * lanes + lid;
-    if (p >= a.cols / kRowVec) return;  // no barrier follows
+    const int lid = threadIdx.x & (lanes - 1);
+    const int sub = kWide ? __builtin_amdgcn_readfirstlane(threadIdx.x >> log) : threadIdx.x >> log;
+    const int nv = a.cols / kRowVec;
     for (int64_t t = (int64_t)blockIdx.x * per + sub; t < a.tokens; t += (int64_t)gridDim.x * per) {
-        float sum[8] = {};
-        if (a.add) unpack_bf16x8(*(const intx4*)(a.add + t * a.cols + (int64_t)p * kRowVec), sum);
-        for (int j0 = 0; j0 < a.k; j0 += 8) {
-            intx4 raw[8];
-            float w[8];
-            bool in[8];
+        for (int p = blockIdx.y * lanes + lid; p < nv; p += gridDim.y * lanes) {
+            const int64_t col = (int64_t)p * kRowVec;
+            float sum[8] = {};
+            if (a.add) unpack_bf16x8(*(const intx4*)(a.add + t * a.cols + col), sum);
+            for (int j0 = 0; j0 < a.k; j0 += 8) {
+                intx4 raw[8];
+                float w[8];
+                bool in[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                int64_t r = -1;
-                w[j] = 1.0f;
-                if (j0 + j < a.k) {
-                    r = a.tok_row[t * a.k + j0 + j];
-                    if (a.w) w[j] = a.w[t * a.k + j0 + j];
+                for (int j = 0; j < 8; ++j) {
+                    int64_t r = -1;
+                    w[j] = 1.0f;
+                    if (j0 + j < a.k) {
+                        const int64_t at = t * a.k + j0 + j;
+                        r = kWide ? ld_uniform(a.tok_row + at) : a.tok_row[at];
+                        if (a.w) w[j] = kWide ? ld_uniform(a.w + at) : a.w[at];
+                    }
+                    in[j] = r >= 0 && r < a.rows;
+                    raw[j] = intx4{0, 0, 0, 0};
+                    if (in[j]) raw[j] = *(const intx4*)(a.src + r * a.cols + col);
                 }
-                in[j] = r >= 0 && r < a.rows;
-                raw[j] = intx4{0, 0, 0, 0};
-                if (in[j]) raw[j] = *(const intx4*)(a.src + r * a.cols + (int64_t)p * kRowVec);
-            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v[8];
-                unpack_bf16x8(raw[j], v);
-                if (in[j])  // (a missing row's weight may be a NaN)
+                for (int j = 0; j < 8; ++j) {
+                    float v[8];
+                    unpack_bf16x8(raw[j], v);
+                    if (in[j])  // (a missing row's weight may be a NaN)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) sum[c] = __builtin_fmaf(w[j], v[c], sum[c]);
+                        for (int c = 0; c < 8; ++c) sum[c] = __builtin_fmaf(w[j], v[c], sum[c]);
+                }
             }
+            *(intx4*)(a.out + t * a.cols + col) = pack_bf16x8(sum);
         }
-        *(intx4*)(a.out + t * a.cols + (int64_t)p * kRowVec) = pack_bf16x8(sum);
     }
 }
 
 void launch_rows_combine(const RowsCombine& a, hipStream_t stream) {
     const int log = row_lanes_log(a.cols), per = kRowThreads >> log;
-    hipLaunchKernelGGL(rows_combine_kernel, dim3(row_grid((a.tokens + per - 1) / per), row_slices(a.cols, log)),
-                       dim3(kRowThreads), 0, stream, a, log);
+    const int64_t groups = (a.tokens + per - 1) / per;
+    const dim3 grid(row_grid(groups), row_slices(groups, a.cols, log));
+    if (log >= 6) hipLaunchKernelGGL(rows_combine_kernel<true>, grid, dim3(kRowThreads), 0, stream, a, log);
+    else hipLaunchKernelGGL(rows_combine_kernel<false>, grid, dim3(kRowThreads), 0, stream, a, log);
 }
 
 // ---------------------------------------------------------------------------
@@ -248,7 +280,7 @@ __global__ __launch_bounds__(kRowThreads) void rows_combine_bwd_kernel(RowsCombi
 
 void launch_rows_combine_bwd(const RowsCombineBwd& a, hipStream_t stream) {
     const int log = row_lanes_log(a.cols), per = kRowThreads >> log;
-    const int slices = (int)row_slices(a.cols, log);
+    const int slices = (a.cols / kRowVec + (1 << log) - 1) >> log;
     const int64_t units = (a.tokens + per - 1) / per;
 #define ROWS_BWD(K)                                                                                             \
     do {                                                                                                        \
