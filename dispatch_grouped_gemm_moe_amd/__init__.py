@@ -35,6 +35,7 @@ EXPORTS = ("moe_status_string", "moe_abi_version", "moe_validate_cfg", "moe_quer
            "moe_block_gemm_swiglu", "moe_query_grad_norm", "moe_grad_norm", "moe_clip_grads")
 MOE_STATIC_WORKSPACE_BYTES = 256 << 20
 MOE_FEW_MAX_TOKENS, MOE_FEW_COUNTER_BYTES = 64, 36864
+MOE_GRAD_COUNTER_BYTES = 8448
 KERNEL_KINDS = ("route", "layout", "gemm_gate_up", "gemm_down", "combine", "gather", "other", "wgrad",
                 "dgrad_down", "dgrad_gate_up", "shared_gemm", "layer")
 
@@ -485,7 +486,7 @@ def moe_block_gemm_swiglu(a, a_scales, wg, wg_scales, wu, wu_scales, h_codes, h_
 
 
 def moe_query_grad_norm(tensors) -> int:
-    """Bytes of moe_grad_norm's workspace for so many tensors; its first 256 are zeroed once by the caller."""
+    """Bytes of moe_grad_norm's workspace for so many tensors; its first MOE_GRAD_COUNTER_BYTES are zeroed once."""
     fn, n = "moe_query_grad_norm", ctypes.c_size_t()
     if not 0 <= tensors < 1 << 31:
         raise MoeError(fn, MOE_E_INVALID)
@@ -514,7 +515,7 @@ def _grad_arrays(fn, dev, grads, like=None):
 
 def moe_grad_norm(grads, norm, ws, stream=None):
     """norm (one fp32 element) = the norm of all tensors' (fp32 or bf16) elements together; ws:
-    moe_query_grad_norm bytes, the first 256 of them zeroed once."""
+    moe_query_grad_norm bytes, the first MOE_GRAD_COUNTER_BYTES of them zeroed once."""
     if torch is None:
         _use_torch()
     fn, dev = "moe_grad_norm", norm.get_device()

@@ -1143,13 +1143,13 @@ moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gro
 
 // ---- gradient norm and clipping ----
 
-constexpr size_t kGradCounterBytes = 256;
+static_assert(MOE_GRAD_COUNTER_BYTES >= kGradLines * kGradLineInts * 4, "a cache line for each counter");
 
 moe_status moe_query_grad_norm(int32_t tensors, size_t* workspace) {
     if (!workspace || tensors < 1) return MOE_E_INVALID;
     if (tensors > (1 << 20)) return MOE_E_UNSUPPORTED;
     const size_t launches = ((size_t)tensors + kGradTensors - 1) / kGradTensors;
-    *workspace = kGradCounterBytes + launches * kGradSlots * sizeof(double);
+    *workspace = MOE_GRAD_COUNTER_BYTES + launches * kGradSlots * sizeof(double);
     return MOE_OK;
 }
 
@@ -1190,14 +1190,14 @@ moe_status moe_grad_norm(int32_t tensors, const void* const* grads, const int64_
     size_t need = 0;
     moe_query_grad_norm(tensors, &need);
     if (ws_bytes < need) return MOE_E_WORKSPACE;
-    int* counter = (int*)ws;
-    double* partial = (double*)((uint8_t*)ws + kGradCounterBytes);
+    int* counters = (int*)ws;
+    double* partial = (double*)((uint8_t*)ws + MOE_GRAD_COUNTER_BYTES);
     int slots = 0;
     for (int32_t i = 0; i < tensors; i += kGradTensors) {
         const GradList a = grad_list(tensors, grads, counts, is_bf16, nullptr, i);
         const bool last = i + kGradTensors >= tensors;
         TIMED(MOE_K_OTHER, (hipStream_t)stream,
-              slots = launch_grad_norm(a, partial, slots, last, counter, norm, (hipStream_t)stream));
+              slots = launch_grad_norm(a, partial, slots, last, counters, norm, (hipStream_t)stream));
     }
     return check_launch();
 }

@@ -496,6 +496,8 @@ void launch_block_dequant(const uint8_t* codes, const float* scales, int64_t row
 
 constexpr int kGradTensors = 96;   // of one launch: what the kernel's arguments (4 KB) hold
 constexpr int kGradSlots = 2048;   // partial sums of one launch
+constexpr int kGradLineInts = 32;  // a counter's cache line; one for 32 workgroups each and one above them
+constexpr int kGradLines = 1 + kGradSlots / 32;
 constexpr uint64_t kGradBf16 = 1ull << 63;  // in a count: the tensor is bf16
 struct GradList {
     int n, chunk;                     // tensors; elements of a workgroup's step
@@ -506,7 +508,7 @@ struct GradList {
 };
 static_assert(sizeof(GradList) + 64 <= 4096, "the kernel's arguments");
 // Returns the slots used up to and with this launch; the last launch of a call joins them all.
-int launch_grad_norm(GradList a, double* partial, int slot0, bool last, int* counter, float* norm, hipStream_t stream);
+int launch_grad_norm(GradList a, double* partial, int slot0, bool last, int* counters, float* norm, hipStream_t stream);
 void launch_grad_clip(GradList a, const float* norm, float max_norm, hipStream_t stream);
 
 // ---- products in blocks of 128 (block.hip) ----

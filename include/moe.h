@@ -548,8 +548,9 @@ moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gro
  *       is not used); is_bf16: host array, non-zero where the tensor is bf16, else
  *       it is fp32; NULL: all fp32;
  *   norm: device fp32.  Summed in 64 bits, so no fp32 square overflows;
- *   ws: moe_query_grad_norm bytes, 16-byte aligned; zero its first 256 bytes once
- *       when it is allocated (every call leaves them zero).  One call at a time:
+ *   ws: moe_query_grad_norm bytes, 16-byte aligned; zero its first
+ *       MOE_GRAD_COUNTER_BYTES bytes once when it is allocated (every call leaves them
+ *       zero).  One call at a time:
  *       calls that overlap on two streams take a workspace each.
  * max_norm must be positive; a NaN norm makes every gradient NaN, an infinite one
  * zero (an infinite gradient NaN).  Tensors need the alignment of their type only;
@@ -559,6 +560,7 @@ moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gro
  * 0 (infinity is: it scales by 1); MOE_E_WORKSPACE for a smaller workspace;
  * MOE_E_UNSUPPORTED for more than 2^20 tensors or 2^48 elements in one.
  */
+#define MOE_GRAD_COUNTER_BYTES 8448
 moe_status moe_query_grad_norm(int32_t tensors, size_t *workspace);
 moe_status moe_grad_norm(int32_t tensors, const void *const *grads, const int64_t *counts, const uint8_t *is_bf16,
                          float *norm, void *ws, size_t ws_bytes, void *stream);

@@ -75,7 +75,7 @@ def test_binding_refuses_tensors_the_kernels_cannot_read():
 
 def _ws(n):
     ws = torch.full((moe.moe_query_grad_norm(n),), 0xff, dtype=torch.uint8, device="cuda")
-    ws[:256] = 0
+    ws[:moe.MOE_GRAD_COUNTER_BYTES] = 0
     return ws
 
 
@@ -111,7 +111,7 @@ def test_norm_and_clip(gpu_lib, case):
         moe.moe_grad_norm(grads, norm, ws)
         torch.cuda.synchronize()
         runs.append(norm.cpu().clone())
-        assert not ws[:256].any()
+        assert not ws[:moe.MOE_GRAD_COUNTER_BYTES].any()
     assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2]) and runs[0][1] == 77
     assert abs(runs[0][0].double() - want) <= want * (2.0 ** -24 + 2.0 ** -40)
     for max_norm in (float(want) * 0.3 + 1e-3, float(want) * 3 + 1, float("inf")):
@@ -203,7 +203,7 @@ def test_captured_replayed_and_on_another_stream(gpu_lib):
         assert abs(norm.item() / (want[0].item() * 2 ** i) - 1) < 1e-6
         moe.moe_grad_norm(out, norm, ws)  # eager work on the same workspace, between replays
         assert abs(norm.item() - 1) < 2e-3
-        assert not ws[:256].any()
+        assert not ws[:moe.MOE_GRAD_COUNTER_BYTES].any()
 
 
 @pytest.mark.gpu
