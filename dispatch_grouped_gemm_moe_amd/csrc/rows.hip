@@ -25,8 +25,8 @@ constexpr int kRowVec = 8;
 
 // Threads that share a token: a power of two from 16 (a block of 128) to the
 // workgroup, so that narrow rows stand side by side in a workgroup.
-static int row_lanes_log(int cols) {
-    const int nv = (cols + kRowVec - 1) / kRowVec;
+static int row_lanes_log(int cols, int vec = kRowVec) {
+    const int nv = (cols + vec - 1) / vec;
     int s = 4;
     while (s < 8 && (1 << s) < nv) ++s;
     return s;
@@ -36,10 +36,26 @@ static unsigned row_grid(int64_t units) { return (unsigned)(units < (1 << 22) ? 
 
 // Workgroups that share a token's columns: one where the tokens alone fill the CUs,
 // which then reads the token's table once.
-static unsigned row_slices(int64_t groups, int cols, int log) {
-    const int slices = (cols / kRowVec + (1 << log) - 1) >> log;
+static unsigned row_slices(int64_t groups, int cols, int log, int vec = kRowVec) {
+    const int slices = (cols / vec + (1 << log) - 1) >> log;
     return (unsigned)(groups >= 2048 ? 1 : slices);
 }
+
+// Loads and stores of rows; kStream: the rows are more than the last cache's 256 MB, so
+// they leave the caches to others.  (16384 tokens of 7168 and 8 rows each, 1.9 GB of rows:
+// combine 421 -> 365 us, its gradient 764 -> 751, dispatch 412 -> 404; but 20000 tokens of
+// 128 and 4 rows each, 20 MB: combine 7.7 -> 9.4.)
+template <bool kStream>
+__device__ __forceinline__ intx4 ld_row(const void* p) {
+    if (kStream) return __builtin_nontemporal_load((const intx4*)p);
+    return *(const intx4*)p;
+}
+template <bool kStream>
+__device__ __forceinline__ void st_row(void* p, intx4 v) {
+    if (kStream) __builtin_nontemporal_store(v, (intx4*)p);
+    else *(intx4*)p = v;
+}
+static bool streams(int64_t rows, int64_t row_bytes) { return rows * row_bytes > (256ll << 20); }
 
 // An entry of a table that no kernel changes while it is read, of a token that is the
 // same in the whole wave: a scalar load.
@@ -52,14 +68,16 @@ __device__ __forceinline__ T ld_uniform(const T* p) {
 // Dispatch, and the quantiser (a dispatch of every row to itself)
 // ---------------------------------------------------------------------------
 
-// A workgroup takes kRowThreads >> log tokens at a time.  kWide: one wave's lanes share
-// a token (rows of more than 256 columns).
-template <bool kCodes, bool kWide>
+// A workgroup takes kRowThreads >> log tokens at a time.  A thread has eight
+// consecutive values, or with codes sixteen, which leave as 16 bytes; a block's eight
+// lanes share its maximum.  kWide: one wave's lanes share a token.
+template <bool kCodes, bool kWide, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch a, int log) {
+    constexpr int kParts = kCodes ? 2 : 1, kVec = kParts * kRowVec;
     const int lanes = 1 << log, per = kRowThreads >> log;
     const int lid = threadIdx.x & (lanes - 1);
     const int sub = kWide ? __builtin_amdgcn_readfirstlane(threadIdx.x >> log) : threadIdx.x >> log;
-    const int nv = a.cols / kRowVec;
+    const int nv = a.cols / kVec;
     int64_t t_lo = 0, t_hi = a.tokens;
     if (a.offsets) {
         t_lo = max(a.offsets[0], 0);
@@ -68,42 +86,58 @@ __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch
     for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < t_hi; t0 += (int64_t)gridDim.x * per) {
         const int64_t t = t0 + sub;
         const bool tok = t >= t_lo && t < t_hi;
-        // (whole groups of 16 lanes: they share a block's maximum)
-        for (int p = blockIdx.y * lanes + lid; (p & ~15) < nv; p += gridDim.y * lanes) {
+        for (int p = blockIdx.y * lanes + lid; (p & ~7) < nv; p += gridDim.y * lanes) {  // whole blocks
             const bool live = tok && p < nv;
-            intx4 raw = {0, 0, 0, 0};
-            float v[8];
+            const int64_t col = (int64_t)p * kVec;
+            intx4 raw[kParts] = {};
+            float v[kParts][8] = {};  // past the row's end: zeros
             if (live) {
                 if (kCodes && a.xf) {
-                    const floatx4* s = (const floatx4*)(a.xf + t * a.cols + (int64_t)p * kRowVec);
-                    const floatx4 f0 = s[0], f1 = s[1];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = c < 4 ? f0[c] : f1[c - 4];
+                    for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                        for (int c = 0; c < 8; c += 4) {
+                            const floatx4 f = *(const floatx4*)(a.xf + t * a.cols + col + 8 * h + c);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) v[h][c + x] = f[x];
+                        }
                 } else {
-                    raw = *(const intx4*)(a.x + t * a.cols + (int64_t)p * kRowVec);
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h) raw[h] = *(const intx4*)(a.x + t * a.cols + col + 8 * h);
                 }
             }
-            uint64_t q = 0;
+            intx4 q = {0, 0, 0, 0};
             float scale = 0.0f;
             if constexpr (kCodes) {
-                if (!a.xf) unpack_bf16x8(raw, v);
-                float m = live ? abs_max8(v) : 0.0f;  // past the row's end: zeros
+                if (!a.xf) {
 #pragma unroll
-                for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s, kWave));
+                    for (int h = 0; h < kParts; ++h) unpack_bf16x8(raw[h], v[h]);
+                }
+                float m = fmaxf(abs_max8(v[0]), abs_max8(v[kParts - 1]));
+#pragma unroll
+                for (int s = 1; s < 8; s *= 2) m = fmaxf(m, __shfl_xor(m, s, kWave));
                 const int e = blk_exp(m);
                 scale = pow2f(e);
-                q = blk_codes8(v, e);
-                if (a.xf) raw = pack_bf16x8(v);
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) {
+                    const uint64_t c8 = blk_codes8(v[h], e);
+                    q[2 * h] = (int)(uint32_t)c8;
+                    q[2 * h + 1] = (int)(uint32_t)(c8 >> 32);
+                    if (a.xf) raw[h] = pack_bf16x8(v[h]);
+                }
             }
             if (!live) continue;
             for (int j = 0; j < a.k; ++j) {
                 const int32_t* at = a.tok_row + t * a.k + j;
                 const int64_t r = !a.tok_row ? t : kWide ? ld_uniform(at) : *at;
                 if (r < 0 || r >= a.rows) continue;  // no row
-                if (a.dst) *(intx4*)(a.dst + r * a.cols + (int64_t)p * kRowVec) = raw;
+                if (a.dst) {
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h) st_row<kStream>(a.dst + r * a.cols + col + 8 * h, raw[h]);
+                }
                 if constexpr (kCodes) {
-                    *(uint64_t*)(a.codes + r * a.cols + (int64_t)p * kRowVec) = q;
-                    if ((p & 15) == 0) a.scales[(int64_t)(p >> 4) * a.rows + r] = scale;
+                    st_row<kStream>(a.codes + r * a.cols + col, q);
+                    if ((p & 7) == 0) a.scales[(int64_t)(p >> 3) * a.rows + r] = scale;
                 }
             }
         }
@@ -111,18 +145,26 @@ __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch
 }
 
 void launch_rows_dispatch(const RowsDispatch& a, hipStream_t stream) {
-    const int log = row_lanes_log(a.cols), per = kRowThreads >> log;
+    const int vec = a.codes ? 2 * kRowVec : kRowVec;
+    const int log = row_lanes_log(a.cols, vec), per = kRowThreads >> log;
     const int64_t groups = (a.tokens + per - 1) / per;
-    const dim3 grid(row_grid(groups), row_slices(groups, a.cols, log));
-#define ROWS_DISPATCH(CODES, WIDE) \
-    hipLaunchKernelGGL((rows_dispatch_kernel<CODES, WIDE>), grid, dim3(kRowThreads), 0, stream, a, log)
+    const dim3 grid(row_grid(groups), row_slices(groups, a.cols, log, vec));
+    const bool big = streams(a.rows, (int64_t)a.cols * ((a.dst ? 2 : 0) + (a.codes ? 1 : 0)));
+#define ROWS_DISPATCH(CODES, WIDE, STREAM) \
+    hipLaunchKernelGGL((rows_dispatch_kernel<CODES, WIDE, STREAM>), grid, dim3(kRowThreads), 0, stream, a, log)
+#define ROWS_DISPATCH2(CODES, WIDE)                  \
+    do {                                             \
+        if (big) ROWS_DISPATCH(CODES, WIDE, true);   \
+        else ROWS_DISPATCH(CODES, WIDE, false);      \
+    } while (0)
     if (a.codes) {
-        if (log >= 6) ROWS_DISPATCH(true, true);
-        else ROWS_DISPATCH(true, false);
+        if (log >= 6) ROWS_DISPATCH2(true, true);
+        else ROWS_DISPATCH2(true, false);
     } else {
-        if (log >= 6) ROWS_DISPATCH(false, true);
-        else ROWS_DISPATCH(false, false);
+        if (log >= 6) ROWS_DISPATCH2(false, true);
+        else ROWS_DISPATCH2(false, false);
     }
+#undef ROWS_DISPATCH2
 #undef ROWS_DISPATCH
 }
 
@@ -132,7 +174,7 @@ void launch_rows_dispatch(const RowsDispatch& a, hipStream_t stream) {
 
 // The sum over a token's rows in fp32, choice by choice in ascending order, rounded
 // once.  Eight rows' loads are in flight at a time.
-template <bool kWide>
+template <bool kWide, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void rows_combine_kernel(RowsCombine a, int log) {
     const int lanes = 1 << log, per = kRowThreads >> log;
     const int lid = threadIdx.x & (lanes - 1);
@@ -158,7 +200,7 @@ __global__ __launch_bounds__(kRowThreads) void rows_combine_kernel(RowsCombine a
                     }
                     in[j] = r >= 0 && r < a.rows;
                     raw[j] = intx4{0, 0, 0, 0};
-                    if (in[j]) raw[j] = *(const intx4*)(a.src + r * a.cols + col);
+                    if (in[j]) raw[j] = ld_row<kStream>(a.src + r * a.cols + col);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -178,124 +220,147 @@ void launch_rows_combine(const RowsCombine& a, hipStream_t stream) {
     const int log = row_lanes_log(a.cols), per = kRowThreads >> log;
     const int64_t groups = (a.tokens + per - 1) / per;
     const dim3 grid(row_grid(groups), row_slices(groups, a.cols, log));
-    if (log >= 6) hipLaunchKernelGGL(rows_combine_kernel<true>, grid, dim3(kRowThreads), 0, stream, a, log);
-    else hipLaunchKernelGGL(rows_combine_kernel<false>, grid, dim3(kRowThreads), 0, stream, a, log);
+#define ROWS_COMBINE(WIDE, STREAM) \
+    hipLaunchKernelGGL((rows_combine_kernel<WIDE, STREAM>), grid, dim3(kRowThreads), 0, stream, a, log)
+    if (log < 6) ROWS_COMBINE(false, false);
+    else if (streams(a.rows, 2ll * a.cols)) ROWS_COMBINE(true, true);
+    else ROWS_COMBINE(true, false);
+#undef ROWS_COMBINE
 }
 
 // ---------------------------------------------------------------------------
 // Gradient of combine
 // ---------------------------------------------------------------------------
 
-// A token per group of lanes, its slices one after the other: the k dot products
-// stay in registers over them and are joined once, in a fixed order.
-template <int kK, bool kDot>
-__global__ __launch_bounds__(kRowThreads) void rows_combine_bwd_kernel(RowsCombineBwd a, int log, int slices,
-                                                                       int64_t units) {
-    __shared__ float s_dot[kRowThreads / kWave][kK];
-    const int lanes = 1 << log, per = kRowThreads >> log;
-    const int lid = threadIdx.x & (lanes - 1), sub = threadIdx.x >> log;
+// A token per group of 1 << log lanes, its columns in one go or one piece after the other:
+// the k dot products stay in registers over them and are joined once, in a fixed order.
+// kWide: one wave's lanes share a token, and its table's entries are scalars.
+template <int kK, bool kDot, bool kWide, bool kStream, int kThreads>
+__global__ __launch_bounds__(kThreads) void rows_combine_bwd_kernel(RowsCombineBwd a, int log, int64_t units) {
+    __shared__ float s_dot[kThreads / kWave][kK];
+    const int lanes = 1 << log, per = kThreads >> log;
+    const int lid = threadIdx.x & (lanes - 1);
+    const int sub = kWide ? __builtin_amdgcn_readfirstlane(threadIdx.x >> log) : threadIdx.x >> log;
     const int nv = a.cols / kRowVec;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t t = u * per + sub;
         const bool tok = t < a.tokens;
-        int64_t r[kK];
-        float w[kK], dot[kK];
-#pragma unroll
-        for (int j = 0; j < kK; ++j) {
-            r[j] = tok && j < a.k ? (int64_t)a.tok_row[t * a.k + j] : -1;
-            if (r[j] >= a.rows) r[j] = -1;
-            w[j] = tok && j < a.k && a.w ? a.w[t * a.k + j] : 1.0f;
-            dot[j] = 0.0f;
-        }
-        for (int s = 0; s < slices; ++s) {
-            const int p = s * lanes + lid;
-            const bool live = tok && p < nv;
-            const int64_t at = (int64_t)p * kRowVec;
-            float d[8] = {};
-            intx4 raw[kK];
-            if (kDot) {
-#pragma unroll
-                for (int j = 0; j < kK; ++j) {
-                    raw[j] = intx4{0, 0, 0, 0};
-                    if (live && r[j] >= 0) raw[j] = *(const intx4*)(a.src + r[j] * a.cols + at);
-                }
-            }
-            if (live) unpack_bf16x8(*(const intx4*)(a.dout + t * a.cols + at), d);
+        for (int j0 = 0; j0 < a.k; j0 += kK) {  // kK choices at a time
+            int r[kK];
+            float w[kK], dot[kK];
 #pragma unroll
             for (int j = 0; j < kK; ++j) {
-                if (kDot) {
-                    float v[8];
-                    unpack_bf16x8(raw[j], v);
-                    if (r[j] >= 0)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) dot[j] = __builtin_fmaf(v[c], d[c], dot[j]);
+                r[j] = -1;
+                w[j] = 1.0f;
+                if (tok && j0 + j < a.k) {
+                    const int64_t at = t * a.k + j0 + j;
+                    r[j] = kWide ? ld_uniform(a.tok_row + at) : a.tok_row[at];
+                    if (r[j] >= a.rows) r[j] = -1;
+                    if (a.w) w[j] = kWide ? ld_uniform(a.w + at) : a.w[at];
                 }
-                if (!a.dsrc && !a.codes) continue;
-                float g[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) g[c] = w[j] * d[c];
-                const intx4 out = pack_bf16x8(g);
-                const bool put = live && r[j] >= 0;
-                if (a.dsrc && put) *(intx4*)(a.dsrc + r[j] * a.cols + at) = out;
-                if (a.codes) {  // of the rounded gradient, as the quantiser of dsrc gives
-                    unpack_bf16x8(out, g);
-                    float m = put ? abs_max8(g) : 0.0f;
-#pragma unroll
-                    for (int x = 1; x < 16; x *= 2) m = fmaxf(m, __shfl_xor(m, x, kWave));
-                    const int e = blk_exp(m);
-                    if (put) {
-                        *(uint64_t*)(a.codes + r[j] * a.cols + at) = blk_codes8(g, e);
-                        if ((p & 15) == 0) a.scales[(int64_t)(p >> 4) * a.rows + r[j]] = pow2f(e);
-                    }
-                }
+                dot[j] = 0.0f;
             }
-        }
-        if constexpr (kDot) {
-            const int span = lanes < kWave ? lanes : kWave;
-#pragma unroll
-            for (int j = 0; j < kK; ++j)
-                for (int s = span / 2; s >= 1; s >>= 1) dot[j] += __shfl_xor(dot[j], s, kWave);
-            if (lanes > kWave) {  // one or two tokens' waves: joined in ascending order
-                if ((threadIdx.x & 63) == 0)
-#pragma unroll
-                    for (int j = 0; j < kK; ++j) s_dot[threadIdx.x >> 6][j] = dot[j];
-                __syncthreads();
-                if (lid == 0)
+            for (int p = lid; (p & ~15) < nv; p += lanes) {  // whole blocks: their lanes share a maximum
+                const bool live = tok && p < nv;
+                const int64_t col = (int64_t)p * kRowVec;
+                float d[8] = {};
+                intx4 raw[kK];
+                if (kDot) {
 #pragma unroll
                     for (int j = 0; j < kK; ++j) {
-                        const int w0 = threadIdx.x >> 6;
-                        float v = s_dot[w0][j];
-                        for (int x = 1; x < lanes / kWave; ++x) v += s_dot[w0 + x][j];
-                        dot[j] = v;
+                        raw[j] = intx4{0, 0, 0, 0};
+                        if (live && r[j] >= 0) raw[j] = ld_row<kStream>(a.src + (int64_t)r[j] * a.cols + col);
                     }
-                __syncthreads();
-            }
-            if (tok && lid == 0)
+                }
+                if (live) unpack_bf16x8(*(const intx4*)(a.dout + t * a.cols + col), d);
 #pragma unroll
-                for (int j = 0; j < kK; ++j)
-                    if (j < a.k) a.dw[t * a.k + j] = r[j] >= 0 ? dot[j] : 0.0f;
+                for (int j = 0; j < kK; ++j) {
+                    if (kDot) {
+                        float v[8];
+                        unpack_bf16x8(raw[j], v);
+                        if (r[j] >= 0)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) dot[j] = __builtin_fmaf(v[c], d[c], dot[j]);
+                    }
+                    if (!a.dsrc && !a.codes) continue;
+                    float g[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) g[c] = w[j] * d[c];
+                    const intx4 out = pack_bf16x8(g);
+                    const bool put = live && r[j] >= 0;
+                    const int64_t at = (int64_t)r[j] * a.cols + col;
+                    if (a.dsrc && put) st_row<kStream>(a.dsrc + at, out);
+                    if (a.codes) {  // of the rounded gradient, as the quantiser of dsrc gives
+                        unpack_bf16x8(out, g);
+                        float m = put ? abs_max8(g) : 0.0f;
+#pragma unroll
+                        for (int x = 1; x < 16; x *= 2) m = fmaxf(m, __shfl_xor(m, x, kWave));
+                        const int e = blk_exp(m);
+                        if (put) {
+                            *(uint64_t*)(a.codes + at) = blk_codes8(g, e);
+                            if ((p & 15) == 0) a.scales[(int64_t)(p >> 4) * a.rows + r[j]] = pow2f(e);
+                        }
+                    }
+                }
+            }
+            if constexpr (kDot) {
+                const int span = lanes < kWave ? lanes : kWave;
+                for (int s = span / 2; s >= 1; s >>= 1)  // (the k exchanges of a step overlap)
+#pragma unroll
+                    for (int j = 0; j < kK; ++j) dot[j] += __shfl_xor(dot[j], s, kWave);
+                if (lanes > kWave) {  // several waves to a token: joined in ascending order
+                    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                        for (int j = 0; j < kK; ++j) s_dot[threadIdx.x >> 6][j] = dot[j];
+                    __syncthreads();
+                    if (lid < kK && j0 + lid < a.k) {  // a lane to a choice
+                        const int w0 = threadIdx.x >> 6;
+                        float v = s_dot[w0][lid];
+                        for (int x = 1; x < lanes / kWave; ++x) v += s_dot[w0 + x][lid];
+                        if (tok) {
+                            const int64_t at = t * a.k + j0 + lid;
+                            const int rj = a.tok_row[at];
+                            a.dw[at] = rj >= 0 && rj < a.rows ? v : 0.0f;
+                        }
+                    }
+                    __syncthreads();
+                } else if (tok && lid == 0) {
+#pragma unroll
+                    for (int j = 0; j < kK; ++j)
+                        if (j0 + j < a.k) a.dw[t * a.k + j0 + j] = r[j] >= 0 ? dot[j] : 0.0f;
+                }
+            }
         }
     }
 }
 
-void launch_rows_combine_bwd(const RowsCombineBwd& a, hipStream_t stream) {
-    const int log = row_lanes_log(a.cols), per = kRowThreads >> log;
-    const int slices = (a.cols / kRowVec + (1 << log) - 1) >> log;
+template <int kK, bool kWide, bool kStream, int kThreads>
+static void launch_rows_bwd(const RowsCombineBwd& a, int log, hipStream_t stream) {
+    const int per = kThreads >> log;
     const int64_t units = (a.tokens + per - 1) / per;
-#define ROWS_BWD(K)                                                                                             \
-    do {                                                                                                        \
-        if (a.dw)                                                                                               \
-            hipLaunchKernelGGL((rows_combine_bwd_kernel<K, true>), dim3(row_grid(units)), dim3(kRowThreads), 0, \
-                               stream, a, log, slices, units);                                                  \
-        else                                                                                                    \
-            hipLaunchKernelGGL((rows_combine_bwd_kernel<K, false>), dim3(row_grid(units)), dim3(kRowThreads), 0, \
-                               stream, a, log, slices, units);                                                  \
-    } while (0)
-    if (a.k <= 2) ROWS_BWD(2);
-    else if (a.k <= 4) ROWS_BWD(4);
-    else if (a.k <= 8) ROWS_BWD(8);
-    else ROWS_BWD(16);
-#undef ROWS_BWD
+    const dim3 grid(row_grid(units));
+    if (a.dw)
+        hipLaunchKernelGGL((rows_combine_bwd_kernel<kK, true, kWide, kStream, kThreads>), grid, dim3(kThreads), 0, stream, a,
+                           log, units);
+    else
+        hipLaunchKernelGGL((rows_combine_bwd_kernel<kK, false, kWide, kStream, kThreads>), grid, dim3(kThreads), 0, stream,
+                           a, log, units);
+}
+
+template <int kK>
+static void launch_rows_bwd(const RowsCombineBwd& a, hipStream_t stream) {
+    const int log = row_lanes_log(a.cols);
+    // few tokens of wide rows: 1024 threads to a token, which then waits for its rows once
+    if (a.cols > kRowThreads * kRowVec && a.tokens < 1024) launch_rows_bwd<kK, true, false, 1024>(a, 10, stream);
+    else if (log < 6) launch_rows_bwd<kK, false, false, kRowThreads>(a, log, stream);
+    else if (streams(a.rows, 4ll * a.cols)) launch_rows_bwd<kK, true, true, kRowThreads>(a, log, stream);
+    else launch_rows_bwd<kK, true, false, kRowThreads>(a, log, stream);
+}
+
+void launch_rows_combine_bwd(const RowsCombineBwd& a, hipStream_t stream) {
+    if (a.k <= 2) launch_rows_bwd<2>(a, stream);
+    else if (a.k <= 4) launch_rows_bwd<4>(a, stream);
+    else launch_rows_bwd<8>(a, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -327,7 +392,7 @@ __global__ __launch_bounds__(kRowThreads) void block_quant_weights_kernel(const 
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
             intx4 raw = {0, 0, 0, 0};
-            if (r0 + x < rows && c0 < cols) raw = *(const intx4*)(src + (g * rows + r0 + x) * cols + c0);
+            if (r0 + x < rows && c0 < cols) raw = ld_row<true>(src + (g * rows + r0 + x) * cols + c0);
             unpack_bf16x8(raw, v[x]);
             m = fmaxf(m, abs_max8(v[x]));
         }
@@ -356,7 +421,7 @@ __global__ __launch_bounds__(kRowThreads) void block_quant_weights_kernel(const 
             for (int x = threadIdx.x; x < kBlk * 8; x += kRowThreads) {
                 const int row = x >> 3, at = (x & 7) * 16;
                 if (bn * kBlk + row < n && bk * kBlk + at < k)
-                    *(intx4*)(dst + (int64_t)row * k + at) = *(const intx4*)(s_q + row * kBwPitch + at);
+                    st_row<true>(dst + (int64_t)row * k + at, *(const intx4*)(s_q + row * kBwPitch + at));
             }
             __syncthreads();
         }
