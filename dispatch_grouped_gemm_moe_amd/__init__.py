@@ -9,6 +9,7 @@ package fails loudly if the library has not been built
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import dataclasses
 import os
@@ -240,8 +241,9 @@ torch = None  # until a call is given tensors: building, sizing and validating n
 
 def _use_torch():
     """torch, and its tensors' methods as functions: looked up once, not for each of a call's tensors."""
-    global torch, _numel, _is_contiguous, _get_device, _data_ptr
+    global torch, _numel, _is_contiguous, _get_device, _data_ptr, _GRAD_KINDS
     import torch
+    _GRAD_KINDS = {torch.float32: 0, torch.bfloat16: 1}
     _numel, _is_contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
     _get_device, _data_ptr = torch.Tensor.get_device, torch.Tensor.data_ptr
 
@@ -494,23 +496,19 @@ def moe_query_grad_norm(tensors) -> int:
     return n.value
 
 
-def _grad_arrays(fn, dev, grads, like=None):
-    """C arrays of the tensors' pointers, and (without `like`, whose sizes and types they must have) of their
-    element counts and types."""
-    n = len(grads)
-    ptrs = (ctypes.c_void_p * n)()
-    counts, kinds = (ctypes.c_int64 * n)(), (ctypes.c_uint8 * n)()
-    for i, t in enumerate(grads):
-        if t.dtype is torch.bfloat16:
-            kinds[i] = 1
-        elif t.dtype is not torch.float32:
-            raise MoeError(fn, MOE_E_INVALID)
-        if not _is_contiguous(t) or _get_device(t) != dev:
-            raise MoeError(fn, MOE_E_INVALID)
-        if like is not None and (t.dtype is not like[i].dtype or _numel(t) != _numel(like[i])):
-            raise MoeError(fn, MOE_E_INVALID)
-        ptrs[i], counts[i] = _data_ptr(t), _numel(t)
-    return ptrs, counts, kinds
+def _grad_arrays(fn, dev, grads):
+    """Arrays of the tensors' pointers, element counts and types (1: bf16), as the C calls read them."""
+    if not all(_is_contiguous(t) and _get_device(t) == dev for t in grads):
+        raise MoeError(fn, MOE_E_INVALID)
+    try:
+        kinds = bytes([_GRAD_KINDS[t.dtype] for t in grads])
+    except KeyError:
+        raise MoeError(fn, MOE_E_INVALID) from None
+    return array.array("Q", [_data_ptr(t) for t in grads]), array.array("q", [_numel(t) for t in grads]), kinds
+
+
+def _address(a):
+    return a.buffer_info()[0]
 
 
 def moe_grad_norm(grads, norm, ws, stream=None):
@@ -520,7 +518,7 @@ def moe_grad_norm(grads, norm, ws, stream=None):
         _use_torch()
     fn, dev = "moe_grad_norm", norm.get_device()
     ptrs, counts, kinds = _grad_arrays(fn, dev, grads)
-    _call(fn, dev, stream, len(grads), ptrs, counts, kinds, _dense(fn, dev, norm, torch.float32, 1),
+    _call(fn, dev, stream, len(kinds), _address(ptrs), _address(counts), kinds, _dense(fn, dev, norm, torch.float32, 1),
           *_buffer(fn, dev, ws))
 
 
@@ -530,10 +528,13 @@ def moe_clip_grads(grads, norm, max_norm, out=None, stream=None):
         _use_torch()
     fn, dev = "moe_clip_grads", norm.get_device()
     ptrs, counts, kinds = _grad_arrays(fn, dev, grads)
-    if out is not None and len(out) != len(grads):
-        raise MoeError(fn, MOE_E_INVALID)
-    outs = ptrs if out is None else _grad_arrays(fn, dev, out, grads)[0]
-    _call(fn, dev, stream, len(grads), ptrs, counts, kinds, _dense(fn, dev, norm, torch.float32, 1), max_norm, outs)
+    outs = ptrs
+    if out is not None:
+        outs, *like = _grad_arrays(fn, dev, out)
+        if like != [counts, kinds]:  # other sizes or types
+            raise MoeError(fn, MOE_E_INVALID)
+    _call(fn, dev, stream, len(kinds), _address(ptrs), _address(counts), kinds, _dense(fn, dev, norm, torch.float32, 1),
+          max_norm, _address(outs))
 
 
 def moe_diag_mfma_loop(kind, operands, blocks, iters, clocks, sink, stream=None):
