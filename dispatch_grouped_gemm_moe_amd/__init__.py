@@ -357,6 +357,14 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _row_scales(fn, device, t, rows, cols):
+    """The pointer of the scales [ceil(cols / 128), rows] of rows in blocks of 128.  A matrix of more columns
+    would be read in another order: refused."""
+    if t is not None and t.dim() > 1 and t.shape[-1] != rows:
+        raise MoeError(fn, MOE_E_INVALID)
+    return _dense(fn, device, t, torch.float32, _blocks(cols) * rows)
+
+
 def moe_dispatch_rows(x, tok_row, dst=None, codes=None, scales=None, stream=None):
     """Row tok_row[t, j] = x[t] for each of the k choices j: of dst (bf16), and / or of codes and scales
     (moe_block_quantize's); rows outside theirs are no rows."""
@@ -365,10 +373,12 @@ def moe_dispatch_rows(x, tok_row, dst=None, codes=None, scales=None, stream=None
     fn, dev, b16, f32, u8 = "moe_dispatch_rows", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
     T, cols = _sizes(fn, *x.shape)
     k = tok_row.shape[1]
-    R = (codes if dst is None else dst).shape[0] if dst is not None or codes is not None else 0
+    R = dst.shape[0] if dst is not None else codes.shape[0] if codes is not None else 0
+    if codes is not None and codes.shape[0] != R:
+        raise MoeError(fn, MOE_E_INVALID)
     _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, x, b16, 0), _dense(fn, dev, tok_row, torch.int32, T * k),
           _dense(fn, dev, dst, b16, R * cols), _dense(fn, dev, codes, u8, R * cols),
-          _dense(fn, dev, scales, f32, _blocks(cols) * R))
+          _row_scales(fn, dev, scales, R, cols))
 
 
 def moe_combine_rows(src, tok_row, out, topk_w=None, add=None, stream=None):
@@ -392,12 +402,14 @@ def moe_combine_rows_bwd(dout, tok_row, src=None, topk_w=None, dsrc=None, dw=Non
     fn, dev, b16, f32, u8 = "moe_combine_rows_bwd", dout.get_device(), torch.bfloat16, torch.float32, torch.uint8
     T, cols = _sizes(fn, *dout.shape)
     k = tok_row.shape[1]
-    rows = [t.shape[0] for t in (src, dsrc, codes) if t is not None]
-    R = min(rows) if rows else 0
+    rows = {t.shape[0] for t in (src, dsrc, codes) if t is not None}
+    if len(rows) > 1:
+        raise MoeError(fn, MOE_E_INVALID)
+    R = rows.pop() if rows else 0
     _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, dout, b16, 0), _dense(fn, dev, src, b16, R * cols),
           _dense(fn, dev, tok_row, torch.int32, T * k), _dense(fn, dev, topk_w, f32, T * k),
           _dense(fn, dev, dsrc, b16, R * cols), _dense(fn, dev, codes, u8, R * cols),
-          _dense(fn, dev, scales, f32, _blocks(cols) * R), _dense(fn, dev, dw, f32, T * k))
+          _row_scales(fn, dev, scales, R, cols), _dense(fn, dev, dw, f32, T * k))
 
 
 def moe_block_quantize(src, codes, scales, stream=None):
@@ -407,8 +419,7 @@ def moe_block_quantize(src, codes, scales, stream=None):
     fn, dev = "moe_block_quantize", src.get_device()
     rows, cols = _sizes(fn, *src.shape)
     _call(fn, dev, stream, rows, cols, _dense(fn, dev, src, torch.bfloat16, 0),
-          _dense(fn, dev, codes, torch.uint8, rows * cols),
-          _dense(fn, dev, scales, torch.float32, _blocks(cols) * rows))
+          _dense(fn, dev, codes, torch.uint8, rows * cols), _row_scales(fn, dev, scales, rows, cols))
 
 
 def moe_block_quantize_weights(src, codes, scales, transposed=False, stream=None):
@@ -432,11 +443,12 @@ def moe_block_dequantize(codes, scales, dst, weights=False, stream=None):
     fn, dev = "moe_block_dequantize", codes.get_device()
     n = codes.shape[-2] if weights else 0
     rows, cols = _sizes(fn, codes.shape[0] * n if weights else codes.shape[0], codes.shape[-1])
-    n_scales = codes.shape[0] * _blocks(n) * _blocks(cols) if weights else _blocks(cols) * rows
     if n >= 1 << 31:
         raise MoeError(fn, MOE_E_UNSUPPORTED)
-    _call(fn, dev, stream, rows, cols, n, _dense(fn, dev, codes, torch.uint8, rows * cols),
-          _dense(fn, dev, scales, torch.float32, n_scales), _dense(fn, dev, dst, torch.bfloat16, rows * cols))
+    s = _dense(fn, dev, scales, torch.float32, codes.shape[0] * _blocks(n) * _blocks(cols)) if weights else \
+        _row_scales(fn, dev, scales, rows, cols)
+    _call(fn, dev, stream, rows, cols, n, _dense(fn, dev, codes, torch.uint8, rows * cols), s,
+          _dense(fn, dev, dst, torch.bfloat16, rows * cols))
 
 
 def _block_operands(fn, dev, a, a_scales, offsets, w):
@@ -448,7 +460,7 @@ def _block_operands(fn, dev, a, a_scales, offsets, w):
     if max(groups, n) >= 1 << 31:
         raise MoeError(fn, MOE_E_UNSUPPORTED)
     return (rows, n, k, groups), (_dense(fn, dev, a, torch.uint8, 0),
-                                  _dense(fn, dev, a_scales, torch.float32, _blocks(k) * rows),
+                                  _row_scales(fn, dev, a_scales, rows, k),
                                   _dense(fn, dev, offsets, torch.int32, groups + 1))
 
 
@@ -480,10 +492,12 @@ def moe_block_gemm_swiglu(a, a_scales, wg, wg_scales, wu, wu_scales, h_codes, h_
         _use_torch()
     fn, dev, f32, u8 = "moe_block_gemm_swiglu", a.get_device(), torch.float32, torch.uint8
     (rows, n, k, groups), ptrs = _block_operands(fn, dev, a, a_scales, offsets, wg)
-    n_w, n_s = groups * n * k, groups * _blocks(n) * _blocks(k)
+    if wu.shape != wg.shape:
+        raise MoeError(fn, MOE_E_INVALID)
+    n_s = groups * _blocks(n) * _blocks(k)
     _call(fn, dev, stream, rows, n, k, groups, *ptrs, _dense(fn, dev, wg, u8, 0), _dense(fn, dev, wg_scales, f32, n_s),
-          _dense(fn, dev, wu, u8, n_w), _dense(fn, dev, wu_scales, f32, n_s), _dense(fn, dev, h_codes, u8, rows * n),
-          _dense(fn, dev, h_scales, f32, _blocks(n) * rows), _dense(fn, dev, h, torch.bfloat16, rows * n),
+          _dense(fn, dev, wu, u8, 0), _dense(fn, dev, wu_scales, f32, n_s), _dense(fn, dev, h_codes, u8, rows * n),
+          _row_scales(fn, dev, h_scales, rows, n), _dense(fn, dev, h, torch.bfloat16, rows * n),
           *_buffer(fn, dev, ws))
 
 

@@ -103,7 +103,7 @@ def test_binding_refuses_tensors_the_kernels_cannot_read():
     w, sw = torch.zeros(2, 32, 64, dtype=u8), torch.zeros(2, 1, 1)
     off, out = torch.zeros(3, dtype=torch.int32), torch.zeros(4, 32, dtype=b16)
     good = dict(a=a, a_scales=sa, w=w, w_scales=sw, out=out, offsets=off, stream=0)
-    bad = (dict(), dict(a=a.view(torch.int8)), dict(a_scales=sa[:, :3]), dict(w=w[:, :, :32]), dict(w_scales=sw[:1]),
+    bad = (dict(), dict(a=a.view(torch.int8)), dict(a_scales=sa[:, :3]), dict(a_scales=torch.zeros(1, 5)), dict(w=w[:, :, :32]), dict(w_scales=sw[:1]),
            dict(out=out[:3]), dict(out=out.float()), dict(offsets=off[:2]), dict(offsets=off.long()), dict(w=w.to("meta")))
     for kw in bad:
         with pytest.raises(moe.MoeError) as e:  # (the first: host tensors)
@@ -111,7 +111,7 @@ def test_binding_refuses_tensors_the_kernels_cannot_read():
         assert e.value.status == moe.MOE_E_INVALID
     good = dict(a=a, a_scales=sa, wg=w, wg_scales=sw, wu=w, wu_scales=sw, h_codes=torch.zeros(4, 32, dtype=u8),
                 h_scales=torch.zeros(1, 4), ws=torch.zeros(4096, dtype=u8), offsets=off, stream=0)
-    for kw in (dict(), dict(wu=w[:1]), dict(wu_scales=sw[:1]), dict(h=out[:3]), dict(h_scales=torch.zeros(1, 3)),
+    for kw in (dict(), dict(wu=w[:1]), dict(wu=w.reshape(2, 64, 32)), dict(wu_scales=sw[:1]), dict(a_scales=torch.zeros(1, 5)), dict(h=out[:3]), dict(h_scales=torch.zeros(1, 3)),
                dict(h_codes=torch.zeros(3, 32, dtype=u8))):
         with pytest.raises(moe.MoeError) as e:
             moe.moe_block_gemm_swiglu(**{**good, **kw})
@@ -261,7 +261,7 @@ def _values(a, sa, w, sw):
 
 def _product(av, wv, offsets):
     """In 64 bits: the product by group, and the sum of its terms' magnitudes; NaN where there is no group."""
-    out = torch.full((av.shape[0], wv.shape[1]), float("nan"), dtype=torch.float64)
+    out = torch.full((av.shape[0], wv.shape[1]), float("nan"), dtype=torch.float64, device=av.device)
     size = torch.zeros_like(out)
     for e in range(wv.shape[0]):
         lo, hi = offsets[e].item(), offsets[e + 1].item()
@@ -278,16 +278,38 @@ PRODUCTS = [([1], 8, 16), ([1], 64, 128), ([3], 264, 144), ([1, 0, 2], 136, 272)
             ([1024], 512, 128), ([40, 600], 776, 2576)]
 
 
+def _uneven(rows, groups):
+    """Counts that differ from group to group, some zero, some of whole tiles."""
+    part = [(7 * i + 3) % 11 if i % 5 else 0 for i in range(groups)]
+    counts = [rows * x // max(1, sum(part)) for x in part]
+    counts[1 % groups] += -counts[1 % groups] % 256 if rows > 2000 else 0
+    return counts
+
+
+# rows, groups, n, k that fall to each of the forms in which the products are computed: tiles of 256 x 256,
+# 128 x 256, 128 x 128, 64 x 256 and the few-row form, the first row past the tables of the tiles' groups
+TILED = [(4100, 40, 1032, 144), (4100, 40, 1032, 400), (4100, 40, 1032, 656), (6100, 3, 2056, 272), (4129, 1, 4104, 272),
+         (1500, 40, 1032, 144), (7000, 40, 264, 272), (2300, 40, 1032, 656), (2049, 1, 2056, 528), (100, 3, 6152, 400),
+         (2300, 40, 264, 656), (1024, 1, 1032, 1040), (100, 40, 1032, 1040), (100, 40, 4104, 272), (300, 40, 1032, 400),
+         (1300, 600, 136, 272)]
+TILED_GLU = [(4100, 40, 528, 144), (4100, 40, 528, 400), (4100, 40, 528, 656), (4129, 1, 2064, 272), (1500, 40, 528, 144),
+             (7000, 40, 144, 272), (7000, 40, 144, 656), (100, 40, 1552, 272), (100, 40, 528, 528), (700, 3, 1040, 656),
+             (1300, 600, 144, 272)]
+SHAPES = PRODUCTS + [(_uneven(r, e), n, k) for r, e, n, k in TILED]
+SHAPES_GLU = [(c, (n + 15) // 16 * 16, k) for c, n, k in PRODUCTS] + [(_uneven(r, e), n, k) for r, e, n, k in TILED_GLU]
+_name = lambda v: "x".join(map(str, [len(v), sum(v)])) if isinstance(v, list) else str(v)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("whole", [True, False])
-@pytest.mark.parametrize("counts,n,k", PRODUCTS)
+@pytest.mark.parametrize("counts,n,k", SHAPES, ids=_name)
 def test_product(gpu_lib, counts, n, k, whole):
     g = torch.Generator().manual_seed(sum(counts) + n + k)
     spare = 3  # rows of no group, left as they were
     rows, groups = sum(counts) + spare, len(counts)
     a, sa, w, sw = _operands(g, rows, k, groups, n, whole)
     off = _offsets(counts)
-    want, size = _product(*_values(a, sa, w, sw), off)
+    want, size = (t.cpu() for t in _product(*_values(a.cuda(), sa.cuda(), w.cuda(), sw.cuda()), off))
     outs = []
     for _ in range(2):
         out = torch.full((rows + 1, n), 77, dtype=torch.bfloat16, device="cuda")
@@ -320,7 +342,7 @@ def test_product_of_one_group_needs_no_offsets(gpu_lib, rows, n, k):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("counts,n,k", [(c, (n + 15) // 16 * 16, k) for c, n, k in PRODUCTS])
+@pytest.mark.parametrize("counts,n,k", SHAPES_GLU, ids=_name)
 def test_swiglu_product(gpu_lib, counts, n, k):
     g = torch.Generator().manual_seed(sum(counts) + n + k + 1)
     spare = 2
@@ -330,9 +352,9 @@ def test_swiglu_product(gpu_lib, counts, n, k):
     # gate products of a size that silu bends
     sg, su = sg / (1e4 * k ** 0.5), su / (1e4 * k ** 0.5)
     off = _offsets(counts)
-    av, wgv = _values(a, sa, wg, sg)
-    gate, gsize = _product(av, wgv, off)
-    up, usize = _product(av, _values(a, sa, wu, su)[1], off)
+    av, wgv = _values(*(t.cuda() for t in (a, sa, wg, sg)))
+    gate, gsize = (t.cpu() for t in _product(av, wgv, off))
+    up, usize = (t.cpu() for t in _product(av, _values(*(t.cuda() for t in (a, sa, wu, su)))[1], off))
     h = gate * torch.sigmoid(gate) * up
     nb = (n + 127) // 128
     ws = torch.full((moe.moe_query_block_swiglu(rows, n, k, groups),), 0xff, dtype=torch.uint8, device="cuda")

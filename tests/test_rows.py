@@ -74,7 +74,10 @@ def test_binding_refuses_tensors_the_kernels_cannot_read():
     good = dict(x=x, tok_row=at, dst=rows, stream=0)
     for kw in (dict(), dict(x=x.float()), dict(x=torch.zeros(64, 4, dtype=b16).t()), dict(tok_row=at.long()),
                dict(tok_row=at[:3]), dict(dst=None), dict(codes=torch.zeros(7, 64, dtype=torch.uint8)),
-               dict(codes=torch.zeros(8, 64, dtype=torch.uint8), scales=torch.zeros(7)), dict(dst=rows.to("meta"))):
+               dict(codes=torch.zeros(8, 64, dtype=torch.uint8), scales=torch.zeros(7)), dict(dst=rows.to("meta")),
+               # another number of rows would be another layout of the scales
+               dict(codes=torch.zeros(9, 64, dtype=torch.uint8), scales=torch.zeros(1, 9)),
+               dict(codes=torch.zeros(8, 64, dtype=torch.uint8), scales=torch.zeros(1, 9))):
         with pytest.raises(moe.MoeError) as e:  # (the first: host tensors)
             moe.moe_dispatch_rows(**{**good, **kw})
         assert e.value.status == moe.MOE_E_INVALID
