@@ -461,36 +461,40 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     const uint32_t v_odd = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_odd * 16;
     const uint32_t v_eight = 8u * (uint32_t)p.k;
     BgSource src, nxt;
-    // Stage s of this tile, or past its last the next tile's; past the last tile's last
-    // nothing is read and the slot, which no wave reads any more, is filled with zeros.
-    auto issue = [&](int s_, int slot) {
+    // The A or the B half (with the scales) of stage s of this tile, or past its last of the
+    // next tile's; past the last tile's last nothing is read and the slot, which no wave reads
+    // any more, is filled with zeros.
+    auto issue = [&](auto half_a, int s_, int slot) {
+        constexpr bool kA = decltype(half_a)::value;
+        constexpr int kRows = kA ? kRowsA : kRowsB;
         const bool beyond = s_ >= KB;
         const BgSource q = beyond ? nxt : src;
         const int s = beyond ? s_ - KB : s_;
         const int left = q.a ? p.k - s * kBlk : 0;  // bytes of a row from this stage on
         uint8_t* st = smem + slot * C::kStage;
-        const __amdgpu_buffer_rsrc_t ra = blk_rsrc(q.a, q.a_bytes), rb = blk_rsrc(q.b, q.b_bytes);
+        const __amdgpu_buffer_rsrc_t r = kA ? blk_rsrc(q.a, q.a_bytes) : blk_rsrc(q.b, q.b_bytes);
         const bool in_e = c_even * 16 < left, in_o = c_odd * 16 < left;
 #pragma unroll
-        for (int i = 0; i < (kRowsA > kRowsB ? kRowsA : kRowsB) / 8; ++i) {
+        for (int i = 0; i < kRows / 8; ++i) {
             // (fewer than sixteen rows to a wave: the wave's own place tells which)
-            auto at = [&](int rows) {
-                const bool odd = rows >= 16 ? (i & 1) : (wave & 1);
-                const uint32_t v = (odd ? v_odd : v_even) + i * v_eight + s * kBlk;
-                return (odd ? in_o : in_e) ? v : kNowhere;
-            };
-            if (i < kRowsA / 8)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + wave * kRowsA * kBlk + i * 1024), 16,
-                                                         at(kRowsA), 0, 0, 0);
-            if (i < kRowsB / 8)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rb, (lds_void*)(st + C::kStageB + wave * kRowsB * kBlk + i * 1024), 16, at(kRowsB), 0, 0, 0);
+            const bool odd = kRows >= 16 ? (i & 1) : (wave & 1);
+            const uint32_t v = (odd ? v_odd : v_even) + i * v_eight + s * kBlk;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (lds_void*)(st + (kA ? 0 : C::kStageB) + wave * kRows * kBlk + i * 1024), 16,
+                (odd ? in_o : in_e) ? v : kNowhere, 0, 0, 0);
         }
         // (a wave without scales fills its area with zeros: a branch here would let the
         // compiler move every addition of the stage past it)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(blk_rsrc(q.s + s * s_step, left > 0 ? q.s_bytes : 0),
-                                                 (lds_void*)(st + C::kStageS + wave * 256), 4, lane * 4, 0, 0, 0);
+        if (!kA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(blk_rsrc(q.s + s * s_step, left > 0 ? q.s_bytes : 0),
+                                                     (lds_void*)(st + C::kStageS + wave * 256), 4, lane * 4, 0, 0, 0);
     };
+    constexpr std::integral_constant<bool, true> kHalfA{};
+    constexpr std::integral_constant<bool, false> kHalfB{};
+    // With two slots, A's half of a slot is loaded again half a stage before B's: its
+    // fragments are in registers before the stage begins.
+    constexpr bool kEarlyA = C::kS == 2;
+    static_assert(!kEarlyA || kFJ >= 4, "the A half's barrier is not the stage's");
 
     const int fr = lane & 31, half = lane >> 5;
     const int fsw = swz8(fr);  // a fragment's rows differ from fr by multiples of 32
@@ -548,7 +552,10 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     nxt = source_of(next);
     // (KB is at least kS, so a tile's loads reach no further than the next tile)
 #pragma unroll
-    for (int s = 0; s < C::kS; ++s) issue(s, s);
+    for (int s = 0; s < C::kS; ++s) {
+        issue(kHalfA, s, s);
+        issue(kHalfB, s, s);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     int slot = 0;
@@ -569,12 +576,22 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                 const int i = f % kFI, j = f / kFI;
                 pin();
                 if (i == 0 && j < kFJ - 1) read_frag(slot, brow + (j + 1) * 32 * kBlk, fb[(j + 1) & 1]);
-                if (i == 0 && j == kFJ - 1) {
-                    // stage s + 1 has landed, and no wave reads stage s any more
-                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((C::kS - 2) * C::kLoads) : "memory");
+                if (kEarlyA && i == 0 && j == kFJ / 2) {
+                    // every wave has multiplied its A fragments of stage s: they have left LDS
+                    asm volatile("" ::: "memory");
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
-                    issue(s + C::kS, slot);
+                    issue(kHalfA, s + C::kS, slot);
+                    pin();
+                }
+                if (i == 0 && j == kFJ - 1) {
+                    // stage s + 1 has landed, and no wave reads stage s any more
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kEarlyA ? kRowsA / 8 : (C::kS - 2) * C::kLoads)
+                                 : "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    if (!kEarlyA) issue(kHalfA, s + C::kS, slot);
+                    issue(kHalfB, s + C::kS, slot);
                     slot = slot == C::kS - 1 ? 0 : slot + 1;
                     pin();
                     read_frag(slot, brow, fb[(j + 1) & 1]);
