@@ -307,6 +307,7 @@ __global__ __launch_bounds__(kBfWaves * kWave, 2) void block_few_kernel(BlockGem
 constexpr int kBgThreads = 512;
 constexpr int kBgGroups = 512;  // groups whose tables fit beside the ring
 constexpr int kBgStg = 2048;    // a wave's staged output
+constexpr int kBgPatch = 8;     // M tiles of a patch
 template <int kWM_, int kWN_, int kFI_, int kFJ_, int kS_>
 struct BgShape {
     static constexpr int kWM = kWM_, kWN = kWN_, kFI = kFI_, kFJ = kFJ_, kS = kS_;
@@ -403,8 +404,10 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         if (lane == 0) s_first[p.groups] = before;
     }
     __syncthreads();
-    // Workgroup b runs on XCD b % 8, whose workgroups take neighbouring tiles: group by
-    // group, column by column, M tiles fastest, so that they share panels in its L2.
+    // Workgroup b runs on XCD b % 8, whose workgroups take neighbouring tiles, so that they
+    // share panels in its L2: group by group, kBgPatch M tiles by all columns after the other,
+    // M fastest.  32 workgroups then read 8 row and 4 column panels; with all of a group's M
+    // tiles first, 16384 x [8192, 8192] took 925 us instead of 862.
     const int total = __builtin_amdgcn_readfirstlane(s_first[p.groups]) * NT;
     const int xcd = blockIdx.x & 7, per = (total + 7) / 8, step = gridDim.x >> 3;
     const int t_end = min((xcd + 1) * per, total);
@@ -420,9 +423,10 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         }
         r.g = e;
         const int f0 = __builtin_amdgcn_readfirstlane(s_first[e]), f1 = __builtin_amdgcn_readfirstlane(s_first[e + 1]);
-        const int in = t - f0 * NT, col = in / (f1 - f0);
+        const int in = t - f0 * NT, block = in / (kBgPatch * NT), rest = in - block * kBgPatch * NT;
+        const int high = min(kBgPatch, f1 - f0 - block * kBgPatch), col = rest / high;
         r.n0 = col * kCols;
-        r.row0 = __builtin_amdgcn_readfirstlane(s_lo[e]) + (in - col * (f1 - f0)) * C::kM;
+        r.row0 = __builtin_amdgcn_readfirstlane(s_lo[e]) + (block * kBgPatch + rest - col * high) * C::kM;
         r.count = min(__builtin_amdgcn_readfirstlane(s_hi[e]) - r.row0, C::kM);
         return r;
     };
@@ -461,12 +465,12 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     const uint32_t v_odd = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_odd * 16;
     const uint32_t v_eight = 8u * (uint32_t)p.k;
     BgSource src, nxt;
-    // The A or the B half (with the scales) of stage s of this tile, or past its last of the
-    // next tile's; past the last tile's last nothing is read and the slot, which no wave reads
-    // any more, is filled with zeros.
-    auto issue = [&](auto half_a, int s_, int slot) {
+    // Part x of kParts of the A or the B half (with the scales) of stage s of this tile, or past
+    // its last of the next tile's; past the last tile's last nothing is read and the slot, which
+    // no wave reads any more, is filled with zeros.
+    auto issue = [&](auto half_a, auto part, auto parts, int s_, int slot) {
         constexpr bool kA = decltype(half_a)::value;
-        constexpr int kRows = kA ? kRowsA : kRowsB;
+        constexpr int kRows = kA ? kRowsA : kRowsB, kPart = decltype(part)::value, kParts = decltype(parts)::value;
         const bool beyond = s_ >= KB;
         const BgSource q = beyond ? nxt : src;
         const int s = beyond ? s_ - KB : s_;
@@ -475,7 +479,7 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         const __amdgpu_buffer_rsrc_t r = kA ? blk_rsrc(q.a, q.a_bytes) : blk_rsrc(q.b, q.b_bytes);
         const bool in_e = c_even * 16 < left, in_o = c_odd * 16 < left;
 #pragma unroll
-        for (int i = 0; i < kRows / 8; ++i) {
+        for (int i = kRows / 8 * kPart / kParts; i < kRows / 8 * (kPart + 1) / kParts; ++i) {
             // (fewer than sixteen rows to a wave: the wave's own place tells which)
             const bool odd = kRows >= 16 ? (i & 1) : (wave & 1);
             const uint32_t v = (odd ? v_odd : v_even) + i * v_eight + s * kBlk;
@@ -485,12 +489,15 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         }
         // (a wave without scales fills its area with zeros: a branch here would let the
         // compiler move every addition of the stage past it)
-        if (!kA)
+        if (!kA && kPart == 0)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(blk_rsrc(q.s + s * s_step, left > 0 ? q.s_bytes : 0),
                                                      (lds_void*)(st + C::kStageS + wave * 256), 4, lane * 4, 0, 0, 0);
     };
     constexpr std::integral_constant<bool, true> kHalfA{};
     constexpr std::integral_constant<bool, false> kHalfB{};
+    constexpr std::integral_constant<int, 0> k0{};
+    constexpr std::integral_constant<int, 1> k1{};
+    constexpr std::integral_constant<int, 2> k2{};
     // With two slots, A's half of a slot is loaded again half a stage before B's: its
     // fragments are in registers before the stage begins.
     constexpr bool kEarlyA = C::kS == 2;
@@ -553,12 +560,12 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     // (KB is at least kS, so a tile's loads reach no further than the next tile)
 #pragma unroll
     for (int s = 0; s < C::kS; ++s) {
-        issue(kHalfA, s, s);
-        issue(kHalfB, s, s);
+        issue(kHalfA, k0, k1, s, s);
+        issue(kHalfB, k0, k1, s, s);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    int slot = 0;
+    int slot = 0, freed = 0;
 #pragma unroll
     for (int i = 0; i < kFI; ++i) read_frag(0, arow + i * kWM * 32 * kBlk, fa[i]);
     read_frag(0, brow, fb[0]);
@@ -581,8 +588,6 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                     asm volatile("" ::: "memory");
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
-                    issue(kHalfA, s + C::kS, slot);
-                    pin();
                 }
                 if (i == 0 && j == kFJ - 1) {
                     // stage s + 1 has landed, and no wave reads stage s any more
@@ -590,14 +595,25 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                                  : "memory");
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
-                    if (!kEarlyA) issue(kHalfA, s + C::kS, slot);
-                    issue(kHalfB, s + C::kS, slot);
+                    if (!kEarlyA) issue(kHalfA, k0, k1, s + C::kS, slot);
+                    freed = slot;
                     slot = slot == C::kS - 1 ? 0 : slot + 1;
-                    pin();
                     read_frag(slot, brow, fb[(j + 1) & 1]);
                     read_scales(slot);
                 }
                 multiply(f);
+                // Loads go out a few at a time under the products: all of a stage's at once, and the
+                // waves wait for the address unit to take them (264 -> 252 us for 16384 x [4096, 4096]).
+                if (kEarlyA && j == kFJ / 2) {
+                    if (kFI == 1) issue(kHalfA, k0, k1, s + C::kS, slot);
+                    else if (i == 0) issue(kHalfA, k0, k2, s + C::kS, slot);
+                    else issue(kHalfA, k1, k2, s + C::kS, slot);
+                }
+                if (j == kFJ - 1) {
+                    if (kFI == 1) issue(kHalfB, k0, k1, s + C::kS, freed);
+                    else if (i == 0) issue(kHalfB, k0, k2, s + C::kS, freed);
+                    else issue(kHalfB, k1, k2, s + C::kS, freed);
+                }
                 if (f == 0) {
                     add(kF - 1);  // of the stage before
 #pragma unroll
