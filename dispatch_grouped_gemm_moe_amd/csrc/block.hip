@@ -765,14 +765,15 @@ enum BlockForm { kFormFew, kForm256x256, kForm128x256, kForm128x128, kForm64x256
 
 // The form with the least expected time, in us.  A tile takes a block of K in `low` us
 // where it is one of few and in `full` us where every CU has one, and `end` us for its
-// epilogue (fitted to products of [4096, 4096] with 256 to 4096 rows and of 32 x [7168,
-// 2048] with 1024 to 131072); tiles run in rounds of one to a CU.  Larger tiles need
-// less of everything for each element, smaller ones fill the CUs sooner and pad a
-// group's rows less.  Measured, us, tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 256 and
-// the few-row form: 1 row x [2048, 1024] -, -, 8.2, 9.2, 3.7; 64 x [4096, 4096] -, -,
-// 21, 26, 13; 256: 54, 35, 23, 27, 39; 2048: 57, 43, 52, 58, 268; 4096: 68, 86, 103, 104,
-// 531; 32 groups of [7168, 2048]: 64 rows -, -, 80, 75, 79; 1024: 121, 105, 99, 93, 116;
-// 8192: 202, 212, 220, 227, 957; 131072: 2107, 2573, 2821, 2984, 14243.
+// epilogue (fitted to products of [4096, 4096] and [4096, 1024] with 256 to 16384 rows);
+// tiles run in rounds of one to a CU.  Larger tiles need less of everything for each
+// element, smaller ones fill the CUs sooner and pad a group's rows less.  Measured, us,
+// tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 256 and the few-row form (-: not timed):
+//   1 row x [2048, 1024]       -, -, 8.2, 9.2, 3.7;   64 rows x [4096, 4096]  -, -, 21, 26, 12
+//   256 rows x [4096, 4096]    43, 31, 22, 27, 39;    2048 rows               48, 40, 48, 56, 268
+//   4096 rows                  61, 78, 91, 104, 531;  16384 rows              234, 299, 344, 394, -
+//   32 groups of [7168, 2048]  64 rows 88, 77, 76, 72, 76;  1024 rows 112, 103, 100, 96, 116
+//   8192 rows                  186, 196, 216, 226, 957;     131072 rows 1819, 2272, 2574, 2912, 14243
 static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
     const double r = (double)rows, kb = blk_count(k);
     const double active = std::min(r, groups * (1.0 - exp(-r / groups)));  // groups with rows, routed evenly
@@ -786,13 +787,13 @@ static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
                              std::max(1.0, strips);
     if (groups > kBgGroups) return best;
     const struct { BlockForm form; int m, n, stages; double low, full, end; } tiles[] = {
-        {kForm256x256, 256, 256, Bg256x256::kS, 1.55, 2.3, 4}, {kForm128x256, 128, 256, Bg128x256::kS, 1.0, 1.41, 3},
-        {kForm128x128, 128, 128, Bg128x128::kS, 0.62, 0.78, 2}, {kForm64x256, 64, 256, Bg64x256::kS, 0.72, 0.83, 2}};
+        {kForm256x256, 256, 256, Bg256x256::kS, 1.155, 1.66, 4.2}, {kForm128x256, 128, 256, Bg128x256::kS, 0.81, 1.08, 2.6},
+        {kForm128x128, 128, 128, Bg128x128::kS, 0.564, 0.62, 1.5}, {kForm64x256, 64, 256, Bg64x256::kS, 0.703, 0.72, 1.5}};
     for (const auto& t : tiles) {
         if (kb < t.stages || (glu && t.n != 256)) continue;  // a block of h is half of 256 columns
         const int cols = glu ? t.n / 2 : t.n;
         const double rounds = parts(t.m) * ((n + cols - 1) / cols) / 256;
-        const double us = 4 + (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds) *
+        const double us = 2.5 + (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds) *
                                   (kb * (rounds <= 1 ? t.low : t.full) + t.end);
         if (us < least) {
             least = us;
