@@ -291,10 +291,11 @@ def _uneven(rows, groups):
 TILED = [(4100, 40, 1032, 144), (4100, 40, 1032, 400), (4100, 40, 1032, 656), (6100, 3, 2056, 272), (4129, 1, 4104, 272),
          (1500, 40, 1032, 144), (7000, 40, 264, 272), (2300, 40, 1032, 656), (2049, 1, 2056, 528), (100, 3, 6152, 400),
          (2300, 40, 264, 656), (1024, 1, 1032, 1040), (100, 40, 1032, 1040), (100, 40, 4104, 272), (300, 40, 1032, 400),
-         (9000, 3, 2056, 144), (8200, 1, 2056, 400), (9100, 40, 1032, 656), (12000, 5, 1544, 1040), (1300, 600, 136, 272)]
+         (9000, 3, 2056, 144), (12000, 3, 4104, 272), (16400, 40, 2056, 144), (30000, 40, 1032, 656),
+         (1300, 600, 136, 272)]
 TILED_GLU = [(4100, 40, 528, 144), (4100, 40, 528, 400), (4100, 40, 528, 656), (4129, 1, 2064, 272), (1500, 40, 528, 144),
              (7000, 40, 144, 272), (7000, 40, 144, 656), (100, 40, 1552, 272), (100, 40, 528, 528), (700, 3, 1040, 656),
-             (9000, 3, 1040, 144), (8200, 1, 1040, 400), (12000, 5, 784, 1040), (1300, 600, 144, 272)]
+             (12000, 3, 2064, 272), (16400, 40, 1040, 144), (30000, 40, 528, 656), (1300, 600, 144, 272)]
 SHAPES = PRODUCTS + [(_uneven(r, e), n, k) for r, e, n, k in TILED]
 SHAPES_GLU = [(c, (n + 15) // 16 * 16, k) for c, n, k in PRODUCTS] + [(_uneven(r, e), n, k) for r, e, n, k in TILED_GLU]
 _name = lambda v: "x".join(map(str, [len(v), sum(v)])) if isinstance(v, list) else str(v)
