@@ -448,9 +448,11 @@ moe_status moe_query_few(const moe_cfg *cfg, size_t *workspace);
  *   dout bf16 [tokens, cols]; src, tok_row, w as above (src may be NULL without
  *   dw); dsrc bf16 [rows, cols], or NULL; codes, scales of the rounded dsrc as
  *   moe_block_quantize holds it, both or neither; dw fp32 [tokens, k], or NULL (0
- *   for a choice without a row).  The gradient of add is dout.
+ *   for a choice without a row).  dsrc may be src itself.  The gradient of add is
+ *   dout.
  *
- * Rows that the table does not name are left as they were.  All pointers 16-byte
+ * Rows that the table does not name are left as they were.  Buffers overlap in no
+ * other way.  All pointers 16-byte
  * aligned (tok_row, w, dw and scales 4).  MOE_E_INVALID for null or misaligned
  * pointers, no output, tokens, k or rows < 1, cols not a positive multiple of 8
  * (of 16 with codes); MOE_E_UNSUPPORTED for k > 16, cols > 2^20, tokens * k or
@@ -521,7 +523,9 @@ moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uin
  * The product of a gradient is the same call: dA = dOut W takes dOut's codes and the
  * turned weights.  Each block's products are summed by the matrix instruction (which
  * cuts off what lies below 2^-13 of the largest of eight neighbouring products),
- * scaled and added up in fp32.  Runs of one call are bitwise repeatable.
+ * scaled and added up in fp32.  Runs of one call are bitwise repeatable.  Outputs
+ * overlap no input.  The matrices are held fixed: what trains weights is
+ * moe_layer_bwd.
  * All pointers 16-byte aligned (scales and offsets 4).  MOE_E_INVALID for null or
  * misaligned pointers, sizes < 1, k not a multiple of 16, n not of 8 (of 16 with
  * SwiGLU), or no offsets with groups > 1; MOE_E_WORKSPACE for a smaller workspace;
@@ -553,7 +557,7 @@ moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gro
  *       zero).  One call at a time:
  *       calls that overlap on two streams take a workspace each.
  * max_norm must be positive; a NaN norm makes every gradient NaN, an infinite one
- * zero (an infinite gradient NaN).  Tensors need the alignment of their type only;
+ * zero (an infinite gradient NaN; with an infinite max_norm too, all of them).  Tensors need the alignment of their type only;
  * those that are not 16-byte aligned are read element by element.
  * Sums have a fixed order, so results are bitwise repeatable.  MOE_E_INVALID for
  * null or misaligned pointers, tensors < 1, a negative count or max_norm not above
