@@ -364,6 +364,12 @@ __device__ __forceinline__ void lds_put_get(uint32_t at0, uint32_t at1, u32x4& d
                  : "memory");
 }
 
+// A store that leaves the caches alone (in asm: two branches that store the same value to
+// the same place, with and without the hint, become one store without it).
+__device__ __forceinline__ void store_past(uint16_t* at, u32x4 v) {
+    asm volatile("global_store_dwordx4 %0, %1, off nt" ::"v"(at), "v"(v) : "memory");
+}
+
 template <class C, bool kGlu>
 __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     constexpr int kFI = C::kFI, kFJ = C::kFJ, kWM = C::kWM, kWN = C::kWN;
@@ -566,6 +572,14 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     int slot = 0, freed = 0;
+    // An output of more than the last cache's 256 MB whose 64 columns are whole lines leaves the
+    // caches to the operands (131072 x [7168, 2048], 32 groups: 1851 -> 1828 us; but 16384 x
+    // [2048, 1024], 67 MB: 38.4 -> 42, and 100000 x [2040, 512], part lines: 186 -> 245).
+    const bool stream = !kGlu && p.n % 64 == 0 && (int64_t)p.rows * p.n > (128ll << 20);
+    // Whether the tile before was whole, so that each wave stored 2 kFI kFJ times: the first
+    // stage then waits for its loads, which are older, and not for those stores too (with the
+    // line above 1851 -> 1805 us; 65536 x [4096, 1024] in 8 groups 318 -> 304).
+    bool stored = false;
 #pragma unroll
     for (int i = 0; i < kFI; ++i) read_frag(0, arow + i * kWM * 32 * kBlk, fa[i]);
     read_frag(0, brow, fb[0]);
@@ -591,8 +605,11 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                 }
                 if (i == 0 && j == kFJ - 1) {
                     // stage s + 1 has landed, and no wave reads stage s any more
-                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kEarlyA ? kRowsA / 8 : (C::kS - 2) * C::kLoads)
-                                 : "memory");
+                    constexpr int kAfter = kEarlyA ? kRowsA / 8 : (C::kS - 2) * C::kLoads;
+                    if (s == 0 && stored)
+                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAfter + 2 * kFI * kFJ) : "memory");
+                    else
+                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAfter) : "memory");
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
                     if (!kEarlyA) issue(kHalfA, k0, k1, s + C::kS, slot);
@@ -664,8 +681,14 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                         const int col = tile.n0 + (wn * kFJ + 2 * jp) * 32 + ch * 8;
                         uint16_t* dst = p.out + (int64_t)(tile.row0 + row + r0) * p.n + col;
                         const bool col_in = col < p.n;  // n is a multiple of 8
-                        if (col_in && row + r0 < tile.count) *(u32x4*)dst = d0;
-                        if (col_in && row + r0 + 8 < tile.count) *(u32x4*)(dst + 8 * (int64_t)p.n) = d1;
+                        const bool in0 = col_in && row + r0 < tile.count, in1 = col_in && row + r0 + 8 < tile.count;
+                        if (stream) {
+                            if (in0) store_past(dst, d0);
+                            if (in1) store_past(dst + 8 * (int64_t)p.n, d1);
+                        } else {
+                            if (in0) *(u32x4*)dst = d0;
+                            if (in1) *(u32x4*)(dst + 8 * (int64_t)p.n) = d1;
+                        }
                     }
                 }
         } else {
@@ -738,6 +761,7 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
             }
         }
         if (next.count == 0) break;
+        stored = !kGlu && kEarlyA && tile.count == C::kM && tile.n0 + kCols <= p.n;
         tile = next;
         src = nxt;
         t += step;
