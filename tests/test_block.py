@@ -331,6 +331,25 @@ def test_product(gpu_lib, counts, n, k, whole):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,k", [(2112, 272), (2048, 640), (2056, 256)])
+def test_output_past_the_last_cache(gpu_lib, n, k):
+    """More than 2^28 bytes of output, of whole lines and not, by tiles of which most are whole: exact sums."""
+    g = torch.Generator().manual_seed(n)
+    counts = _uneven(70000, 3)
+    rows = sum(counts) + 3
+    a, sa, w, sw = _operands(g, rows, k, 3, n, True)
+    off = _offsets(counts)
+    a, sa, w, sw = a.cuda(), sa.cuda(), w.cuda(), sw.cuda()
+    av, wv = _values(a, sa, w, sw)
+    out = torch.full((rows, n), 77, dtype=torch.bfloat16, device="cuda")
+    moe.moe_block_gemm(a.view(torch.uint8), sa, w.view(torch.uint8), sw, out, offsets=off.cuda())
+    for e in range(3):
+        lo, hi = off[e].item(), off[e + 1].item()
+        assert torch.equal(out[lo:hi], (av[lo:hi] @ wv[e].t()).float().bfloat16())
+    assert (out[sum(counts):] == 77).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,n,k", [(1, 64, 128), (37, 200, 336), (300, 264, 512)])
 def test_product_of_one_group_needs_no_offsets(gpu_lib, rows, n, k):
     g = torch.Generator().manual_seed(rows)
