@@ -336,8 +336,8 @@ struct BgTile {
     int g, row0, count, n0;  // n0: first output column; count: rows, at most kM; 0: no tile
 };
 
-// LDS accesses of the epilogue, in asm: the compiler would wait for the next tile's
-// loads into the ring too.
+// LDS accesses between two tiles' products, in asm: the compiler would wait for the next
+// tile's loads into the ring, and for the stores before them, too.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void lds_put(uint32_t at, uint32_t v) {
@@ -349,11 +349,18 @@ __device__ __forceinline__ void lds_put2(uint32_t at, u32x2 v) {
 __device__ __forceinline__ void lds_get4(uint32_t at, u32x4& d) {
     asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(d) : "v"(at) : "memory");
 }
-__device__ __forceinline__ void lds_get4x2(uint32_t at0, uint32_t at1, u32x4& d0, u32x4& d1) {
-    asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(d0), "=&v"(d1)
-                 : "v"(at0), "v"(at1)
-                 : "memory");
+// The lane, formed anew where it is needed: kept live over the products it would be spilled,
+// and a spilled value's return waits for every load and store before it.
+__device__ __forceinline__ int lane_now() {
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
+}
+
+__device__ __forceinline__ int lds_get(uint32_t at) {
+    int d;
+    asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(d) : "v"(at) : "memory");
+    return d;
 }
 
 // The wave's own writes, then two reads: LDS serves a wave in order.
@@ -417,23 +424,27 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     const int total = __builtin_amdgcn_readfirstlane(s_first[p.groups]) * NT;
     const int xcd = blockIdx.x & 7, per = (total + 7) / 8, step = gridDim.x >> 3;
     const int t_end = min((xcd + 1) * per, total);
+    const uint32_t t_first = lds_at(smem) + C::kTables, t_lo = t_first + (p.groups + 1) * 4, t_hi = t_lo + p.groups * 4;
+    auto uniform = [](uint32_t at) { return __builtin_amdgcn_readfirstlane(lds_get(at)); };
     auto tile_at = [&](int t) {
         BgTile r{0, 0, 0, 0};
         if (t >= t_end) return r;
+        const int l = lane_now();
         int e = 0;  // the last group with no more than t tiles before it; it is not empty
         for (int e0 = 0; e0 < p.groups; e0 += kWave) {
-            const int x = e0 + lane;
-            const uint64_t at = __ballot(x < p.groups && s_first[min(x, p.groups - 1)] * NT <= t);
+            const int x = e0 + l;
+            const int before = lds_get(t_first + min(x, p.groups - 1) * 4);
+            const uint64_t at = __ballot(x < p.groups && before * NT <= t);
             if (!at) break;
             e = e0 + 63 - __builtin_clzll(at);
         }
         r.g = e;
-        const int f0 = __builtin_amdgcn_readfirstlane(s_first[e]), f1 = __builtin_amdgcn_readfirstlane(s_first[e + 1]);
+        const int f0 = uniform(t_first + e * 4), f1 = uniform(t_first + e * 4 + 4);
         const int in = t - f0 * NT, block = in / (kBgPatch * NT), rest = in - block * kBgPatch * NT;
         const int high = min(kBgPatch, f1 - f0 - block * kBgPatch), col = rest / high;
         r.n0 = col * kCols;
-        r.row0 = __builtin_amdgcn_readfirstlane(s_lo[e]) + (block * kBgPatch + rest - col * high) * C::kM;
-        r.count = min(__builtin_amdgcn_readfirstlane(s_hi[e]) - r.row0, C::kM);
+        r.row0 = uniform(t_lo + e * 4) + (block * kBgPatch + rest - col * high) * C::kM;
+        r.count = min(uniform(t_hi + e * 4) - r.row0, C::kM);
         return r;
     };
     constexpr int kRowsA = C::kM / 8, kRowsB = C::kN / 8;  // rows of a stage that a wave loads
@@ -467,8 +478,8 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     // A load fills eight rows of a stage: lane l row l / 8, chunk l % 8 in LDS, which holds the
     // row's chunk (l % 8) ^ swz8(row), that is with bit 2 turned for every other eight rows.
     const int c_even = (lane & 7) ^ (lane >> 4), c_odd = c_even ^ 4;
-    const uint32_t v_even = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_even * 16;
-    const uint32_t v_odd = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_odd * 16;
+    uint32_t v_even = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_even * 16;
+    uint32_t v_odd = (uint32_t)(lane >> 3) * (uint32_t)p.k + c_odd * 16;
     const uint32_t v_eight = 8u * (uint32_t)p.k;
     BgSource src, nxt;
     // Part x of kParts of the A or the B half (with the scales) of stage s of this tile, or past
@@ -576,15 +587,17 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     // caches to the operands (131072 x [7168, 2048], 32 groups: 1851 -> 1828 us; but 16384 x
     // [2048, 1024], 67 MB: 38.4 -> 42, and 100000 x [2040, 512], part lines: 186 -> 245).
     const bool stream = !kGlu && p.n % 64 == 0 && (int64_t)p.rows * p.n > (128ll << 20);
-    // Whether the tile before was whole, so that each wave stored 2 kFI kFJ times: the first
-    // stage then waits for its loads, which are older, and not for those stores too (with the
-    // line above 1851 -> 1805 us; 65536 x [4096, 1024] in 8 groups 318 -> 304).
+    // Whether the tile before was whole, so that each wave stored kStores times at least: the first
+    // stage then waits for its loads, which are older, and not for those stores too.  (With the
+    // line above and nothing else that waits for them between two tiles 1851 -> 1798 us; 65536 x
+    // [4096, 1024] in 8 groups 318 -> 298; SwiGLU of 24576 x [1024, 2048], 64 groups 149 -> 144.)
     bool stored = false;
 #pragma unroll
     for (int i = 0; i < kFI; ++i) read_frag(0, arow + i * kWM * 32 * kBlk, fa[i]);
     read_frag(0, brow, fb[0]);
     read_scales(0);
     for (;;) {
+        asm volatile("" : "+v"(v_even), "+v"(v_odd));  // opaque: the first stage's addresses are not kept
 #pragma unroll
         for (int i = 0; i < kFI; ++i)
 #pragma unroll
@@ -605,11 +618,13 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                 }
                 if (i == 0 && j == kFJ - 1) {
                     // stage s + 1 has landed, and no wave reads stage s any more
+                    constexpr int kStores = kGlu ? kFI * kFJ / 2 : 2 * kFI * kFJ;
                     constexpr int kAfter = kEarlyA ? kRowsA / 8 : (C::kS - 2) * C::kLoads;
-                    if (s == 0 && stored)
-                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAfter + 2 * kFI * kFJ) : "memory");
+                    if (stored)
+                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAfter + kStores) : "memory");
                     else
                         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAfter) : "memory");
+                    stored = false;
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
                     if (!kEarlyA) issue(kHalfA, k0, k1, s + C::kS, slot);
@@ -648,15 +663,14 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         add(kF - 1);
 
         const uint32_t stg = lds_at(smem) + C::kRing;
-        int tid = threadIdx.x;  // opaque: the lane addresses are formed here, not kept live
-        asm volatile("" : "+v"(tid));
+        const int l = lane_now();
         if constexpr (!kGlu) {
             // 16 rows of 64 columns at a time through the wave's own block of LDS (chunk c of row r
             // at c ^ swz8(r)) and out in whole lines; no barrier, so the waves part here.  (32 rows of
             // all columns at a time by the whole workgroup, with two barriers each: 6.8 us a tile of
             // 256 x 256.)
             const uint32_t blk = stg + wave * kBgStg;
-            const int l = tid & 63, r16 = l & 15, h2 = (l >> 5) & 1, r0 = l >> 3, ch = l & 7;
+            const int r16 = l & 15, h2 = (l >> 5) & 1, r0 = l >> 3, ch = l & 7;
             const uint32_t put = blk + r16 * kBlk + 8 * h2;
             const uint32_t g0 = blk + r0 * kBlk + ((ch ^ swz8(r0)) << 4), g1 = blk + (r0 + 8) * kBlk + ((ch ^ swz8(r0 + 8)) << 4);
 #pragma unroll
@@ -694,8 +708,8 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
         } else {
             // h in place of the gate's fragments; a row's block of 128 is kWN waves' columns
             constexpr int kJ = kFJ / 2;
-            const int c0 = wn * kJ * 32 + 4 * half;  // this lane's first column of the tile
-            const int rl = wm * 32 + (tid & 31);
+            const int h2 = l >> 5, c0 = wn * kJ * 32 + 4 * h2;  // this lane's first column of the tile
+            const int rl = wm * 32 + (l & 31);
             const uint32_t mx = lds_at(smem) + C::kMax;
             float m[kFI];
 #pragma unroll
@@ -706,62 +720,63 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float g = acc[i][j][c];
-                        float h = blk_swiglu(g, acc[i][kJ + j][c]);
-                        if (tile.n0 + c0 + 32 * j + 8 * (c >> 2) >= p.n) h = 0.0f;  // n is a multiple of 16
+                        const float h = blk_swiglu(g, acc[i][kJ + j][c]);  // (past column n: of zeros)
                         acc[i][j][c] = h;
                         m[i] = fmaxf(m[i], fabsf(h));
                     }
                 m[i] = fmaxf(m[i], __shfl_xor(m[i], 32, kWave));
                 const float mi = m[i];  // (a cast of the array's element would be of its first one)
-                if (half == 0)
+                if (h2 == 0)
                     lds_put(mx + ((i * kWM * 32 + rl) * kWN + wn) * 4, __builtin_bit_cast(uint32_t, mi));
             }
             lds_barrier();
+            // A wave's columns of 32 rows go through its own block of LDS (chunk c of row r at c ^
+            // r / 4) and out; the waves part here.
+            constexpr int kChunks = 2 * kJ;  // of 16 codes
+            const uint32_t blk = stg + wave * kBgStg;
+            auto chunk_at = [&](int r, int c) { return blk + r * (16 * kChunks) + ((c ^ ((r >> 2) & (kChunks - 1))) << 4); };
+            const int r = l & 31;
 #pragma unroll
             for (int i = 0; i < kFI; ++i) {
-                if (i * kWM * 32 >= tile.count) break;
+                const int base = (i * kWM + wm) * 32;  // the wave's first row of these
+                if (base >= tile.count) break;
                 u32x4 all;  // the row's maxima (with two waves across, the next row's behind them)
-                lds_get4(mx + (i * kWM * 32 + rl) * kWN * 4 / 16 * 16, all);
+                lds_get4(mx + (base + r) * kWN * 4 / 16 * 16, all);
                 const uint32_t a0 = all[0], a1 = all[1], a2 = all[2], a3 = all[3];
                 auto f32 = [](uint32_t x) { return __builtin_bit_cast(float, x); };
                 const float lo = fmaxf(f32(a0), f32(a1)), hi = fmaxf(f32(a2), f32(a3));
-                const int e = blk_exp(kWN == 4 ? fmaxf(lo, hi) : (rl & 1 ? hi : lo));
-                const int row = tile.row0 + i * kWM * 32 + rl;
-                const bool row_in = i * kWM * 32 + rl < tile.count;
-                if (wn == 0 && half == 0 && row_in) p.hs[(int64_t)(tile.n0 / kBlk) * p.rows + row] = pow2f(e);
+                const int e = blk_exp(kWN == 4 ? fmaxf(lo, hi) : (r & 1 ? hi : lo));
+                const int64_t row = tile.row0 + base + r;
+                const bool row_in = base + r < tile.count;
+                if (wn == 0 && h2 == 0 && row_in) p.hs[(int64_t)(tile.n0 / kBlk) * p.rows + row] = pow2f(e);
                 const float inv = pow2f(-e);
 #pragma unroll
                 for (int j = 0; j < kJ; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const floatx16& x = acc[i][j];
-                        const int col = c0 + 32 * j + 8 * q;
-                        lds_put(stg + rl * kBlk + (((col >> 4) ^ swz8(rl)) << 4) + (col & 15),
+                        lds_put(chunk_at(r, 2 * j + (q >> 1)) + 8 * (q & 1) + 4 * h2,
                                 fp8x4(x[4 * q] * inv, x[4 * q + 1] * inv, x[4 * q + 2] * inv, x[4 * q + 3] * inv));
-                        if (p.h16 && row_in && tile.n0 + col < p.n)
-                            *(u32x2*)(p.h16 + (int64_t)row * p.n + tile.n0 + col) =
+                        const int col = tile.n0 + c0 + 32 * j + 8 * q;
+                        if (p.h16 && row_in && col < p.n)
+                            *(u32x2*)(p.h16 + row * p.n + col) =
                                 u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])};
                     }
-                lds_barrier();
-                // kWM x 32 rows of eight chunks: 64 rows at once
-                const int r0 = tid >> 3, ch = tid & 7;
-                const bool col_in = tile.n0 + ch * 16 < p.n;
-                auto from = [&](int r) { return stg + r * kBlk + ((ch ^ swz8(r)) << 4); };
-                uint8_t* dst = p.hq + (int64_t)(tile.row0 + i * kWM * 32 + r0) * p.n + tile.n0 + ch * 16;
+                const int r0 = l / kChunks, ch = l % kChunks, col = tile.n0 + wn * kJ * 32 + ch * 16;
+                uint8_t* dst = p.hq + (int64_t)(tile.row0 + base + r0) * p.n + col;
                 u32x4 d0, d1;
-                if constexpr (kWM == 4) {
-                    lds_get4x2(from(r0), from(r0 + 64), d0, d1);
-                    if (col_in && i * kWM * 32 + r0 + 64 < tile.count) *(u32x4*)(dst + 64 * (int64_t)p.n) = d1;
+                if constexpr (kJ == 2) {  // 16 rows at once
+                    lds_put_get(chunk_at(r0, ch), chunk_at(r0 + 16, ch), d0, d1);
+                    if (col < p.n && base + r0 + 16 < tile.count) *(u32x4*)(dst + 16 * (int64_t)p.n) = d1;
                 } else {
-                    static_assert(kWM == 2, "");
-                    lds_get4(from(r0), d0);
+                    static_assert(kJ == 1, "");
+                    lds_get4(chunk_at(r0, ch), d0);
                 }
-                if (col_in && i * kWM * 32 + r0 < tile.count) *(u32x4*)dst = d0;
-                lds_barrier();
+                if (col < p.n && base + r0 < tile.count) *(u32x4*)dst = d0;
             }
         }
         if (next.count == 0) break;
-        stored = !kGlu && kEarlyA && tile.count == C::kM && tile.n0 + kCols <= p.n;
+        stored = kEarlyA && tile.count == C::kM && tile.n0 + kCols <= p.n;
         tile = next;
         src = nxt;
         t += step;
@@ -797,7 +812,7 @@ enum BlockForm { kFormFew, kForm256x256, kForm128x256, kForm128x128, kForm64x256
 //   256 rows x [4096, 4096]    43, 31, 22, 27, 39;    2048 rows               48, 40, 48, 56, 268
 //   4096 rows                  61, 78, 91, 104, 531;  16384 rows              234, 299, 344, 394, -
 //   32 groups of [7168, 2048]  64 rows 88, 77, 76, 72, 76;  1024 rows 112, 103, 100, 96, 116
-//   8192 rows                  186, 196, 216, 226, 957;     131072 rows 1819, 2272, 2574, 2912, 14243
+//   8192 rows                  186, 196, 216, 226, 957;     131072 rows 1798, 2272, 2574, 2912, 14243
 static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
     const double r = (double)rows, kb = blk_count(k);
     const double active = std::min(r, groups * (1.0 - exp(-r / groups)));  // groups with rows, routed evenly
