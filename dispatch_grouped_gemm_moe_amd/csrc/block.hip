@@ -23,6 +23,7 @@ namespace moe {
 // A piece of a buffer load that lies past a row's end or a matrix's last row asks for
 // this offset: past every buffer here (they hold less than 2 GiB), so it reads as zero.
 constexpr uint32_t kNowhere = 0x80000000u;
+constexpr int kPastCaches = 2;  // of a buffer load: the non-temporal hint
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t blk_rsrc(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
@@ -136,7 +137,7 @@ __device__ __forceinline__ void few_frags(uint32_t p0, uint32_t p1, intx8 (&w)[k
 // A wave's step is kU blocks of K.  Its weights come straight into one of the wave's own
 // two LDS slots in whole lines, eight rows an instruction, asked for a step ahead; the
 // rows of a, which every workgroup of the group reads, come from the cache into registers.
-template <int kNF, int kTF, bool kGlu>
+template <int kNF, int kTF, bool kGlu, bool kPast>
 __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int row0, int count, int n0,
                                                uint8_t (*s_w)[2][kBfSlot]) {
     constexpr int kW = kGlu ? 2 * kNF : kNF;  // weight fragments: the gate's, then the up matrix's
@@ -167,7 +168,8 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
             const int at = ((s * kBfWaves + wave) * kU + q / 2 / kW) * kBlk + ((lane & 7) ^ (4 * (q & 1) | (lane >> 4))) * 16;
             // k is a multiple of 16: a piece is inside the row or not
             const uint32_t o = at < a.k ? (uint32_t)row * (uint32_t)a.k + at + f % kNF * off16 : kNowhere;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(f < kNF ? rw : ru, (lds_void*)(dst + q * 1024), 16, o, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(f < kNF ? rw : ru, (lds_void*)(dst + q * 1024), 16, o, 0, 0,
+                                                     kPast ? kPastCaches : 0);
         }
     };
     struct Rows {
@@ -281,16 +283,16 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
     }
 }
 
-template <int kNF, bool kGlu>
+template <int kNF, bool kGlu, bool kPast>
 __global__ __launch_bounds__(kBfWaves * kWave, 2) void block_few_kernel(BlockGemm a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_w[kBfWaves][2][kBfSlot];
     int g, row0, count;
     for (int slot = blockIdx.y; find_part<kBfRows>(a.offsets, a.groups, a.rows, slot, g, row0, count);
          slot += gridDim.y) {
         const int n0 = blockIdx.x * 16 * kNF;
-        if (count <= 16) block_few_part<kNF, 1, kGlu>(a, g, row0, count, n0, s_w);
-        else if (count <= 32) block_few_part<kNF, 2, kGlu>(a, g, row0, count, n0, s_w);
-        else block_few_part<kNF, 4, kGlu>(a, g, row0, count, n0, s_w);
+        if (count <= 16) block_few_part<kNF, 1, kGlu, kPast>(a, g, row0, count, n0, s_w);
+        else if (count <= 32) block_few_part<kNF, 2, kGlu, kPast>(a, g, row0, count, n0, s_w);
+        else block_few_part<kNF, 4, kGlu, kPast>(a, g, row0, count, n0, s_w);
     }
 }
 
@@ -377,7 +379,7 @@ __device__ __forceinline__ void store_past(uint16_t* at, u32x4 v) {
     asm volatile("global_store_dwordx4 %0, %1, off nt" ::"v"(at), "v"(v) : "memory");
 }
 
-template <class C, bool kGlu>
+template <class C, bool kGlu, bool kPast>
 __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     constexpr int kFI = C::kFI, kFJ = C::kFJ, kWM = C::kWM, kWN = C::kWN;
     constexpr int kCols = kGlu ? C::kN / 2 : C::kN;  // output columns of a tile
@@ -502,7 +504,8 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
             const uint32_t v = (odd ? v_odd : v_even) + i * v_eight + s * kBlk;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (lds_void*)(st + (kA ? 0 : C::kStageB) + wave * kRows * kBlk + i * 1024), 16,
-                (odd ? in_o : in_e) ? v : kNowhere, 0, 0, 0);
+                (odd ? in_o : in_e) ? v : kNowhere, 0, 0,
+                kPast && !kA ? kPastCaches : 0);
         }
         // (a wave without scales fills its area with zeros: a branch here would let the
         // compiler move every addition of the stage past it)
@@ -787,9 +790,9 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-template <class C, bool kGlu>
+template <class C, bool kGlu, bool kPast>
 __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) {
-    block_gemm_tiles<C, kGlu>(p);
+    block_gemm_tiles<C, kGlu, kPast>(p);
 }
 
 // Parts of at most `part` rows that `rows` rows of `groups` groups can fall into.
@@ -802,29 +805,51 @@ using Bg64x256 = BgShape<2, 4, 1, 2, 3>;
 
 enum BlockForm { kFormFew, kForm256x256, kForm128x256, kForm128x128, kForm64x256 };
 
+// Groups with rows, routed evenly.
+static double active_groups(int64_t rows, int groups) {
+    return std::min((double)rows, groups * (1.0 - exp(-(double)rows / groups)));
+}
+
+// Whether the weights' loads leave the caches alone: more than the last cache's 256 MB of them,
+// and so few rows to a group that one part holds them and the weights are read once (us: SwiGLU
+// of [2048, 7168] in 32 groups, 64 rows 163 -> 155, 512 rows 172 -> 153; [7168, 2048] in 32
+// groups, 512 rows 94 -> 87; but 2048 rows 119 -> 133, and 8 rows, which need 105 MB of
+// weights, 22.6 -> 24.3).
+static bool weights_past_caches(const BlockGemm& a) {
+    const double active = active_groups(a.rows, a.groups);
+    return a.rows <= active * (kBfRows / 2) && active * a.n * a.k * (a.wu ? 2 : 1) > 256.0 * (1 << 20);
+}
+
 // The form with the least expected time, in us.  A tile takes a block of K in `low` us
 // where it is one of few and in `full` us where every CU has one, and `end` us for its
 // epilogue (fitted to products of [4096, 4096] and [4096, 1024] with 256 to 16384 rows);
-// tiles run in rounds of one to a CU.  Larger tiles need less of everything for each
-// element, smaller ones fill the CUs sooner and pad a group's rows less.  Measured, us,
-// tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 256 and the few-row form (-: not timed):
+// tiles run in rounds of one to a CU, and no faster than they read the weights.  Larger
+// tiles need less of everything for each element, smaller ones fill the CUs sooner and pad a
+// group's rows less.  The few-row form needs more the more fragments of 16 rows a part has;
+// past 64 groups a workgroup takes longer to find its part.  Measured, us, tiles of 256 x 256,
+// 128 x 256, 128 x 128, 64 x 256 and the few-row form (-: not timed):
 //   1 row x [2048, 1024]       -, -, 8.2, 9.2, 3.7;   64 rows x [4096, 4096]  -, -, 21, 26, 12
 //   256 rows x [4096, 4096]    43, 31, 22, 27, 39;    2048 rows               48, 40, 48, 56, 268
 //   4096 rows                  61, 78, 91, 104, 531;  16384 rows              234, 299, 344, 394, -
-//   32 groups of [7168, 2048]  64 rows 88, 77, 76, 72, 76;  1024 rows 112, 103, 100, 96, 116
-//   8192 rows                  186, 196, 216, 226, 957;     131072 rows 1798, 2272, 2574, 2912, 14243
+//   16 groups of [4096, 4096]  32 rows -, -, 63, 66, 49;  128 rows            -, -, 67, 69, 53
+//   32 groups of [7168, 2048]  64 rows -, -, 85, 77, 71;  512 rows            -, -, 98, 85, 87
+//   1024 rows                  112, 103, 100, 96, 116;    8192 rows           186, 196, 216, 226, 957
+//   131072 rows                1798, 2272, 2574, 2912, 14243
+//   SwiGLU, [2048, 7168]       64 rows -, -, -, 134, 132; 512 rows            -, -, -, 142, 160
+//   256 groups of [512, 1024]  512 rows -, -, 32, 27, 31; SwiGLU              -, -, -, 50, 58
 static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
-    const double r = (double)rows, kb = blk_count(k);
-    const double active = std::min(r, groups * (1.0 - exp(-r / groups)));  // groups with rows, routed evenly
+    const double r = (double)rows, kb = blk_count(k), active = active_groups(rows, groups);
     auto parts = [&](int m) {  // of m rows: half a part of padding to a group
         return groups == 1 ? ceil(r / m) : std::max(active, r / m + active / 2);
     };
-    const double per_group = r / active;
+    const double per_group = r / active, wide = glu ? 2 : 1;
     const double strips = ((n + 15) / 16) * parts(kBfRows) / 256;
+    const double busy = per_group <= (groups == 1 ? 16 : 10) ? 1 : per_group <= 16 ? 1.2 : per_group <= 32 ? 1.5 : 3;
     BlockForm best = kFormFew;
-    double least = 3.5 + kb * 0.14 * (glu ? 2 : 1) * (per_group <= 16 ? 1.0 : per_group <= 32 ? 1.4 : 2.0) *
-                             std::max(1.0, strips);
+    double least = 3.5 + wide * std::max(kb * 0.14 * std::min(busy, 2.0),
+                                         strips * busy * (kb * 0.09 + (groups > kWave ? 0.3 : 0.05)));
     if (groups > kBgGroups) return best;
+    const double weights = wide * active * n * k / 5.4e6;  // read at 5.4 TB/s
     const struct { BlockForm form; int m, n, stages; double low, full, end; } tiles[] = {
         {kForm256x256, 256, 256, Bg256x256::kS, 1.155, 1.66, 4.2}, {kForm128x256, 128, 256, Bg128x256::kS, 0.81, 1.08, 2.6},
         {kForm128x128, 128, 128, Bg128x128::kS, 0.564, 0.62, 1.5}, {kForm64x256, 64, 256, Bg64x256::kS, 0.703, 0.72, 1.5}};
@@ -832,8 +857,9 @@ static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
         if (kb < t.stages || (glu && t.n != 256)) continue;  // a block of h is half of 256 columns
         const int cols = glu ? t.n / 2 : t.n;
         const double rounds = parts(t.m) * ((n + cols - 1) / cols) / 256;
-        const double us = 2.5 + (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds) *
-                                  (kb * (rounds <= 1 ? t.low : t.full) + t.end);
+        const double run = (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds) *
+                           (kb * (rounds <= 1 ? t.low : t.full) + t.end);
+        const double us = 2.5 + std::max(run, weights) + std::min(run, weights) / 10;
         if (us < least) {
             least = us;
             best = t.form;
@@ -844,9 +870,10 @@ static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
 
 bool block_gemm_large(int64_t rows, int n, int k, int groups) { return block_form(rows, n, k, groups, true) != kFormFew; }
 
+template <bool kPast>
 static void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream) {
 #define BLOCK_FEW(NF, GLU)                                                                                      \
-    hipLaunchKernelGGL((block_few_kernel<NF, GLU>),                                                             \
+    hipLaunchKernelGGL((block_few_kernel<NF, GLU, kPast>),                                                      \
                        dim3((a.n + 16 * NF - 1) / (16 * NF), std::min(most_parts(a.rows, a.groups, kBfRows), 65535)), \
                        dim3(kBfWaves * kWave), 0, stream, a)
     const int64_t strips = (int64_t)((a.n + 15) / 16) * std::min(a.rows, a.groups);
@@ -861,18 +888,21 @@ static void launch_block_gemm_few(const BlockGemm& a, hipStream_t stream) {
 #undef BLOCK_FEW
 }
 
-template <class C, bool kGlu>
+template <class C, bool kGlu, bool kPast = false>
 static void launch_block_gemm_tiles(const BlockGemm& a, hipStream_t stream) {
     const int cols = kGlu ? C::kN / 2 : C::kN;
     const int64_t tiles = (int64_t)most_parts(a.rows, a.groups, C::kM) * ((a.n + cols - 1) / cols);
     const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256);  // a multiple of the XCDs
-    hipLaunchKernelGGL((block_gemm_kernel<C, kGlu>), dim3(grid), dim3(kBgThreads), C::kSmem, stream, a);
+    hipLaunchKernelGGL((block_gemm_kernel<C, kGlu, kPast>), dim3(grid), dim3(kBgThreads), C::kSmem, stream, a);
 }
 
 void launch_block_gemm(const BlockGemm& a, hipStream_t stream) {
-    const bool glu = a.wu != nullptr;
+    const bool glu = a.wu != nullptr, past = weights_past_caches(a);
     switch (block_form(a.rows, a.n, a.k, a.groups, glu)) {
-        case kFormFew: launch_block_gemm_few(a, stream); return;
+        case kFormFew:
+            if (past) launch_block_gemm_few<true>(a, stream);
+            else launch_block_gemm_few<false>(a, stream);
+            return;
         case kForm256x256:
             if (glu) launch_block_gemm_tiles<Bg256x256, true>(a, stream);
             else launch_block_gemm_tiles<Bg256x256, false>(a, stream);
@@ -882,8 +912,10 @@ void launch_block_gemm(const BlockGemm& a, hipStream_t stream) {
             else launch_block_gemm_tiles<Bg128x256, false>(a, stream);
             return;
         case kForm128x128: launch_block_gemm_tiles<Bg128x128, false>(a, stream); return;
-        case kForm64x256:
-            if (glu) launch_block_gemm_tiles<Bg64x256, true>(a, stream);
+        case kForm64x256:  // the only tiles that few rows to a group fall to
+            if (glu && past) launch_block_gemm_tiles<Bg64x256, true, true>(a, stream);
+            else if (glu) launch_block_gemm_tiles<Bg64x256, true>(a, stream);
+            else if (past) launch_block_gemm_tiles<Bg64x256, false, true>(a, stream);
             else launch_block_gemm_tiles<Bg64x256, false>(a, stream);
             return;
     }

@@ -280,6 +280,8 @@ PRODUCTS = [([1], 8, 16), ([1], 64, 128), ([3], 264, 144), ([1, 0, 2], 136, 272)
 
 def _uneven(rows, groups):
     """Counts that differ from group to group, some zero, some of whole tiles."""
+    if groups == 1:
+        return [rows]
     part = [(7 * i + 3) % 11 if i % 5 else 0 for i in range(groups)]
     counts = [rows * x // max(1, sum(part)) for x in part]
     counts[1 % groups] += -counts[1 % groups] % 256 if rows > 2000 else 0
@@ -292,10 +294,11 @@ TILED = [(4100, 40, 1032, 144), (4100, 40, 1032, 400), (4100, 40, 1032, 656), (6
          (1500, 40, 1032, 144), (7000, 40, 264, 272), (2300, 40, 1032, 656), (2049, 1, 2056, 528), (100, 3, 6152, 400),
          (2300, 40, 264, 656), (1024, 1, 1032, 1040), (100, 40, 1032, 1040), (100, 40, 4104, 272), (300, 40, 1032, 400),
          (9000, 3, 2056, 144), (12000, 3, 4104, 272), (16400, 40, 2056, 144), (30000, 40, 1032, 656),
-         (1300, 600, 136, 272)]
+         (1300, 600, 136, 272), (12000, 600, 136, 272), (5000, 520, 40, 272)]
 TILED_GLU = [(4100, 40, 528, 144), (4100, 40, 528, 400), (4100, 40, 528, 656), (4129, 1, 2064, 272), (1500, 40, 528, 144),
              (7000, 40, 144, 272), (7000, 40, 144, 656), (100, 40, 1552, 272), (100, 40, 528, 528), (700, 3, 1040, 656),
-             (12000, 3, 2064, 272), (16400, 40, 1040, 144), (30000, 40, 528, 656), (1300, 600, 144, 272)]
+             (12000, 3, 2064, 272), (16400, 40, 1040, 144), (30000, 40, 528, 656), (1300, 600, 144, 272),
+             (12000, 600, 144, 272)]
 SHAPES = PRODUCTS + [(_uneven(r, e), n, k) for r, e, n, k in TILED]
 SHAPES_GLU = [(c, (n + 15) // 16 * 16, k) for c, n, k in PRODUCTS] + [(_uneven(r, e), n, k) for r, e, n, k in TILED_GLU]
 _name = lambda v: "x".join(map(str, [len(v), sum(v)])) if isinstance(v, list) else str(v)
@@ -408,6 +411,49 @@ def test_swiglu_product(gpu_lib, counts, n, k):
         assert (torch.frexp(hs[b, :m])[0] == 0.5).all()
         assert (amax <= 448 * hs[b, :m].double() * (1 + HALF)).all()
         assert ((amax >= 224 * hs[b, :m].double() * (1 - HALF)) | (hs[b, :m] <= 2.0 ** -126)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("counts", [[1, 0, 2, 1] * 10, [0, 16, 3, 37, 8] * 8, [2, 0, 1] * 200], ids=_name)
+def test_weights_past_the_last_cache(gpu_lib, counts, glu):
+    """More than 2^28 bytes of weights for few rows to a group, in every form they fall to: whole numbers, exact sums."""
+    groups, spare = len(counts), 2
+    n, k = (2064, 3600) if groups < 100 else (528, 1168)
+    n = n if glu else 2 * n + 8
+    rows = sum(counts) + spare
+    g = torch.Generator(device="cuda").manual_seed(groups + rows)
+    draw = lambda *shape: torch.randint(-2, 3, shape, generator=g, device="cuda").to(torch.float8_e4m3fn)
+    a, ws = draw(rows, k), [draw(groups, n, k) for _ in range(2 if glu else 1)]
+    sa = torch.exp2(torch.randint(-2, 3, ((k + 127) // 128, rows), generator=g, device="cuda").float())
+    sw = torch.exp2(torch.randint(-8, -6, (groups, (n + 127) // 128, (k + 127) // 128), generator=g, device="cuda").float())
+    off = _offsets(counts)
+    want = []
+    for w in ws:
+        want.append(torch.full((rows, n), float("nan"), dtype=torch.float64, device="cuda"))
+        for e in range(groups):
+            lo, hi = off[e].item(), off[e + 1].item()
+            if hi > lo:
+                av, wv = _values(a[lo:hi], sa[:, lo:hi], w[e:e + 1], sw[e:e + 1])
+                want[-1][lo:hi] = av @ wv[0].t()
+    m, u = sum(counts), lambda t: t.view(torch.uint8)
+    out = torch.full((rows, n), 77, dtype=torch.bfloat16, device="cuda")
+    if not glu:
+        moe.moe_block_gemm(u(a), sa, u(ws[0]), sw, out, offsets=off.cuda())
+        assert torch.equal(out[:m], want[0][:m].float().bfloat16()) and (out[m:] == 77).all()
+        return
+    nb = (n + 127) // 128
+    hq, hs = torch.full((rows, n), 77, dtype=torch.uint8, device="cuda"), torch.full((nb, rows), 77.0, device="cuda")
+    buf = torch.empty(moe.moe_query_block_swiglu(rows, n, k, groups), dtype=torch.uint8, device="cuda")
+    moe.moe_block_gemm_swiglu(u(a), sa, u(ws[0]), sw, u(ws[1]), sw, hq, hs, buf, h=out, offsets=off.cuda())
+    h = (want[0] * torch.sigmoid(want[0]) * want[1])[:m]
+    near = out[:m].double()
+    # (a hardware exponential and reciprocal of a few 2^-24 of the value each, in front of the rounding)
+    assert ((near - h).abs() <= h.abs() * HALF * 1.01 + h.abs() * 2.0 ** -18).all()
+    s = hs.double().t().repeat_interleave(128, 1)[:m, :n]
+    held = hq[:m].view(torch.float8_e4m3fn).double() * s
+    assert ((held - near).abs() <= near.abs() * (2.0 ** -4 + HALF) * 1.01 + s * 2.0 ** -10).all()
+    assert (out[m:] == 77).all() and (hq[m:] == 77).all() and (hs[:, m:] == 77).all()
 
 
 @pytest.mark.gpu
