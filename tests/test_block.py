@@ -218,6 +218,31 @@ def test_quantize_weights_bit_for_bit(gpu_lib, groups, n, k):
 
 
 @pytest.mark.gpu
+def test_dequantize_past_32_bits(gpu_lib):
+    """Values past 2^32 bytes, as rows and as matrices (one scale each for all blocks but the last row's)."""
+    cols, n = 4112, 1024
+    R = n * 511
+    codes = (torch.arange(R * cols, dtype=torch.int64, device="cuda") % 126).to(torch.uint8).view(R, cols)
+    codes[-1] += 128  # negative ones
+    back = torch.empty(R, cols, dtype=torch.bfloat16, device="cuda")
+    assert 2 * back.numel() > 1 << 32
+    scales = torch.full((33, R), 2.0, device="cuda")
+    scales[:, -1] = 0.5
+    moe.moe_block_dequantize(codes, scales, back)
+    table = torch.arange(256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).bfloat16()
+    for lo in range(0, R, 1 << 16):
+        part = codes[lo:lo + (1 << 16)]
+        assert torch.equal(back[lo:lo + (1 << 16)], table[part.int()] * scales[0, lo:lo + (1 << 16), None].bfloat16())
+    w = torch.full((511, n // 128, 33), 4.0, device="cuda")
+    w[-1, -1] = 0.25
+    moe.moe_block_dequantize(codes.view(511, n, cols), w, back.view(511, n, cols), weights=True)
+    for lo in range(0, R, 1 << 16):
+        part = codes[lo:lo + (1 << 16)]
+        s = w[:, :, 0].reshape(-1).repeat_interleave(128)[lo:lo + (1 << 16), None]
+        assert torch.equal(back[lo:lo + (1 << 16)], table[part.int()] * s.bfloat16())
+
+
+@pytest.mark.gpu
 def test_quantize_nan_and_infinity(gpu_lib):
     v = torch.ones(4, 256, dtype=torch.bfloat16)
     v[0, 3], v[1, 130], v[2, 7] = float("nan"), float("inf"), -float("inf")
