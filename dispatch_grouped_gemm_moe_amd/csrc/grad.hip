@@ -87,7 +87,8 @@ __device__ __forceinline__ GradSums grad_squares(const void* src, const GradChun
 // Workgroup b sums chunks b, b + grid, ... into its own slot.  The last workgroup to
 // finish (of a call's last launch) adds all slots in ascending order.  They count in 32
 // to a counter, and the last of 32 to one above them, each in a cache line of its own:
-// 2048 workgroups on one counter take 25 us to pass it.
+// 2048 workgroups on one counter take 25 us to pass it.  1.4e9 fp32 values: 823 us (6.9 TB/s);
+// a layer's few thousand 5.6 us.
 __global__ __launch_bounds__(kGradThreads) void grad_norm_kernel(GradList a, double* partial, int slot0, int slots,
                                                                  int* counters, float* norm) {
     __shared__ double s_sum[kGradThreads / kWave];

@@ -523,9 +523,10 @@ moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uin
  * The product of a gradient is the same call: dA = dOut W takes dOut's codes and the
  * turned weights.  Each block's products are summed by the matrix instruction (which
  * cuts off what lies below 2^-13 of the largest of eight neighbouring products),
- * scaled and added up in fp32.  Runs of one call are bitwise repeatable.  Outputs
- * overlap no input.  The matrices are held fixed: what trains weights is
- * moe_layer_bwd.
+ * scaled and added up in fp32.  Past 512 groups the form for few rows does it all,
+ * which reads a group's matrix once for every 64 of its rows.  Runs of one call are
+ * bitwise repeatable.  Outputs overlap no input.  The matrices are held fixed: what
+ * trains weights is moe_layer_bwd.
  * All pointers 16-byte aligned (scales and offsets 4).  MOE_E_INVALID for null or
  * misaligned pointers, sizes < 1, k not a multiple of 16, n not of 8 (of 16 with
  * SwiGLU), or no offsets with groups > 1; MOE_E_WORKSPACE for a smaller workspace;
@@ -554,11 +555,12 @@ moe_status moe_block_gemm_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gro
  *   norm: device fp32.  Summed in 64 bits, so no fp32 square overflows;
  *   ws: moe_query_grad_norm bytes, 16-byte aligned; zero its first
  *       MOE_GRAD_COUNTER_BYTES bytes once when it is allocated (every call leaves them
- *       zero).  One call at a time:
- *       calls that overlap on two streams take a workspace each.
+ *       zero).  One call at a time: calls that overlap on two streams take a workspace
+ *       each.
  * max_norm must be positive; a NaN norm makes every gradient NaN, an infinite one
- * zero (an infinite gradient NaN; with an infinite max_norm too, all of them).  Tensors need the alignment of their type only;
- * those that are not 16-byte aligned are read element by element.
+ * zero (an infinite gradient NaN; with an infinite max_norm too, all of them).
+ * Tensors need the alignment of their type only; those that are not 16-byte aligned
+ * are read element by element.
  * Sums have a fixed order, so results are bitwise repeatable.  MOE_E_INVALID for
  * null or misaligned pointers, tensors < 1, a negative count or max_norm not above
  * 0 (infinity is: it scales by 1); MOE_E_WORKSPACE for a smaller workspace;
