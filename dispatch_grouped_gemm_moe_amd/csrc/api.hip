@@ -1064,7 +1064,7 @@ moe_status moe_block_quantize_weights(int32_t groups, int32_t n, int32_t k, cons
     if (groups < 1 || n < 1 || k < 16 || k % 16 || (transposed != 0 && transposed != 1)) return MOE_E_INVALID;
     if ((transposed && n % 8) || !src || !codes || !scales) return MOE_E_INVALID;
     if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_E_INVALID;
-    if ((int64_t)groups * n > (1 << 30) || (int64_t)n * k >= (1ll << 31)) return MOE_E_UNSUPPORTED;
+    if ((int64_t)groups * n > (1 << 30) || k > (1 << 20) || (int64_t)n * k >= (1ll << 31)) return MOE_E_UNSUPPORTED;
     TIMED(MOE_K_OTHER, (hipStream_t)stream,
           launch_block_quant_weights(src, groups, n, k, transposed, codes, scales, (hipStream_t)stream));
     return check_launch();
@@ -1075,7 +1075,7 @@ moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uin
     if (rows < 1 || cols < 16 || cols % 16 || n < 0 || (n && rows % n) || !codes || !scales || !dst)
         return MOE_E_INVALID;
     if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(dst, 16)) return MOE_E_INVALID;
-    if (rows > (1 << 30) || (n == 0 && cols > (1 << 20)) || (int64_t)n * cols >= (1ll << 31)) return MOE_E_UNSUPPORTED;
+    if (rows > (1 << 30) || cols > (1 << 20) || (int64_t)n * cols >= (1ll << 31)) return MOE_E_UNSUPPORTED;
     TIMED(MOE_K_OTHER, (hipStream_t)stream, launch_block_dequant(codes, scales, rows, cols, n, dst, (hipStream_t)stream));
     return check_launch();
 }

@@ -452,9 +452,8 @@ moe_status moe_query_few(const moe_cfg *cfg, size_t *workspace);
  *   dout.
  *
  * Rows that the table does not name are left as they were.  Buffers overlap in no
- * other way.  All pointers 16-byte
- * aligned (tok_row, w, dw and scales 4).  MOE_E_INVALID for null or misaligned
- * pointers, no output, tokens, k or rows < 1, cols not a positive multiple of 8
+ * other way.  All pointers 16-byte aligned (tok_row, w, dw and scales 4).
+ * MOE_E_INVALID for null or misaligned pointers, no output, tokens, k or rows < 1, cols not a positive multiple of 8
  * (of 16 with codes); MOE_E_UNSUPPORTED for k > 16, cols > 2^20, tokens * k or
  * rows > 2^30.  Sums have a fixed order, so results are bitwise repeatable.
  */
@@ -492,7 +491,7 @@ moe_status moe_combine_rows_bwd(int64_t tokens, int32_t k, int32_t cols, int64_t
  * MOE_E_INVALID for null or misaligned pointers, sizes < 1, cols and k not
  * multiples of 16, n not a multiple of 8 with transposed = 1, n not a divisor of
  * rows or an unknown transposed; MOE_E_UNSUPPORTED for rows (groups * n) > 2^30,
- * cols > 2^20 or n * k >= 2^31.
+ * cols or k > 2^20 or n * k >= 2^31.
  */
 moe_status moe_block_quantize(int64_t rows, int32_t cols, const uint16_t *src, uint8_t *codes, float *scales,
                               void *stream);

@@ -85,7 +85,7 @@ def test_quantize_refuses(kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(g=0), 1), (dict(n=0), 1), (dict(n=12), 1), (dict(k=24), 1), (dict(t=2), 1), (dict(t=-1), 1),
     (dict(src=None), 1), (dict(q=None), 1), (dict(s=None), 1), (dict(src=FAKE + 8), 1), (dict(q=FAKE + 8), 1),
-    (dict(s=FAKE + 2), 1), (dict(g=1 << 25), 2), (dict(n=1 << 20, k=1 << 11), 2)])
+    (dict(s=FAKE + 2), 1), (dict(g=1 << 25), 2), (dict(n=1 << 20, k=1 << 11), 2), (dict(n=8, k=(1 << 20) + 16), 2)])
 def test_quantize_weights_refuses(kw, want):
     a = dict(g=2, n=64, k=64, t=1, src=FAKE, q=FAKE, s=FAKE)
     a.update(kw)
@@ -95,6 +95,8 @@ def test_quantize_weights_refuses(kw, want):
 def test_dequantize_refuses_rows_that_are_no_whole_matrices():
     call = lambda rows, n: moe.lib().moe_block_dequantize(rows, 64, n, FAKE, FAKE, FAKE, None)
     assert call(10, 4) == call(10, -1) == moe.MOE_E_INVALID
+    wide = moe.lib().moe_block_dequantize(8, (1 << 20) + 16, 8, FAKE, FAKE, FAKE, None)
+    assert wide == moe.MOE_E_UNSUPPORTED  # more columns than the products and the kernel's grid take
 
 
 def test_binding_refuses_tensors_the_kernels_cannot_read():
