@@ -1053,9 +1053,7 @@ moe_status moe_block_quantize(int64_t rows, int32_t cols, const uint16_t* src, u
     if (rows < 1 || cols < 16 || cols % 16 || !src || !codes || !scales) return MOE_E_INVALID;
     if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_E_INVALID;
     if (rows > (1 << 30) || cols > (1 << 20)) return MOE_E_UNSUPPORTED;
-    RowsDispatch a{};
-    a.tokens = rows; a.rows = rows; a.cols = cols; a.k = 1; a.x = src; a.codes = codes; a.scales = scales;
-    TIMED(MOE_K_GATHER, (hipStream_t)stream, launch_rows_dispatch(a, (hipStream_t)stream));
+    TIMED(MOE_K_GATHER, (hipStream_t)stream, launch_block_quant(src, rows, cols, codes, scales, (hipStream_t)stream));
     return check_launch();
 }
 

@@ -450,8 +450,8 @@ struct RowsDispatch {
     int64_t tokens, rows;      // rows: of dst, or of the codes
     int cols, k;
     const uint16_t* x;         // [tokens][cols]
-    const float* xf;           // or fp32 values in its place (codes only)
-    const int32_t* tok_row;    // [tokens][k]; NULL: token t is row t, k = 1
+    const float* xf;           // or fp32 values in its place (codes, and dst in bf16 beside them)
+    const int32_t* tok_row;    // [tokens][k]; NULL: token t is row t, k = 1 (with xf)
     const int32_t* offsets;    // or NULL; else only tokens offsets[0] .. offsets[groups] - 1
     int groups;
     uint16_t* dst;             // or NULL
@@ -485,6 +485,8 @@ struct RowsCombineBwd {
 };
 void launch_rows_combine_bwd(const RowsCombineBwd& a, hipStream_t stream);
 
+// x [rows][cols] -> codes, scales [blk_count(cols)][rows]
+void launch_block_quant(const uint16_t* x, int64_t rows, int cols, uint8_t* codes, float* scales, hipStream_t stream);
 // src [groups][n][k] ([groups][k][n] transposed) -> codes [groups][n][k], scales [groups][n / 128][k / 128]
 void launch_block_quant_weights(const uint16_t* src, int groups, int n, int k, int transposed, uint8_t* codes,
                                 float* scales, hipStream_t stream);

@@ -12,6 +12,8 @@
 //
 // A thread holds vectors of eight consecutive values (16 bytes of bf16); a block of
 // 128 that gets one scale is 16 neighbouring lanes.
+#include <algorithm>
+
 #include "block8.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
@@ -65,12 +67,11 @@ __device__ __forceinline__ T ld_uniform(const T* p) {
 }
 
 // ---------------------------------------------------------------------------
-// Dispatch, and the quantiser (a dispatch of every row to itself)
+// Dispatch
 // ---------------------------------------------------------------------------
 
 // Measured: 16384 tokens of 7168 to 8 rows each 405 us (5.2 TB/s, mostly writes), as codes
-// 299 us (3.9 TB/s: scales of neighbouring rows are written by different XCDs); the quantiser
-// of 131072 rows of 7168 505 us (5.6 TB/s).
+// 299 us (3.9 TB/s: scales of neighbouring rows are written by different XCDs).
 //
 // A workgroup takes kRowThreads >> log tokens at a time.  A thread has eight
 // consecutive values, or with codes sixteen, which leave as 16 bytes; a block's eight
@@ -170,6 +171,61 @@ void launch_rows_dispatch(const RowsDispatch& a, hipStream_t stream) {
     }
 #undef ROWS_DISPATCH2
 #undef ROWS_DISPATCH
+}
+
+// ---------------------------------------------------------------------------
+// The quantiser of rows
+// ---------------------------------------------------------------------------
+
+// A workgroup takes kC blocks next to each other of 32 / kC rows, eight lanes to a block and
+// sixteen values to a lane, so that no width leaves lanes idle but in its last blocks, and the
+// scales of neighbouring rows are written together.  Four blocks where they divide the row, one
+// where it has just one, else two.  (us, kC of 1, 2, 4 and, before, a workgroup to a row:
+// 131072 x 7168 547, 503, 488 (5.8 TB/s), 504; 8191 x 4112 25.4, 21.5, 23.4, 22.3; 24576 x 2048
+// 26.0, 25.5, 26.2, 29.3; 64 x 7168 3.4, 3.4, 3.4, 4.0; 80000 x 128 6.8, 7.5, 10.9, 8.7.)
+template <int kC, bool kStream>
+__global__ __launch_bounds__(kRowThreads) void block_quant_kernel(const uint16_t* x, int64_t rows, int cols,
+                                                                  uint8_t* codes, float* scales) {
+    constexpr int kR = kRowThreads / 8 / kC;
+    const int lid = threadIdx.x & 7, kb = blockIdx.x * kC + (threadIdx.x >> 3) % kC;
+    const int col = kb * kBlk + lid * 16;
+    if (kb * kBlk >= cols) return;  // a whole block; no barrier follows
+    for (int64_t r = (int64_t)blockIdx.y * kR + (threadIdx.x >> 3) / kC; r < rows; r += (int64_t)gridDim.y * kR) {
+        const int64_t at = r * cols + col;
+        float v[2][8] = {};  // past the row's end: zeros
+        if (col < cols) {
+            unpack_bf16x8(ld_row<kStream>(x + at), v[0]);
+            unpack_bf16x8(ld_row<kStream>(x + at + 8), v[1]);
+        }
+        float m = fmaxf(abs_max8(v[0]), abs_max8(v[1]));
+#pragma unroll
+        for (int s = 1; s < 8; s *= 2) m = fmaxf(m, __shfl_xor(m, s, kWave));
+        const int e = blk_exp(m);
+        if (lid == 0) scales[(int64_t)kb * rows + r] = pow2f(e);
+        if (col < cols) {
+            const uint64_t lo = blk_codes8(v[0], e), hi = blk_codes8(v[1], e);
+            st_row<kStream>(codes + at, intx4{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi,
+                                              (int)(uint32_t)(hi >> 32)});
+        }
+    }
+}
+
+template <int kC>
+static void launch_block_quant(const uint16_t* x, int64_t rows, int cols, uint8_t* codes, float* scales,
+                               hipStream_t stream) {
+    constexpr int kR = kRowThreads / 8 / kC;
+    const dim3 grid((blk_count(cols) + kC - 1) / kC, (unsigned)std::min<int64_t>((rows + kR - 1) / kR, 65535));
+    if (streams(rows, 2ll * cols))
+        hipLaunchKernelGGL((block_quant_kernel<kC, true>), grid, dim3(kRowThreads), 0, stream, x, rows, cols, codes, scales);
+    else
+        hipLaunchKernelGGL((block_quant_kernel<kC, false>), grid, dim3(kRowThreads), 0, stream, x, rows, cols, codes, scales);
+}
+
+void launch_block_quant(const uint16_t* x, int64_t rows, int cols, uint8_t* codes, float* scales, hipStream_t stream) {
+    const int nb = blk_count(cols);
+    if (nb == 1) launch_block_quant<1>(x, rows, cols, codes, scales, stream);
+    else if (nb % 4 == 0) launch_block_quant<4>(x, rows, cols, codes, scales, stream);
+    else launch_block_quant<2>(x, rows, cols, codes, scales, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -220,6 +220,22 @@ def test_quantize_weights_bit_for_bit(gpu_lib, groups, n, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(530001, 512), (1050003, 272), (2100001, 128)])
+def test_quantize_many_rows(gpu_lib, rows, cols):
+    """More rows than the grid has, past the last cache: as in pieces."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    v = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    nb, step = (cols + 127) // 128, 1 << 16
+    q, s = torch.empty(rows, cols, dtype=torch.uint8, device="cuda"), torch.empty(nb, rows, device="cuda")
+    moe.moe_block_quantize(v, q, s)
+    for lo in range(0, rows, step):
+        part = v[lo:lo + step]
+        pq, ps = torch.empty_like(part, dtype=torch.uint8), torch.empty(nb, len(part), device="cuda")
+        moe.moe_block_quantize(part, pq, ps)
+        assert torch.equal(pq, q[lo:lo + step]) and torch.equal(ps, s[:, lo:lo + step])
+
+
+@pytest.mark.gpu
 def test_dequantize_past_32_bits(gpu_lib):
     """Values past 2^32 bytes, as rows and as matrices (one scale each for all blocks but the last row's)."""
     cols, n = 4112, 1024
