@@ -12,6 +12,7 @@ from __future__ import annotations
 import array
 import ctypes
 import dataclasses
+import operator
 import os
 
 from .build import lib_path
@@ -236,6 +237,7 @@ def moe_mx_quantize(src, codes, scales, stream=None):
                                                       _stream(stream)))
 
 
+_dtype = operator.attrgetter("dtype")
 torch = None  # until a call is given tensors: building, sizing and validating need none
 
 
@@ -512,13 +514,13 @@ def moe_query_grad_norm(tensors) -> int:
 
 def _grad_arrays(fn, dev, grads):
     """Arrays of the tensors' pointers, element counts and types (1: bf16), as the C calls read them."""
-    if not all(_is_contiguous(t) and _get_device(t) == dev for t in grads):
+    if not all(map(_is_contiguous, grads)) or set(map(_get_device, grads)) - {dev}:
         raise MoeError(fn, MOE_E_INVALID)
     try:
-        kinds = bytes([_GRAD_KINDS[t.dtype] for t in grads])
+        kinds = bytes(map(_GRAD_KINDS.__getitem__, map(_dtype, grads)))
     except KeyError:
         raise MoeError(fn, MOE_E_INVALID) from None
-    return array.array("Q", [_data_ptr(t) for t in grads]), array.array("q", [_numel(t) for t in grads]), kinds
+    return array.array("Q", list(map(_data_ptr, grads))), array.array("q", list(map(_numel, grads))), kinds
 
 
 def _address(a):
