@@ -814,7 +814,7 @@ enum BlockForm { kFormFew, kForm256x256, kForm128x256, kForm128x128, kForm64x256
 
 // Groups with rows, routed evenly.
 static double active_groups(int64_t rows, int groups) {
-    return std::min((double)rows, groups * (1.0 - exp(-(double)rows / groups)));
+    return groups * (1.0 - pow(1.0 - 1.0 / groups, (double)rows));
 }
 
 // Whether the weights' loads leave the caches alone: more than the last cache's 256 MB of them,
@@ -919,7 +919,7 @@ void launch_block_gemm(const BlockGemm& a, hipStream_t stream) {
             else launch_block_gemm_tiles<Bg128x256, false>(a, stream);
             return;
         case kForm128x128: launch_block_gemm_tiles<Bg128x128, false>(a, stream); return;
-        case kForm64x256:  // the only tiles that few rows to a group fall to
+        case kForm64x256:  // (few rows to a group and many weights fall to other tiles at a few sizes only)
             if (glu && past) launch_block_gemm_tiles<Bg64x256, true, true>(a, stream);
             else if (glu) launch_block_gemm_tiles<Bg64x256, true>(a, stream);
             else if (past) launch_block_gemm_tiles<Bg64x256, false, true>(a, stream);
