@@ -827,46 +827,69 @@ static bool weights_past_caches(const BlockGemm& a) {
     return a.rows <= active * (kBfRows / 2) && active * a.n * a.k * (a.wu ? 2 : 1) > 256.0 * (1 << 20);
 }
 
-// The form with the least expected time, in us.  A tile takes a block of K in `low` us
-// where it is one of few and in `full` us where every CU has one, and `end` us for its
-// epilogue (fitted to products of [4096, 4096] and [4096, 1024] with 256 to 16384 rows);
-// tiles run in rounds of one to a CU, and no faster than they read the weights.  Larger
-// tiles need less of everything for each element, smaller ones fill the CUs sooner and pad a
-// group's rows less.  The few-row form needs more the more fragments of 16 rows a part has;
-// past 64 groups a workgroup takes longer to find its part.  Measured, us, tiles of 256 x 256,
-// 128 x 256, 128 x 128, 64 x 256 and the few-row form (-: not timed):
+// Parts of at most m rows, routed evenly: the sum over groups of the expected ceil(rows / m),
+// that is the chance of more than j m rows over all j, a group's rows being normal about their
+// mean with its root as deviation.
+static double expected_parts(int64_t rows, int groups, int m) {
+    if (groups == 1) return (double)((rows + m - 1) / m);
+    const double mean = (double)rows / groups, dev = sqrt(mean);
+    if (2 * dev > m) return groups * (mean / m + 0.5);
+    double sum = active_groups(rows, groups);
+    int64_t j = std::max<int64_t>(1, (int64_t)ceil((mean - 4 * dev) / m));
+    sum += (double)groups * (j - 1);
+    for (; j * m < mean + 4 * dev; ++j) sum += groups * 0.5 * erfc((j * m + 0.5 - mean) / (sqrt(2.0) * dev));
+    return sum;
+}
+
+// The form with the least expected time, in us.  A tile takes a block of K in `low` us where
+// it is one of few and in `full` us where every CU has one, and `end` us for its epilogue;
+// tiles run in rounds of one to a CU, while codes are read at `rate` TB/s.  Larger tiles need
+// less of everything for each element, smaller ones fill the CUs sooner and pad a group's rows
+// less.  The few-row form needs more the more fragments of 16 rows a part has; past 64 groups a
+// workgroup takes longer to find its part.  The constants are fitted to 1200 shapes, 1 to
+// 32768 rows, 1 to 256 groups, n up to 7168 and k of 416 to 7168, drawn evenly on
+// logarithmic scales, and those below, each timed in every form.  On 400 others the chosen
+// form is 1.5 % slower than the best one on average, and more than 10 % slower for 3 in 100.
+// Measured, us, tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 256 and the few-row form (-: not
+// timed):
 //   1 row x [2048, 1024]       -, -, 8.2, 9.2, 3.7;   64 rows x [4096, 4096]  -, -, 21, 26, 12
 //   256 rows x [4096, 4096]    43, 31, 22, 27, 39;    2048 rows               48, 40, 48, 56, 268
 //   4096 rows                  61, 78, 91, 104, 531;  16384 rows              234, 299, 344, 394, -
 //   16 groups of [4096, 4096]  32 rows -, -, 63, 66, 49;  128 rows            -, -, 67, 69, 53
 //   32 groups of [7168, 2048]  64 rows -, -, 85, 77, 71;  512 rows            -, -, 98, 85, 87
-//   1024 rows                  112, 103, 100, 96, 116;    8192 rows           186, 196, 216, 226, 957
+//   1024 rows                  112, 103, 100, 96, 116;    2048 rows           125, 113, 108, 113, -
+//   3000 rows                  123, 117, 114, 120, -;     8192 rows           186, 196, 216, 226, 957
 //   131072 rows                1798, 2272, 2574, 2912, 14243
 //   SwiGLU, [2048, 7168]       64 rows -, -, -, 134, 132; 512 rows            -, -, -, 142, 160
+//   1500 rows                  206, 179, -, 163, 211;     2048 rows           208, 191, -, 181, -
 //   256 groups of [512, 1024]  512 rows -, -, 32, 27, 31; SwiGLU              -, -, -, 50, 58
 static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
     const double r = (double)rows, kb = blk_count(k), active = active_groups(rows, groups);
-    auto parts = [&](int m) {  // of m rows: half a part of padding to a group
-        return groups == 1 ? ceil(r / m) : std::max(active, r / m + active / 2);
-    };
     const double per_group = r / active, wide = glu ? 2 : 1;
-    const double strips = ((n + 15) / 16) * parts(kBfRows) / 256;
-    const double busy = per_group <= (groups == 1 ? 16 : 10) ? 1 : per_group <= 16 ? 1.2 : per_group <= 32 ? 1.5 : 3;
+    const double strips = ((n + 15) / 16) * expected_parts(rows, groups, kBfRows) / 256;
+    double busy = per_group <= 16 ? 1 : per_group <= 32 ? 1.65 : 2.55;
+    if (groups > 1) {  // rows differ from group to group: 1 to 8 rows, 1.2 at 16, 1.65 at 32, 2.55 from 64 on
+        const double at = log2(std::min(std::max(per_group, 8.0), 64.0)) - 3;
+        busy = at <= 1 ? 1 + 0.2 * at : at <= 2 ? 1.2 + 0.45 * (at - 1) : 1.65 + 0.9 * (at - 2);
+    }
     BlockForm best = kFormFew;
-    double least = 3.5 + wide * std::max(kb * 0.14 * std::min(busy, 2.0),
-                                         strips * busy * (kb * 0.09 + (groups > kWave ? 0.3 : 0.05)));
+    double least = 4.2 + (glu ? 2.2 : 1) * std::max(kb * 0.075 * std::min(busy, 2.0),
+                                                    strips * busy * (kb * 0.08 + (groups > kWave ? 0.32 : 0.19)));
     if (groups > kBgGroups) return best;
-    const double weights = wide * active * n * k / 5.4e6;  // read at 5.4 TB/s
-    const struct { BlockForm form; int m, n, stages; double low, full, end; } tiles[] = {
-        {kForm256x256, 256, 256, Bg256x256::kS, 1.155, 1.66, 4.2}, {kForm128x256, 128, 256, Bg128x256::kS, 0.81, 1.08, 2.6},
-        {kForm128x128, 128, 128, Bg128x128::kS, 0.564, 0.62, 1.5}, {kForm64x256, 64, 256, Bg64x256::kS, 0.703, 0.72, 1.5}};
+    const double bytes = wide * active * n * k + r * k;
+    const struct { BlockForm form; int m, n, stages; double low, full, end, rate; } tiles[] = {
+        {kForm256x256, 256, 256, Bg256x256::kS, 1.5, 1.63, 3.6, 5.0},
+        {kForm128x256, 128, 256, Bg128x256::kS, 0.9, 1.08, 2.7, 4.8},
+        {kForm128x128, 128, 128, Bg128x128::kS, 0.63, 0.68, 1.4, 5.2},
+        {kForm64x256, 64, 256, Bg64x256::kS, 0.735, 0.965, 2.05, 5.5}};
     for (const auto& t : tiles) {
         if (kb < t.stages || (glu && t.n != 256)) continue;  // a block of h is half of 256 columns
         const int cols = glu ? t.n / 2 : t.n;
-        const double rounds = parts(t.m) * ((n + cols - 1) / cols) / 256;
-        const double run = (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds) *
+        const double rounds = expected_parts(rows, groups, t.m) * ((n + cols - 1) / cols) / 256;
+        const double run = (rounds <= 1 ? 1 : rounds <= 3 ? ceil(rounds) : rounds + 0.25) *
                            (kb * (rounds <= 1 ? t.low : t.full) + t.end);
-        const double us = 2.5 + std::max(run, weights) + std::min(run, weights) / 10;
+        const double read = bytes / (t.rate * 1e6);
+        const double us = 3.2 + std::max(run, read) + 0.2 * std::min(run, read);
         if (us < least) {
             least = us;
             best = t.form;

@@ -458,7 +458,7 @@ def test_swiglu_product(gpu_lib, counts, n, k):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("glu", [False, True])
-@pytest.mark.parametrize("counts", [[1, 0, 2, 1] * 10, [0, 16, 3, 37, 8] * 8, [2, 0, 1] * 200], ids=_name)
+@pytest.mark.parametrize("counts", [[1, 0, 2, 1] * 10, [0, 16, 3, 37, 8] * 8, [25, 20, 30, 40, 0] * 8, [2, 0, 1] * 200], ids=_name)
 def test_weights_past_the_last_cache(gpu_lib, counts, glu):
     """More than 2^28 bytes of weights for few rows to a group, in every form they fall to: whole numbers, exact sums."""
     groups, spare = len(counts), 2
