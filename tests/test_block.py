@@ -631,6 +631,41 @@ def test_captured_and_on_another_stream(gpu_lib):
 
 
 @pytest.mark.gpu
+def test_two_calls_at_once(gpu_lib):
+    """Products of both kinds on two streams, a workspace each, while the other's run: as alone."""
+    g = torch.Generator().manual_seed(31)
+    jobs = []
+    for rows, groups, n, k in ((3000, 5, 1040, 528), (90, 12, 528, 1040)):
+        counts = _uneven(rows, groups)
+        rows = sum(counts)
+        a, sa, wg, sg = _operands(g, rows, k, groups, n)
+        _, _, wu, su = _operands(g, 1, k, groups, n)
+        off = _offsets(counts).cuda()
+        a, wg, wu, sa, sg, su = u8(a), u8(wg), u8(wu), sa.cuda(), sg.cuda() / 1e5, su.cuda() / 1e5
+        out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+        hq, hs = torch.empty(rows, n, dtype=torch.uint8, device="cuda"), torch.empty((n + 127) // 128, rows, device="cuda")
+        ws = torch.empty(moe.moe_query_block_swiglu(rows, n, k, groups), dtype=torch.uint8, device="cuda")
+
+        def run(stream, a=a, sa=sa, wg=wg, sg=sg, wu=wu, su=su, out=out, hq=hq, hs=hs, ws=ws, off=off):
+            moe.moe_block_gemm(a, sa, wg, sg, out, offsets=off, stream=stream)
+            moe.moe_block_gemm_swiglu(a, sa, wg, sg, wu, su, hq, hs, ws, offsets=off, stream=stream)
+
+        run(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        jobs.append((run, (out, hq, hs), [t.clone() for t in (out, hq, hs)], torch.cuda.Stream()))
+    for _, outs, _, _ in jobs:
+        for t in outs:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for run, _, _, stream in jobs:
+            run(stream)
+    torch.cuda.synchronize()
+    for _, outs, alone, _ in jobs:
+        assert all(torch.equal(x, y) for x, y in zip(outs, alone))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H,I,E,k", [(1, 128, 64, 8, 2), (9, 256, 144, 5, 3), (200, 384, 256, 4, 2)])
 def test_the_layer_in_parts(gpu_lib, T, H, I, E, k):
     """Router, layout, rows of codes, both products and the weighted sum in a row, as a server runs them,
