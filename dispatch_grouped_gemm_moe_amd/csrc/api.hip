@@ -350,12 +350,12 @@ moe_status scratch_address(void** out) {
 
 // The device status word (two ints at the start of a workspace): cleared by a
 // kernel (not a memset, so that a captured call records no memset node), and
-// copied out to the caller's buffer after the forward.
+// copied out to the caller's buffer, the record as its wait site, after the forward.
 __global__ void status_clear_kernel(int32_t* word) {
     if (threadIdx.x < 2) word[threadIdx.x] = 0;
 }
 __global__ void status_copy_kernel(const int32_t* word, int32_t* dst) {
-    if (threadIdx.x < 2) dst[threadIdx.x] = word[threadIdx.x];
+    if (threadIdx.x < 2) dst[threadIdx.x] = threadIdx.x ? wait_site(word[1]) : word[0];
 }
 
 }  // namespace
@@ -913,7 +913,7 @@ moe_status moe_read_device_status(void* ws, void* stream, int32_t* code, int32_t
     int32_t h[2] = {0, 0};
     if (hipMemcpy(h, ws, sizeof(h), hipMemcpyDeviceToHost) != hipSuccess) return MOE_E_HIP;
     *code = h[0];
-    *detail = h[1];
+    *detail = wait_site(h[1]);
     if (h[0] != 0) {
         const int32_t z[2] = {0, 0};
         if (hipMemcpy(ws, z, sizeof(z), hipMemcpyHostToDevice) != hipSuccess) return MOE_E_HIP;

@@ -137,6 +137,13 @@ void launch_mx_quant(const uint16_t* src, int64_t rows, int cols, int layout, ui
 // down and combine progress, then the launch's abort word; zeroed by
 // launch_mega).  Wait sites recorded in the status detail: 0 ring slot (down),
 // 1 ring slot (combine), 2 combine input, 3 down input.
+// The status word holds a code and the largest wait_record of the waits that
+// ended in vain.
+constexpr int kWaitSiteBits = 2;
+__host__ __device__ __forceinline__ int wait_record(int phase, int site) {  // the earlier the phase, the larger
+    return (((1 << 29) - 1 - phase) << kWaitSiteBits) | site;
+}
+__host__ __device__ __forceinline__ int wait_site(int record) { return record & ((1 << kWaitSiteBits) - 1); }
 struct MegaArgs {
     int T, H, I, k, Mb, nmb, S, comm, e_end, with_shared, ld_tok_prow, mx;
     int e_mx;  // experts [0, e_mx) run MXFP8 tiles (m1/m2), the rest (the shared expert) bf16 (g1/g2)

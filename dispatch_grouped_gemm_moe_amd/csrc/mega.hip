@@ -41,8 +41,8 @@
 // (L2 write-back) on the counter; consumers poll the counter with relaxed
 // agent-scope loads and take one agent-scope acquire (L2 invalidate) when it
 // reaches the target, before reading.  Every wait is bounded in
-// wall-clock time: on expiry the workgroup records MOE_DEV_WAIT_TIMEOUT in the
-// device status word and every workgroup leaves.
+// wall-clock time: on expiry the workgroups that wait record MOE_DEV_WAIT_TIMEOUT
+// in the device status word and every workgroup leaves.
 #include "common.hpp"
 #include "gemm_tile.hpp"
 #include "kernels.hpp"
@@ -94,12 +94,17 @@ __device__ __forceinline__ uint64_t now_ticks() { return __builtin_amdgcn_s_memr
 // Thread 0 waits until *ctr >= target (agent-scope acquire), then the whole
 // workgroup continues.  Returns false if this launch is being abandoned (this
 // wait expired, or another workgroup's did: the launch's abort word, zeroed
-// with the counters, is set).  An expiry is also recorded in the device status
-// word (first expiry wins; it stays until moe_read_device_status reads it).
+// with the counters, is set).  Every wait that ends so is recorded in the device
+// status word, where the one for the earliest phase stays until
+// moe_read_device_status reads it.  phase = 3 j + (0 gate|up, 1 down, 2 combine)
+// of the phase waited for: a phase depends on phases of lower numbers only, so
+// the lowest one is what stopped the others.  (Which wait expires first says
+// nothing: a workgroup without down tiles waits for the down counter from the
+// moment at which the others wait for gate|up.)
 // acquire = false serves waits that only order this workgroup's later stores
 // after other workgroups' completed reads (a ring slot becoming free): no data
 // is read, so the L2 is left as it is.
-__device__ bool wait_counter(const MegaArgs& a, int* ctr, int target, int site, int* s_flag, bool acquire) {
+__device__ bool wait_counter(const MegaArgs& a, int* ctr, int target, int phase, int site, int* s_flag, bool acquire) {
     if (threadIdx.x == 0) {
         int ok = 1;
         int* abort_word = a.counters + 3 * a.nmb;
@@ -108,13 +113,12 @@ __device__ bool wait_counter(const MegaArgs& a, int* ctr, int target, int site, 
         // L2) and acquire once at the end: an acquire per poll would invalidate
         // the XCD's L2 on every iteration, under every GEMM tile running there.
         while (__hip_atomic_load(ctr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < target) {
-            if (__hip_atomic_load(abort_word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0) { ok = 0; break; }
-            if (now_ticks() - t0 > a.spin_ticks) {
+            if (__hip_atomic_load(abort_word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0 ||
+                now_ticks() - t0 > a.spin_ticks) {
                 __hip_atomic_store(abort_word, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                int expected = 0;
-                if (__hip_atomic_compare_exchange_strong(a.status, &expected, (int)MOE_DEV_WAIT_TIMEOUT,
-                                                         __ATOMIC_RELAXED, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-                    __hip_atomic_store(a.status + 1, site, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_fetch_max(a.status + 1, wait_record(phase, site), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(a.status, (int)MOE_DEV_WAIT_TIMEOUT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 ok = 0;
                 break;
             }
@@ -241,7 +245,7 @@ void mega_kernel(MegaArgs a) {
         // ---- combine workers: group by group, each minibatch's tokens split in
         // contiguous chunks
         for (int j = 0; j < ng; ++j) {
-            if (!wait_counter(a, d_done + j, G, 2, &s_flag, true)) return;
+            if (!wait_counter(a, d_done + j, G, 3 * j + 1, 2, &s_flag, true)) return;
             for (int b = j * a.group; b < min(a.nmb, (j + 1) * a.group); ++b) {
                 const int Tm = tokens_of(a, b);
                 const int chunk = ceil_div(Tm, a.comm);
@@ -291,11 +295,11 @@ void mega_kernel(MegaArgs a) {
         const int b0 = j * a.group, b1 = min(a.nmb, b0 + a.group);
         if (!ready) {
             if (kind == kGateUp && j >= Sg) {  // the group's ring slots free again
-                if (!wait_counter(a, d_done + (j - Sg), G, 0, &s_flag, false)) return;
-                if (y_in_ring && !wait_counter(a, comb_done + (j - Sg), comb_target, 1, &s_flag, false)) return;
+                if (!wait_counter(a, d_done + (j - Sg), G, 3 * (j - Sg) + 1, 0, &s_flag, false)) return;
+                if (y_in_ring && !wait_counter(a, comb_done + (j - Sg), comb_target, 3 * (j - Sg) + 2, 1, &s_flag, false)) return;
             }
-            if (kind == kDown && !wait_counter(a, gu_done + j, G, 3, &s_flag, true)) return;
-            if (kind == kCombine && !wait_counter(a, d_done + j, G, 2, &s_flag, true)) return;
+            if (kind == kDown && !wait_counter(a, gu_done + j, G, 3 * j, 3, &s_flag, true)) return;
+            if (kind == kCombine && !wait_counter(a, d_done + j, G, 3 * j + 1, 2, &s_flag, true)) return;
             ready = true;
         }
         int lv = (int)(v - qstart);

@@ -70,7 +70,7 @@ enum moe_flags {
        workgroup 0 never signals that it has finished the first gate|up phase.
        The waits on that phase then run into their bound (2 s), the launch
        drains, the device status word records MOE_DEV_WAIT_TIMEOUT with the wait
-       site as detail, and `out` is unspecified.  No effect on a forward that
+       site as detail (3: a wait of a down tile), and `out` is unspecified.  No effect on a forward that
        runs one launch per GEMM. */
     MOE_F_DEBUG_DROP_SIGNAL = 1u << 3,
     /* MOE_PREC_MXFP8 only (MOE_E_INVALID otherwise): the routed experts'
@@ -297,7 +297,10 @@ moe_status moe_layer_bwd(const moe_cfg *cfg, const moe_weights *w, const uint16_
  */
 typedef enum moe_device_error {
     MOE_DEV_OK = 0,
-    MOE_DEV_WAIT_TIMEOUT = 1 /* a bounded device-side wait expired; detail = wait site */
+    /* a bounded device-side wait expired; detail = wait site, of all waits that
+       ended with it that on the earliest phase: 0 a ring slot that down still
+       reads, 1 one that combine still reads, 2 combine's input, 3 down's input */
+    MOE_DEV_WAIT_TIMEOUT = 1
 } moe_device_error;
 
 moe_status moe_read_device_status(void *ws, void *stream, int32_t *code, int32_t *detail);

@@ -130,3 +130,23 @@ def test_dropped_signal_expires_the_bounded_wait_then_next_forward_is_clean(gpu_
     assert layer.device_status() == (moe.MOE_OK, 0, 0)
     err = O.rel_inf_err(layer.out.float().cpu().numpy(), O.layer_forward(inp)["out"])
     assert err <= TOL["bf16"], err
+
+
+@pytest.mark.parametrize("w,slots,comm", [
+    # combine workgroups wait for the down counter from the launch's start, before any down tile waits
+    (_wl("lk_watchdog_comm8", T=1100, H=256, I=192, E=6, k=3, minibatch=128), 2, 8),
+    # few tiles: most workgroups own none of a phase and wait for a later one at once
+    (_wl("lk_watchdog_few_tiles", T=600, H=128, I=64, E=4, k=1, minibatch=64), 3, 0),
+    (_wl("lk_watchdog_mx", T=1200, H=512, I=256, E=4, k=2, minibatch=128, prec="mxfp8"), 4, 0)], ids=lambda v: getattr(v, "name", str(v)))
+def test_the_status_names_the_phase_that_stopped_the_others(gpu_lib, w, slots, comm):
+    """Whichever of the waits expires first, the reported site is that of the waits on the phase that was never
+    signalled (3: down tiles, for gate|up), not of those that wait for it in turn."""
+    from gpu_harness import Layer
+    layer = Layer(make_inputs(w), flags=moe.MOE_F_DEBUG_DROP_SIGNAL, ring_slots=slots, comm_cus=comm)
+    for _ in range(2):
+        print("%s: forward with a dropped signal (waits expire after 2 s)" % w.name, flush=True)
+        assert layer.forward_path(keep=False) == LK
+        assert layer.device_status() == (moe.MOE_E_DEVICE, moe.MOE_DEV_WAIT_TIMEOUT, 3)
+    layer.cfg.flags &= ~moe.MOE_F_DEBUG_DROP_SIGNAL
+    assert layer.forward_path(keep=False) == LK
+    assert layer.device_status() == (moe.MOE_OK, 0, 0)
