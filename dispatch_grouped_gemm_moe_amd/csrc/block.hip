@@ -382,10 +382,10 @@ __device__ __forceinline__ void lds_put_get(uint32_t at0, uint32_t at1, u32x4& d
 
 // A store that leaves the caches alone (in asm: two branches that store the same value to
 // the same place, with and without the hint, become one store without it).  The s_nop is the
-// wait state that a wide store needs before a VALU instruction may write its data registers,
-// which the compiler keeps only after stores of its own.
+// two wait states that a store of more than 8 bytes needs on gfx950 before a VALU instruction
+// may write its data registers, which the compiler keeps only after stores of its own.
 __device__ __forceinline__ void store_past(uint16_t* at, u32x4 v) {
-    asm volatile("global_store_dwordx4 %0, %1, off nt\n\ts_nop 0" ::"v"(at), "v"(v) : "memory");
+    asm volatile("global_store_dwordx4 %0, %1, off nt\n\ts_nop 1" ::"v"(at), "v"(v) : "memory");
 }
 
 template <class C, bool kGlu, bool kPast>
