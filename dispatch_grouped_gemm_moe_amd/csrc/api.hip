@@ -1105,8 +1105,8 @@ moe_status moe_query_block_swiglu(int64_t rows, int32_t n, int32_t k, int32_t gr
     if (!workspace) return MOE_E_INVALID;
     moe_status st = check_block(rows, n, k, groups, 16);
     if (st != MOE_OK) return st;
-    // the small tiles' h in fp32; the large ones quantise it themselves
-    *workspace = block_gemm_large(rows, n, k, groups) ? kAlign : align_up((size_t)rows * n * 4);
+    // the small tiles' h in fp32, for these rows or fewer; the large ones quantise it themselves
+    *workspace = align_up((size_t)block_few_rows(rows, n, k, groups) * n * 4);
     return MOE_OK;
 }
 

@@ -843,6 +843,16 @@ static double expected_parts(int64_t rows, int groups, int m) {
     return sum;
 }
 
+// Most of up to `rows` rows whose SwiGLU product may fall to the few-row form, which leaves h in
+// fp32 in the caller's workspace: no more for fewer rows, so that a workspace for many serves
+// fewer.  All of them where no tile fits, and for narrow outputs, whose h is small beside the
+// rows; else a bound that lies above every choice (of 10^6 shapes drawn on logarithmic scales
+// the times below would choose it for 3612 rows, or 53 rows to a group, at most).
+int64_t block_few_rows(int64_t rows, int n, int k, int groups) {
+    if (groups > kBgGroups || n < kBlk || blk_count(k) < Bg128x256::kS) return rows;
+    return std::min<int64_t>(rows, std::max(4096, kBfRows * groups));
+}
+
 // The form with the least expected time, in us.  A tile takes a block of K in `low` us where
 // it is one of few and in `full` us where every CU has one, and `end` us for its epilogue;
 // tiles run in rounds of one to a CU, while codes are read at `rate` TB/s.  Larger tiles need
@@ -878,6 +888,7 @@ static BlockForm block_form(int64_t rows, int n, int k, int groups, bool glu) {
     double least = 4.2 + (glu ? 2.2 : 1) * std::max(kb * 0.075 * std::min(busy, 2.0),
                                                     strips * busy * (kb * 0.08 + (groups > kWave ? 0.32 : 0.19)));
     if (groups > kBgGroups) return best;
+    if (glu && rows > block_few_rows(rows, n, k, groups)) least = INFINITY;
     const double bytes = wide * active * n * k + r * k;
     const struct { BlockForm form; int m, n, stages; double low, full, end, rate; } tiles[] = {
         {kForm256x256, 256, 256, Bg256x256::kS, 1.5, 1.63, 3.6, 5.0},

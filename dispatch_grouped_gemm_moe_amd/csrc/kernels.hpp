@@ -540,6 +540,8 @@ struct BlockGemm {
 };
 // Whether a product runs in the large tiles, which write h's codes themselves.
 bool block_gemm_large(int64_t rows, int n, int k, int groups);
+// Most rows, of up to `rows`, with which it runs in the small ones.
+int64_t block_few_rows(int64_t rows, int n, int k, int groups);
 void launch_block_gemm(const BlockGemm& a, hipStream_t stream);
 
 }  // namespace moe

@@ -520,8 +520,9 @@ moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uin
  *       product takes it, quantised from fp32 by the rule above;
  *   h bf16 [rows, n], or NULL: h itself as well;
  *   ws: moe_query_block_swiglu bytes (host-only query; its refusals of sizes are
- *       those below), 16-byte aligned, of any content; calls that overlap on two
- *       streams take one each.
+ *       those below; what it answers for some rows is enough for fewer rows of the
+ *       same n, k and groups), 16-byte aligned, of any content; calls that overlap
+ *       on two streams take one each.
  * The product of a gradient is the same call: dA = dOut W takes dOut's codes and the
  * turned weights.  Each block's products are summed by the matrix instruction (which
  * cuts off what lies below 2^-13 of the largest of eight neighbouring products),

@@ -71,6 +71,19 @@ def test_swiglu_workspace():
         assert e.value.status == want
 
 
+@pytest.mark.parametrize("n,k,groups", [(1024, 2048, 64), (2048, 7168, 32), (16, 13296, 26), (32, 3264, 1), (128, 128, 5),
+                                        (144, 272, 256), (2048, 512, 600), (4096, 4096, 1), (528, 1040, 512)])
+def test_a_swiglu_workspace_serves_fewer_rows(n, k, groups):
+    """Sized once for the most rows of a batch: no smaller batch needs more."""
+    most = 0
+    for rows in sorted({int(1.05 ** i) for i in range(300)} | {4095, 4096, 4097, 24576, 131072, 1 << 24}):
+        if rows > 1 << 24:
+            break
+        need = moe.moe_query_block_swiglu(rows, n, k, groups)
+        assert need >= most, rows
+        most = need
+
+
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=0), 1), (dict(cols=24), 1), (dict(cols=0), 1), (dict(src=None), 1), (dict(q=None), 1),
     (dict(s=None), 1), (dict(src=FAKE + 8), 1), (dict(q=FAKE + 8), 1), (dict(s=FAKE + 2), 1),
@@ -454,6 +467,31 @@ def test_swiglu_product(gpu_lib, counts, n, k):
         assert (torch.frexp(hs[b, :m])[0] == 0.5).all()
         assert (amax <= 448 * hs[b, :m].double() * (1 + HALF)).all()
         assert ((amax >= 224 * hs[b, :m].double() * (1 - HALF)) | (hs[b, :m] <= 2.0 ** -126)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,k,groups", [(1024, 2048, 6), (144, 656, 20)])
+def test_swiglu_workspace_of_the_largest_batch(gpu_lib, n, k, groups):
+    """Batches of 12000 rows and fewer, in tiles and in the few-row form, in one workspace sized for the largest:
+    the bits that each gives in its own, and nothing behind it."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    draw = lambda *shape: torch.randint(-2, 3, shape, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    wg, wu = draw(groups, n, k), draw(groups, n, k)
+    sw = torch.full((groups, (n + 127) // 128, (k + 127) // 128), 2.0 ** -8, device="cuda")
+    need = moe.moe_query_block_swiglu(12000, n, k, groups)
+    ws = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
+    for rows in (12000, 3000, 700, 64, 6, 1):
+        counts = _uneven(rows, groups)
+        rows = sum(counts) or 1
+        a, sa = draw(rows, k), torch.ones((k + 127) // 128, rows, device="cuda")
+        off = _offsets(counts if sum(counts) else [1] + [0] * (groups - 1)).cuda()
+        res = []
+        for buf in (ws[:need], torch.empty(moe.moe_query_block_swiglu(rows, n, k, groups), dtype=torch.uint8, device="cuda")):
+            hq, hs = torch.empty(rows, n, dtype=torch.uint8, device="cuda"), torch.empty((n + 127) // 128, rows, device="cuda")
+            moe.moe_block_gemm_swiglu(a, sa, wg, sw, wu, sw, hq, hs, buf, offsets=off)
+            res.append((hq, hs))
+        assert all(torch.equal(x, y) for x, y in zip(*res))
+        assert (ws[need:] == 77).all()
 
 
 @pytest.mark.gpu
