@@ -459,7 +459,7 @@ struct RowsDispatch {
     const uint16_t* x;         // [tokens][cols]
     const float* xf;           // or fp32 values in its place (codes, and dst in bf16 beside them)
     const int32_t* tok_row;    // [tokens][k]; NULL: token t is row t, k = 1 (with xf)
-    const int32_t* offsets;    // or NULL; else only tokens offsets[0] .. offsets[groups] - 1
+    const int32_t* offsets;    // or NULL; else only tokens offsets[0] .. the greater of the last two - 1
     int groups;
     uint16_t* dst;             // or NULL
     uint8_t* codes;            // [rows][cols] and their scales [blk_count(cols)][rows], or NULL

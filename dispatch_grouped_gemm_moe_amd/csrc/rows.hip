@@ -85,8 +85,10 @@ __global__ __launch_bounds__(kRowThreads) void rows_dispatch_kernel(RowsDispatch
     const int nv = a.cols / kVec;
     int64_t t_lo = 0, t_hi = a.tokens;
     if (a.offsets) {
+        // (a last bound below the one before it, as moe_dispatch_layout's error report: no row in
+        // the last group, as for the products)
         t_lo = max(a.offsets[0], 0);
-        t_hi = min((int64_t)a.offsets[a.groups], a.tokens);
+        t_hi = min((int64_t)max(a.offsets[a.groups - 1], a.offsets[a.groups]), a.tokens);
     }
     for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < t_hi; t0 += (int64_t)gridDim.x * per) {
         const int64_t t = t0 + sub;

@@ -602,6 +602,50 @@ def test_product_nan_codes_and_offsets_outside(gpu_lib):
         assert torch.equal(out.cpu(), want.float().bfloat16())
 
 
+BOUNDS = [([-5, 25, 40, 1 << 20], [(0, 25, 0), (25, 40, 1), (40, None, 2)]), ([0, 25, 30, -1], [(0, 25, 0), (25, 30, 1)]),
+          ([0, 1 << 30, 1 << 30, -1], [(0, None, 0)]), ([50000, 60000, 70000, 80000], []), ([0, 0, 0, -1], []),
+          ([7, 7, 30, 30], [(7, 30, 1)])]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,k,rows", [(144, 400, 60), (272, 144, 50), (1040, 528, 3000), (528, 656, 1200), (2064, 272, 9000)])
+@pytest.mark.parametrize("glu", [False, True])
+def test_bounds_outside_the_rows(gpu_lib, n, k, rows, glu):
+    """In the few-row form and in tiles: bounds are cut off, a last one of -1 names no row, other rows are left."""
+    g = torch.Generator().manual_seed(n + rows)
+    a, sa, w, sw = _operands(g, rows, k, 3, n, True)
+    sw = sw * 2.0 ** -8
+    a, sa, w, sw = a.cuda(), sa.cuda(), w.cuda(), sw.cuda()
+    av, wv = _values(a, sa, w, sw)
+    byte = lambda t: t.view(torch.uint8)
+    nb = (n + 127) // 128
+    ws = torch.empty(moe.moe_query_block_swiglu(rows, n, k, 3), dtype=torch.uint8, device="cuda") if glu else None
+    for bounds, live in BOUNDS:
+        off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        out = torch.full((rows + 1, n), 77, dtype=torch.bfloat16, device="cuda")
+        want = torch.full((rows + 1, n), 77.0, dtype=torch.float64, device="cuda")
+        named = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        for lo, hi, e in live:
+            hi = rows if hi is None else hi
+            want[lo:hi], named[lo:hi] = av[lo:hi] @ wv[e].t(), True
+        if not glu:
+            moe.moe_block_gemm(byte(a), sa, byte(w), sw, out[:-1], offsets=off)
+            assert torch.equal(out, want.float().bfloat16()), bounds
+            continue
+        hq = torch.full((rows, n), 77, dtype=torch.uint8, device="cuda")
+        hs = torch.full((nb, rows), 77.0, device="cuda")
+        moe.moe_block_gemm_swiglu(byte(a), sa, byte(w), sw, byte(w), sw, hq, hs, ws, h=out[:-1], offsets=off)
+        h = (want * want * torch.sigmoid(want))[:-1][named]
+        near = out[:-1][named].double()
+        # (a hardware exponential and reciprocal of a few 2^-24 of the value each, in front of the rounding)
+        assert ((near - h).abs() <= h.abs() * HALF * 1.01 + h.abs() * 2.0 ** -18).all(), bounds
+        s = hs.double().t().repeat_interleave(128, 1)[:, :n][named]
+        held = hq.view(torch.float8_e4m3fn).double()[named] * s
+        assert ((held - near).abs() <= near.abs() * (2.0 ** -4 + HALF) * 1.01 + s * 2.0 ** -10).all(), bounds
+        assert (out[:-1][~named] == 77).all() and (out[-1] == 77).all() and (hq[~named] == 77).all()
+        assert (hs[:, ~named] == 77).all()
+
+
 @pytest.mark.gpu
 def test_extreme_scales(gpu_lib):
     """Scales far apart whose products are normal numbers, and a result that overflows."""
