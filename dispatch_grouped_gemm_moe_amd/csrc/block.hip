@@ -36,9 +36,17 @@ __device__ __forceinline__ float blk_swiglu(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-// Part `slot` of the rows: groups in ascending order, each in parts of kRows rows (the
-// last one shorter).  False past the last part.  Offsets outside the rows are cut off,
-// so whatever the table holds, no row outside them is named.  Uniform in the wave.
+// Parts of at most `part` rows that `rows` rows of `groups` groups can fall into.  The kernels
+// take no more of them, whatever a table holds (where moe_dispatch_layout has reported an
+// error it may be anything: groups that overlap could make 2^34 of them).
+__host__ __device__ __forceinline__ int most_parts(int rows, int groups, int part) {
+    return rows / part + (groups < rows ? groups : rows);
+}
+
+// Part `slot` (below most_parts) of the rows: groups in ascending order, each in parts of kRows
+// rows (the last one shorter).  False past the last part.  Offsets outside the rows are cut off
+// and the count of parts ends at kParts, which no slot reaches, so whatever the table holds, no
+// row outside them is named.  Uniform in the wave.
 template <int kRows>
 __device__ __forceinline__ bool find_part(const int32_t* offsets, int groups, int rows, int slot, int& g, int& row0,
                                           int& count) {
@@ -48,6 +56,7 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int groups, in
         count = min(rows - row0, kRows);
         return count > 0;
     }
+    constexpr int kParts = 1 << 29;  // (a lane has at most 2^10 groups of 2^24 rows: 2^28 parts)
     const int lane = threadIdx.x & 63, per = (groups + kWave - 1) / kWave;
     int lo = 0, hi = 0, mine = 0;  // of the lane's groups: the last one's bounds, their parts
     for (int i = 0; i < per; ++i) {
@@ -60,7 +69,7 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int groups, in
 #pragma unroll
     for (int s = 1; s < kWave; s *= 2) {
         const int v = __shfl_up(upto, s, kWave);
-        if (lane >= s) upto += v;
+        if (lane >= s) upto = min(upto + v, kParts);
     }
     const uint64_t past = __ballot(upto > slot);
     if (!past) return false;
@@ -290,7 +299,8 @@ template <int kNF, bool kGlu, bool kPast>
 __global__ __launch_bounds__(kBfWaves * kWave, 2) void block_few_kernel(BlockGemm a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_w[kBfWaves][2][kBfSlot];
     int g, row0, count;
-    for (int slot = blockIdx.y; find_part<kBfRows>(a.offsets, a.groups, a.rows, slot, g, row0, count);
+    const int most = most_parts(a.rows, a.groups, kBfRows);
+    for (int slot = blockIdx.y; slot < most && find_part<kBfRows>(a.offsets, a.groups, a.rows, slot, g, row0, count);
          slot += gridDim.y) {
         const int n0 = blockIdx.x * 16 * kNF;
         if (count <= 16) block_few_part<kNF, 1, kGlu, kPast>(a, g, row0, count, n0, s_w);
@@ -403,6 +413,7 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
     const int KB = blk_count(p.k), NB = blk_count(p.n), NT = (p.n + kCols - 1) / kCols;
 
     if (wave == 0) {
+        const int most = most_parts(p.rows, p.groups, C::kM);
         int before = 0;
         for (int e0 = 0; e0 < p.groups; e0 += kWave) {
             const int e = e0 + lane;
@@ -419,13 +430,13 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
                 if (lane >= s) upto += v;
             }
             if (e < p.groups) {
-                s_first[e] = before + upto - tiles;
+                s_first[e] = min(before + upto - tiles, most);
                 s_lo[e] = lo;
                 s_hi[e] = hi;
             }
             before += __shfl(upto, kWave - 1, kWave);
         }
-        if (lane == 0) s_first[p.groups] = before;
+        if (lane == 0) s_first[p.groups] = min(before, most);
     }
     __syncthreads();
     // Workgroup b runs on XCD b % 8, whose workgroups take neighbouring tiles, so that they
@@ -803,9 +814,6 @@ template <class C, bool kGlu, bool kPast>
 __global__ __launch_bounds__(kBgThreads, 2) void block_gemm_kernel(BlockGemm p) {
     block_gemm_tiles<C, kGlu, kPast>(p);
 }
-
-// Parts of at most `part` rows that `rows` rows of `groups` groups can fall into.
-static int most_parts(int rows, int groups, int part) { return rows / part + (groups < rows ? groups : rows); }
 
 using Bg256x256 = BgShape<4, 2, 2, 4, 2>;
 using Bg128x256 = BgShape<4, 2, 1, 4, 2>;

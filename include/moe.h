@@ -512,7 +512,9 @@ moe_status moe_block_dequantize(int64_t rows, int32_t cols, int32_t n, const uin
  *       ascending from 0, as moe_dispatch_layout writes it; NULL with groups = 1:
  *       every row.  A group may be empty; bounds outside the rows are cut off, a
  *       last bound of -1 (moe_dispatch_layout's error report) leaves the last group
- *       without rows, and rows of no group are left as they were;
+ *       without rows, and rows of no group are left as they were.  A table that does
+ *       not ascend (the rest of one behind that report may be anything) gives rows
+ *       unspecified values, in no more time, and touches nothing outside the buffers;
  *   w uint8 [groups, n, k], w_scales fp32 [groups][ceil(n/128)][ceil(k/128)];
  *   out bf16 [rows, n].
  * moe_block_gemm_swiglu is the gate and up products with SwiGLU behind them:

@@ -647,6 +647,41 @@ def test_bounds_outside_the_rows(gpu_lib, n, k, rows, glu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("groups,n,k,rows", [(5, 144, 400, 60), (40, 1032, 400, 4100), (40, 528, 656, 7000), (3, 2064, 272, 9000),
+                                             (600, 136, 272, 1300), (16384, 8, 16, 1 << 24)])
+def test_a_table_of_anything(gpu_lib, groups, n, k, rows):
+    """moe_dispatch_layout leaves the table unwritten where it reports an error, and the calls behind it are under
+    way by then: they end, and write nothing outside their outputs.  (The last case: groups of all rows would make
+    2^31 parts.)"""
+    g = torch.Generator(device="cuda").manual_seed(groups)
+    draw = lambda *shape: torch.randint(0, 120, shape, generator=g, device="cuda", dtype=torch.uint8)
+    scales = lambda *shape: torch.ones(shape, device="cuda")
+    a, sa, w = draw(rows, k), scales((k + 127) // 128, rows), draw(groups, n, k)
+    sw = scales(groups, (n + 127) // 128, (k + 127) // 128)
+    buf = torch.full((rows + 512, n), 77, dtype=torch.bfloat16, device="cuda")
+    tables = [torch.randint(-(1 << 31), 1 << 31, (groups + 1,), generator=g, device="cuda").int(),
+              torch.randint(0, rows + 1, (groups + 1,), generator=g, device="cuda").int(),
+              (torch.arange(groups + 1, device="cuda") % 2 * rows).int(),
+              torch.arange(groups, -1, -1, device="cuda").mul(rows // groups).int()]
+    for off in tables:
+        print("table %s ..." % off[:4].tolist(), flush=True)
+        moe.moe_block_gemm(a, sa, w, sw, buf[256:-256], offsets=off)
+        torch.cuda.synchronize()
+        assert (buf[:256] == 77).all() and (buf[-256:] == 77).all()
+        if n % 16:
+            continue
+        nb = (n + 127) // 128
+        ws = torch.empty(moe.moe_query_block_swiglu(rows, n, k, groups), dtype=torch.uint8, device="cuda")
+        hq = torch.full((rows + 512, n), 77, dtype=torch.uint8, device="cuda")
+        hs = torch.full((nb * rows + 512,), 77.0, device="cuda")
+        moe.moe_block_gemm_swiglu(a, sa, w, sw, w, sw, hq[256:-256], hs[256:-256].view(nb, rows), ws,
+                                  h=buf[256:-256], offsets=off)
+        torch.cuda.synchronize()
+        for t in (buf, hq, hs):
+            assert (t[:256] == 77).all() and (t[-256:] == 77).all()
+
+
+@pytest.mark.gpu
 def test_extreme_scales(gpu_lib):
     """Scales far apart whose products are normal numbers, and a result that overflows."""
     a = torch.full((2, 256), 448.0).to(torch.float8_e4m3fn)
