@@ -243,8 +243,9 @@ torch = None  # until a call is given tensors: building, sizing and validating n
 
 def _use_torch():
     """torch, and its tensors' methods as functions: looked up once, not for each of a call's tensors."""
-    global torch, _numel, _is_contiguous, _get_device, _data_ptr, _GRAD_KINDS
+    global torch, _numel, _is_contiguous, _get_device, _data_ptr, _GRAD_KINDS, _CODE_KINDS
     import torch
+    _CODE_KINDS = torch.uint8, torch.float8_e4m3fn
     _GRAD_KINDS = {torch.float32: 0, torch.bfloat16: 1}
     _numel, _is_contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
     _get_device, _data_ptr = torch.Tensor.get_device, torch.Tensor.data_ptr
@@ -359,6 +360,15 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _codes(fn, device, t, n):
+    """_dense of E4M3 codes: as bytes, or in torch's own type for them, in which a checkpoint's arrive."""
+    if t is None:
+        return None
+    if t.dtype not in _CODE_KINDS or _numel(t) < n or not _is_contiguous(t) or _get_device(t) != device:
+        raise MoeError(fn, MOE_E_INVALID)
+    return _data_ptr(t)
+
+
 def _row_scales(fn, device, t, rows, cols):
     """The pointer of the scales [ceil(cols / 128), rows] of rows in blocks of 128.  A matrix of more columns
     would be read in another order: refused."""
@@ -372,14 +382,14 @@ def moe_dispatch_rows(x, tok_row, dst=None, codes=None, scales=None, stream=None
     (moe_block_quantize's); rows outside theirs are no rows."""
     if torch is None:
         _use_torch()
-    fn, dev, b16, f32, u8 = "moe_dispatch_rows", x.get_device(), torch.bfloat16, torch.float32, torch.uint8
+    fn, dev, b16 = "moe_dispatch_rows", x.get_device(), torch.bfloat16
     T, cols = _sizes(fn, *x.shape)
     k = tok_row.shape[1]
     R = dst.shape[0] if dst is not None else codes.shape[0] if codes is not None else 0
     if codes is not None and codes.shape[0] != R:
         raise MoeError(fn, MOE_E_INVALID)
     _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, x, b16, 0), _dense(fn, dev, tok_row, torch.int32, T * k),
-          _dense(fn, dev, dst, b16, R * cols), _dense(fn, dev, codes, u8, R * cols),
+          _dense(fn, dev, dst, b16, R * cols), _codes(fn, dev, codes, R * cols),
           _row_scales(fn, dev, scales, R, cols))
 
 
@@ -401,7 +411,7 @@ def moe_combine_rows_bwd(dout, tok_row, src=None, topk_w=None, dsrc=None, dw=Non
     dw[t, j] = <src[tok_row[t, j]], dout[t]>."""
     if torch is None:
         _use_torch()
-    fn, dev, b16, f32, u8 = "moe_combine_rows_bwd", dout.get_device(), torch.bfloat16, torch.float32, torch.uint8
+    fn, dev, b16, f32 = "moe_combine_rows_bwd", dout.get_device(), torch.bfloat16, torch.float32
     T, cols = _sizes(fn, *dout.shape)
     k = tok_row.shape[1]
     rows = {t.shape[0] for t in (src, dsrc, codes) if t is not None}
@@ -410,7 +420,7 @@ def moe_combine_rows_bwd(dout, tok_row, src=None, topk_w=None, dsrc=None, dw=Non
     R = rows.pop() if rows else 0
     _call(fn, dev, stream, T, k, cols, R, _dense(fn, dev, dout, b16, 0), _dense(fn, dev, src, b16, R * cols),
           _dense(fn, dev, tok_row, torch.int32, T * k), _dense(fn, dev, topk_w, f32, T * k),
-          _dense(fn, dev, dsrc, b16, R * cols), _dense(fn, dev, codes, u8, R * cols),
+          _dense(fn, dev, dsrc, b16, R * cols), _codes(fn, dev, codes, R * cols),
           _row_scales(fn, dev, scales, R, cols), _dense(fn, dev, dw, f32, T * k))
 
 
@@ -421,7 +431,7 @@ def moe_block_quantize(src, codes, scales, stream=None):
     fn, dev = "moe_block_quantize", src.get_device()
     rows, cols = _sizes(fn, *src.shape)
     _call(fn, dev, stream, rows, cols, _dense(fn, dev, src, torch.bfloat16, 0),
-          _dense(fn, dev, codes, torch.uint8, rows * cols), _row_scales(fn, dev, scales, rows, cols))
+          _codes(fn, dev, codes, rows * cols), _row_scales(fn, dev, scales, rows, cols))
 
 
 def moe_block_quantize_weights(src, codes, scales, transposed=False, stream=None):
@@ -434,8 +444,7 @@ def moe_block_quantize_weights(src, codes, scales, transposed=False, stream=None
     if max(groups, n, k) >= 1 << 31:
         raise MoeError(fn, MOE_E_UNSUPPORTED)
     _call(fn, dev, stream, groups, n, k, _dense(fn, dev, src, torch.bfloat16, groups * n * k), 1 if transposed else 0,
-          _dense(fn, dev, codes, torch.uint8, 0),
-          _dense(fn, dev, scales, torch.float32, groups * _blocks(n) * _blocks(k)))
+          _codes(fn, dev, codes, 0), _dense(fn, dev, scales, torch.float32, groups * _blocks(n) * _blocks(k)))
 
 
 def moe_block_dequantize(codes, scales, dst, weights=False, stream=None):
@@ -449,7 +458,7 @@ def moe_block_dequantize(codes, scales, dst, weights=False, stream=None):
         raise MoeError(fn, MOE_E_UNSUPPORTED)
     s = _dense(fn, dev, scales, torch.float32, codes.shape[0] * _blocks(n) * _blocks(cols)) if weights else \
         _row_scales(fn, dev, scales, rows, cols)
-    _call(fn, dev, stream, rows, cols, n, _dense(fn, dev, codes, torch.uint8, rows * cols), s,
+    _call(fn, dev, stream, rows, cols, n, _codes(fn, dev, codes, rows * cols), s,
           _dense(fn, dev, dst, torch.bfloat16, rows * cols))
 
 
@@ -461,8 +470,7 @@ def _block_operands(fn, dev, a, a_scales, offsets, w):
         raise MoeError(fn, MOE_E_INVALID)
     if max(groups, n) >= 1 << 31:
         raise MoeError(fn, MOE_E_UNSUPPORTED)
-    return (rows, n, k, groups), (_dense(fn, dev, a, torch.uint8, 0),
-                                  _row_scales(fn, dev, a_scales, rows, k),
+    return (rows, n, k, groups), (_codes(fn, dev, a, 0), _row_scales(fn, dev, a_scales, rows, k),
                                   _dense(fn, dev, offsets, torch.int32, groups + 1))
 
 
@@ -473,7 +481,7 @@ def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None):
         _use_torch()
     fn, dev = "moe_block_gemm", a.get_device()
     (rows, n, k, groups), ptrs = _block_operands(fn, dev, a, a_scales, offsets, w)
-    _call(fn, dev, stream, rows, n, k, groups, *ptrs, _dense(fn, dev, w, torch.uint8, 0),
+    _call(fn, dev, stream, rows, n, k, groups, *ptrs, _codes(fn, dev, w, 0),
           _dense(fn, dev, w_scales, torch.float32, groups * _blocks(n) * _blocks(k)),
           _dense(fn, dev, out, torch.bfloat16, rows * n))
 
@@ -493,13 +501,13 @@ def moe_block_gemm_swiglu(a, a_scales, wg, wg_scales, wu, wu_scales, h_codes, h_
     [ceil(n / 128), rows], and in bf16 where h is given; ws: moe_query_block_swiglu bytes."""
     if torch is None:
         _use_torch()
-    fn, dev, f32, u8 = "moe_block_gemm_swiglu", a.get_device(), torch.float32, torch.uint8
+    fn, dev, f32 = "moe_block_gemm_swiglu", a.get_device(), torch.float32
     (rows, n, k, groups), ptrs = _block_operands(fn, dev, a, a_scales, offsets, wg)
     if wu.shape != wg.shape:
         raise MoeError(fn, MOE_E_INVALID)
     n_s = groups * _blocks(n) * _blocks(k)
-    _call(fn, dev, stream, rows, n, k, groups, *ptrs, _dense(fn, dev, wg, u8, 0), _dense(fn, dev, wg_scales, f32, n_s),
-          _dense(fn, dev, wu, u8, 0), _dense(fn, dev, wu_scales, f32, n_s), _dense(fn, dev, h_codes, u8, rows * n),
+    _call(fn, dev, stream, rows, n, k, groups, *ptrs, _codes(fn, dev, wg, 0), _dense(fn, dev, wg_scales, f32, n_s),
+          _codes(fn, dev, wu, 0), _dense(fn, dev, wu_scales, f32, n_s), _codes(fn, dev, h_codes, rows * n),
           _row_scales(fn, dev, h_scales, rows, n), _dense(fn, dev, h, torch.bfloat16, rows * n),
           *_buffer(fn, dev, ws))
 

@@ -538,6 +538,46 @@ def test_weights_past_the_last_cache(gpu_lib, counts, glu):
 
 
 @pytest.mark.gpu
+def test_codes_in_torch_s_own_type(gpu_lib):
+    """Every call takes torch.float8_e4m3fn where it takes bytes, and gives the same bits; other 8-bit types are refused."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    T, k, H, I, E = 20, 2, 272, 144, 3
+    R, f8 = T * k, torch.float8_e4m3fn
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    W = [torch.randn(E, *s, generator=g, device="cuda").mul(0.1).bfloat16() for s in ((H, I), (H, I), (I, H))]
+    at = torch.randperm(R, generator=g, device="cuda").view(T, k).int()
+    off, topk_w = _offsets([13, 0, 27]).cuda(), torch.rand(T, k, generator=g, device="cuda")
+    new = lambda dtype, *shape: torch.zeros(*shape, dtype=torch.uint8, device="cuda").view(dtype)
+    scales = lambda *shape: torch.zeros(shape, device="cuda")
+    ws = torch.empty(moe.moe_query_block_swiglu(R, I, H, E), dtype=torch.uint8, device="cuda")
+
+    def layer(dtype):
+        xq, xs, hq, hs = new(dtype, R, H), scales(3, R), new(dtype, R, I), scales(2, R)
+        w = []
+        for v in W:
+            kk, n = v.shape[1:]
+            w += [new(dtype, E, n, kk), scales(E, (n + 127) // 128, (kk + 127) // 128)]
+            moe.moe_block_quantize_weights(v, w[-2], w[-1], transposed=True)
+        moe.moe_dispatch_rows(x, at, codes=xq, scales=xs)
+        moe.moe_block_gemm_swiglu(xq, xs, *w[:4], hq, hs, ws, offsets=off)
+        y, held, back = (torch.zeros(R, n, dtype=torch.bfloat16, device="cuda") for n in (H, I, H))
+        moe.moe_block_gemm(hq, hs, *w[4:], y, offsets=off)
+        moe.moe_block_dequantize(hq, hs, held)
+        dq, ds, bq, bs = new(dtype, R, H), scales(3, R), new(dtype, R, H), scales(3, R)
+        moe.moe_block_quantize(y, dq, ds)
+        moe.moe_combine_rows_bwd(x, at, topk_w=topk_w, codes=bq, scales=bs)
+        wv = torch.zeros(E, H, I, dtype=torch.bfloat16, device="cuda")
+        moe.moe_block_dequantize(*w[4:], wv, weights=True)
+        return [t.view(torch.uint8) for t in (xq, xs, hq, hs, *w, y, held, dq, ds, bq, bs, wv)]
+
+    assert all(torch.equal(a, b) for a, b in zip(layer(torch.uint8), layer(f8)))
+    for other in (torch.int8, torch.float8_e5m2, torch.float8_e4m3fnuz):
+        with pytest.raises(moe.MoeError) as e:
+            layer(other)
+        assert e.value.status == moe.MOE_E_INVALID
+
+
+@pytest.mark.gpu
 def test_turned_weights_give_the_input_gradient(gpu_lib):
     """dA = dOut W: the product with the same blocks turned, against the formula and against a difference."""
     g = torch.Generator().manual_seed(3)
