@@ -230,6 +230,102 @@ def test_combine_backward(gpu_lib, T, k, H, dropped, spare):
             assert (codes[:-1][~named] == 77).all() and (scales[:, ~named] == 77).all() and (codes[-1] == 77).all()
 
 
+# Tokens enough to fill the CUs (one workgroup walks a row in several pieces), rows wider than a 1024-thread
+# workgroup covers at once, and rows past the last cache's 256 MB: T, k, H, dropped, spare
+LARGE = [(2100, 3, 2064, 0.1, 5), (2100, 9, 2064, 0.0, 0), (2500, 3, 4112, 0.2, 0), (2100, 9, 4112, 0.1, 3), (2051, 2, 7168, 0.0, 1),
+         (16500, 4, 128, 0.1, 0), (33000, 1, 48, 0.0, 2), (3, 2, 8208, 0.0, 0), (5, 9, 16400, 0.3, 1), (1023, 2, 2064, 0.1, 0),
+         (1024, 2, 2064, 0.1, 0), (5000, 6, 8208, 0.1, 0), (10000, 8, 4112, 0.1, 0)]
+
+
+def _large(T, k, H, dropped, spare, seed):
+    g = torch.Generator().manual_seed(seed)
+    at, rows = _table(g, T, k, dropped, spare)
+    kept = (at >= 0) & (at < rows)
+    t_of, j_of = (v.cuda() for v in kept.nonzero(as_tuple=True))
+    r_of = at[kept].long().cuda()  # row r_of[i] is that of choice (t_of[i], j_of[i])
+    free = torch.ones(rows, dtype=torch.bool, device="cuda")
+    free[r_of] = False
+    return torch.Generator(device="cuda").manual_seed(seed), at.cuda(), rows, t_of, j_of, r_of, free
+
+
+def _normal(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,dropped,spare", LARGE)
+def test_dispatch_of_many_tokens_and_wide_rows(gpu_lib, T, k, H, dropped, spare):
+    g, at, rows, t_of, _, r_of, free = _large(T, k, H, dropped, spare, T + k + H)
+    x, nb = _normal(g, T, H), (H + 127) // 128
+    dst = _guarded(rows, H)
+    moe.moe_dispatch_rows(x, at, dst=dst[:-1])
+    assert torch.equal(dst[r_of], x[t_of]) and (dst[:-1][free] == 77).all() and (dst[-1] == 77).all()
+    q, s = torch.zeros(T, H, dtype=torch.uint8, device="cuda"), torch.zeros(nb, T, device="cuda")
+    moe.moe_block_quantize(x, q, s)
+    for with_dst in (False, True):
+        codes, scales, dst2 = _guarded(rows, H, dtype=torch.uint8), torch.full((nb, rows), 77.0, device="cuda"), _guarded(rows, H)
+        moe.moe_dispatch_rows(x, at, dst=dst2[:-1] if with_dst else None, codes=codes[:-1], scales=scales)
+        assert torch.equal(codes[r_of], q[t_of]) and torch.equal(scales[:, r_of], s[:, t_of])
+        assert (codes[:-1][free] == 77).all() and (codes[-1] == 77).all() and (scales[:, free] == 77).all()
+        assert torch.equal(dst2, dst) if with_dst else (dst2 == 77).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,dropped,spare", LARGE)
+def test_combine_of_many_tokens_and_wide_rows(gpu_lib, T, k, H, dropped, spare):
+    g, at, rows, t_of, j_of, r_of, _ = _large(T, k, H, dropped, spare, T + k + H + 1)
+    src, add, w = _normal(g, rows, H), _normal(g, T, H), _normal(g, T, k, dtype=torch.float32)
+    for ww, aa in ((None, None), (w, add)):
+        out = _guarded(T, H)
+        moe.moe_combine_rows(src, at, out[:-1], topk_w=ww, add=aa)
+        want = torch.zeros(T, H, dtype=torch.float64, device="cuda") if aa is None else aa.double()
+        size = want.abs()
+        for j in range(k):
+            i = (j_of == j).nonzero()[:, 0]
+            term = src[r_of[i]].double() * (1.0 if ww is None else ww[t_of[i], j, None].double())
+            want[t_of[i]] += term
+            size[t_of[i]] += term.abs()
+        assert ((out[:-1].double() - want).abs() <= want.abs() * HALF + (k + 1) * 2.0 ** -24 * size * 1.01).all()
+        assert (out[-1] == 77).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,dropped,spare", LARGE)
+def test_combine_backward_of_many_tokens_and_wide_rows(gpu_lib, T, k, H, dropped, spare):
+    """A dot product goes over H / 2048 pieces of a row in at most H / 256 / 8 + 8 additions of a lane and the joins of
+    ten steps and 16 waves: (H / 16 + 40) 2^-24 of the sum of magnitudes covers it."""
+    g, at, rows, t_of, j_of, r_of, free = _large(T, k, H, dropped, spare, T + k + H + 2)
+    src, dout, w = _normal(g, rows, H), _normal(g, T, H), _normal(g, T, k, dtype=torch.float32)
+    d, dw = _guarded(rows, H), torch.full((T * k + 1,), 77.0, device="cuda")
+    moe.moe_combine_rows_bwd(dout, at, src=src, topk_w=w, dsrc=d[:-1], dw=dw[:-1].view(T, k))
+    got = dw[:-1].view(T, k)
+    assert dw[-1] == 77 and (d[-1] == 77).all() and (d[:-1][free] == 77).all()
+    want_dw, size = torch.zeros(T, k, dtype=torch.float64, device="cuda"), torch.zeros(T, k, dtype=torch.float64, device="cuda")
+    for j in range(k):
+        i = (j_of == j).nonzero()[:, 0]
+        grad = dout[t_of[i]].double() * w[t_of[i], j, None].double()
+        assert ((d[r_of[i]].double() - grad).abs() <= grad.abs() * (HALF + 2.0 ** -24)).all()
+        terms = src[r_of[i]].double() * dout[t_of[i]].double()
+        want_dw[t_of[i], j], size[t_of[i], j] = terms.sum(1), terms.abs().sum(1)
+    assert ((got.double() - want_dw).abs() <= (H / 16 + 40) * 2.0 ** -24 * size).all()
+    # each output alone, in place, and as codes of the rounded gradient: the same bits
+    d2, dw2 = _guarded(rows, H), torch.empty(T, k, device="cuda")
+    moe.moe_combine_rows_bwd(dout, at, topk_w=w, dsrc=d2[:-1])
+    moe.moe_combine_rows_bwd(dout, at, src=src, topk_w=w, dw=dw2)
+    assert torch.equal(d2, d) and torch.equal(dw2, got)
+    buf = src.clone()
+    moe.moe_combine_rows_bwd(dout, at, src=buf, topk_w=w, dsrc=buf, dw=dw2)
+    assert torch.equal(buf[r_of], d[r_of]) and torch.equal(buf[free], src[free]) and torch.equal(dw2, got)
+    nb = (H + 127) // 128
+    q, s = torch.zeros(rows, H, dtype=torch.uint8, device="cuda"), torch.zeros(nb, rows, device="cuda")
+    moe.moe_block_quantize(d[:-1], q, s)
+    codes, scales = _guarded(rows, H, dtype=torch.uint8), torch.full((nb, rows), 77.0, device="cuda")
+    moe.moe_combine_rows_bwd(dout, at, src=src, topk_w=w, dsrc=d2[:-1], codes=codes[:-1], scales=scales, dw=dw2)
+    assert torch.equal(codes[r_of], q[r_of]) and torch.equal(scales[:, r_of], s[:, r_of])
+    assert torch.equal(d2, d) and torch.equal(dw2, got)
+    assert (codes[:-1][free] == 77).all() and (codes[-1] == 77).all() and (scales[:, free] == 77).all()
+
+
 @pytest.mark.gpu
 def test_gradients_against_differences(gpu_lib):
     """d/dw and d/dsrc of sum(out * dout): out is linear in each, so a difference of any step is exact up to
