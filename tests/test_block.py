@@ -642,6 +642,108 @@ def test_product_nan_codes_and_offsets_outside(gpu_lib):
         assert torch.equal(out.cpu(), want.float().bfloat16())
 
 
+# rows, groups, n, k that fall to the few-row form and to each of the tiles (of the plain product, and with SwiGLU)
+FORMS = [(60, 2, 144, 400), (4100, 40, 1040, 656), (12000, 3, 4112, 272), (1500, 40, 1040, 144), (2300, 40, 272, 656),
+         (700, 40, 1040, 656), (300, 40, 4112, 272), (1300, 600, 144, 272)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,groups,n,k", FORMS)
+def test_nan_codes_reach_their_own_outputs_only(gpu_lib, rows, groups, n, k):
+    g = torch.Generator().manual_seed(rows + n)
+    counts = _uneven(rows, groups)
+    rows = sum(counts)
+    a, sa, w, sw = _operands(g, rows, k, groups, n, True)
+    sw = sw * 2.0 ** -8
+    off = _offsets(counts)
+    e = max(range(groups), key=lambda i: counts[i])  # the group whose matrix is spoilt
+    lo, hi = off[e].item(), off[e + 1].item()
+    r0 = 0 if e else hi if hi < rows else 0
+    r0 = r0 if not lo <= r0 < hi else rows - 1
+    a2, w2 = a.view(torch.uint8).clone(), w.view(torch.uint8).clone()
+    a2[r0, k - 1], w2[e, n - 5, 5] = 0x7f, 0xff
+    bad = torch.zeros(rows, n, dtype=torch.bool, device="cuda")
+    bad[r0], bad[lo:hi, n - 5] = True, True
+    sa, sw, off = sa.cuda(), sw.cuda(), off.cuda()
+    outs = []
+    for ac, wc in ((u8(a), u8(w)), (a2.cuda(), w2.cuda())):
+        out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+        moe.moe_block_gemm(ac, sa, wc, sw, out, offsets=off)
+        ws = torch.empty(moe.moe_query_block_swiglu(rows, n, k, groups), dtype=torch.uint8, device="cuda")
+        hq, hs = torch.empty(rows, n, dtype=torch.uint8, device="cuda"), torch.empty((n + 127) // 128, rows, device="cuda")
+        h = torch.empty_like(out)
+        moe.moe_block_gemm_swiglu(ac, sa, u8(w), sw, wc, sw, hq, hs, ws, h=h, offsets=off)
+        outs.append((out, h, hq.view(torch.float8_e4m3fn).float(), hs))
+    (out, h, hq, hs), (out2, h2, hq2, hs2) = outs
+    for x, y in ((out, out2), (h, h2)):
+        assert torch.isnan(y[bad]).all() and torch.equal(x[~bad], y[~bad])
+    assert torch.isnan(hq2[bad]).all() and not torch.isnan(hq2[~bad]).any()
+    # the block's scale comes from the other values: it differs where the spoilt one was the largest
+    same = (hs == hs2).t().repeat_interleave(128, 1)[:, :n] & ~bad
+    assert torch.equal(hq[same], hq2[same]) and same[~bad].float().mean() > 0.9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,groups,n,k", FORMS)
+def test_a_captured_graph_follows_new_offsets(gpu_lib, rows, groups, n, k):
+    """Both products captured once and replayed on other tables, operands and scales in the same buffers."""
+    g = torch.Generator().manual_seed(rows + n + 1)
+    counts = _uneven(rows, groups)
+    rows = sum(counts)
+    sets = []
+    for i in range(3):
+        a, sa, w, sw = _operands(g, rows, k, groups, n)
+        turned = counts[i % groups:] + counts[:i % groups]
+        if i == 2:
+            turned[0] = 0  # fewer rows than the buffers hold
+        sets.append((u8(a), sa.cuda(), u8(w), sw.cuda() * 1e-4, _offsets(turned).cuda()))
+    bufs = [t.clone() for t in sets[0]]
+    a, sa, w, sw, off = bufs
+    out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    hq, hs = torch.empty(rows, n, dtype=torch.uint8, device="cuda"), torch.empty((n + 127) // 128, rows, device="cuda")
+    h, ws = torch.empty_like(out), torch.empty(moe.moe_query_block_swiglu(rows, n, k, groups), dtype=torch.uint8, device="cuda")
+
+    def step():
+        moe.moe_block_gemm(a, sa, w, sw, out, offsets=off)
+        moe.moe_block_gemm_swiglu(a, sa, w, sw, w, sw, hq, hs, ws, h=h, offsets=off)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new in sets + sets[:1]:
+        for t, v in zip(bufs, new):
+            t.copy_(v)
+        res = []
+        for run in (step, graph.replay):
+            for t in (out, hq, hs, h, ws):
+                t.fill_(7)
+            run()
+            torch.cuda.synchronize()
+            res.append([t.clone() for t in (out, hq, hs, h)])
+        assert all(torch.equal(x, y) for x, y in zip(*res))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,groups,n,k", FORMS)
+def test_extreme_scales_in_every_form(gpu_lib, rows, groups, n, k):
+    """Row scales of 2^100 and 2^-100 in turn; their products with the weights' go down to 2^-126, the smallest normal
+    number, and up to 2^110, at which no sum of whole numbers below 2^13 overflows: exact sums."""
+    g = torch.Generator().manual_seed(rows + n + 2)
+    counts = _uneven(rows, groups)
+    rows = sum(counts)
+    a, sa, w, sw = _operands(g, rows, k, groups, n, True)
+    off = _offsets(counts)
+    sa = torch.exp2(torch.tensor([100.0, -100.0])[torch.arange(rows) % 2]).expand_as(sa).contiguous()
+    for scale in (2.0 ** -26, 2.0 ** 10, 1.0):
+        sw = torch.full_like(sw, scale)
+        want, _ = _product(*_values(a.cuda(), sa.cuda(), w.cuda(), sw.cuda()), off)
+        out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+        moe.moe_block_gemm(u8(a), sa.cuda(), u8(w), sw.cuda(), out, offsets=off.cuda())
+        assert torch.equal(out, want.float().bfloat16())
+
+
 BOUNDS = [([-5, 25, 40, 1 << 20], [(0, 25, 0), (25, 40, 1), (40, None, 2)]), ([0, 25, 30, -1], [(0, 25, 0), (25, 30, 1)]),
           ([0, 1 << 30, 1 << 30, -1], [(0, None, 0)]), ([50000, 60000, 70000, 80000], []), ([0, 0, 0, -1], []),
           ([7, 7, 30, 30], [(7, 30, 1)])]
@@ -871,3 +973,55 @@ def test_the_layer_in_parts(gpu_lib, T, H, I, E, k):
     # h is held in 8 bits (2^-4 of a value at most, a third of that in the mean) and enters a sum of I terms:
     # against the unquantised h the output is off by about 2^-5.5 of its own size, at most
     assert (out.cpu().double() - want).norm() <= want.norm() * 2.0 ** -4.5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 128, 64, 8, 2), (9, 256, 144, 5, 3), (200, 384, 256, 4, 2), (2000, 512, 528, 6, 3)])
+def test_the_layer_in_parts_call_by_call(gpu_lib, T, H, I, E, k):
+    """The same run, each call against the formula in 64 bits on what the call before it gave: the codes of h that the
+    down product takes, its rows that the sum takes.  So no step's own quantisation stands in the next one's bound."""
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    packed = []
+    for n, kk in ((I, H), (I, H), (H, I)):
+        q, s = torch.empty(E, n, kk, dtype=torch.uint8, device="cuda"), torch.empty(E, (n + 127) // 128, (kk + 127) // 128, device="cuda")
+        moe.moe_block_quantize_weights(torch.randn(E, kk, n, generator=g, device="cuda").mul(0.05).bfloat16(), q, s, transposed=True)
+        packed.append((q, s))
+    cfg = moe.make_cfg(T, (H + 63) // 64 * 64, 64, E, k)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx, counts, offsets, row_token, tok_row = (torch.empty(s, **i32) for s in ((T, k), E, E + 1, T * k, (T, k)))
+    topk_w = torch.empty(T, k, device="cuda")
+    moe.moe_route(cfg, x, torch.randn(H, E, generator=g, device="cuda") * 0.05, None, idx, topk_w)
+    moe.moe_dispatch_layout(cfg, idx, counts, offsets, row_token, tok_row)
+    R = T * k
+    codes = lambda rows, cols: (torch.empty(rows, cols, dtype=torch.uint8, device="cuda"),
+                                torch.empty((cols + 127) // 128, rows, device="cuda"))
+    (xq, xs), (hq, hs) = codes(R, H), codes(R, I)
+    y, out = torch.empty(R, H, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    h = torch.empty(R, I, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(moe.moe_query_block_swiglu(R, I, H, E), dtype=torch.uint8, device="cuda")
+    moe.moe_dispatch_rows(x, tok_row, codes=xq, scales=xs)
+    moe.moe_block_gemm_swiglu(xq, xs, *packed[0], *packed[1], hq, hs, ws, h=h, offsets=offsets)
+    moe.moe_block_gemm(hq, hs, *packed[2], y, offsets=offsets)
+    moe.moe_combine_rows(y, tok_row, out, topk_w=topk_w)
+    torch.cuda.synchronize()
+    f8 = lambda t: t.view(torch.float8_e4m3fn)
+    off = offsets.cpu()
+    # x's codes are one rounding of x each, within half a step of E4M3 (2^-4 of it, 2^-10 of the scale below the normal codes)
+    sx = xs.double().t().repeat_interleave(128, 1)[:, :H]
+    rows = x[row_token.long()].double()
+    assert ((f8(xq).double() * sx - rows).abs() <= rows.abs() * 2.0 ** -4 + sx * 2.0 ** -10).all()
+    (gate, gs), (up, us) = (_product(*_values(f8(xq), xs, f8(q), s), off) for q, s in packed[:2])
+    hw = gate * torch.sigmoid(gate) * up
+    dg, du = gs * CUT, us * CUT
+    tol = 1.1 * dg * (up.abs() + du) + gate.abs() * du + hw.abs() * 2.0 ** -18
+    assert ((h.double() - hw).abs() <= (hw.abs() + tol) * HALF + tol).all()
+    sh = hs.double().t().repeat_interleave(128, 1)[:, :I]
+    held, near = f8(hq).double() * sh, h.double()
+    assert ((held - near).abs() <= near.abs() * (2.0 ** -4 + HALF) * 1.01 + sh * 2.0 ** -10).all()
+    yw, size = _product(*_values(f8(hq), hs, f8(packed[2][0]), packed[2][1]), off)
+    assert ((y.double() - yw).abs() <= yw.abs() * HALF + size * CUT * 1.01).all()
+    assert (y.double() - yw).norm() <= yw.norm() * HALF * 1.125
+    terms = y.double()[tok_row.long()] * topk_w.double()[..., None]
+    want, size = terms.sum(1), terms.abs().sum(1)
+    assert ((out.double() - want).abs() <= want.abs() * HALF + (k + 1) * 2.0 ** -24 * size * 1.01).all()
