@@ -31,11 +31,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t blk_rsrc(const void* p, uint32
 
 __device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 
-// silu(g) * u with the hardware's reciprocal (1 ulp) for the division
-__device__ __forceinline__ float blk_swiglu(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 // Parts of at most `part` rows that `rows` rows of `groups` groups can fall into.  The kernels
 // take no more of them, whatever a table holds (where moe_dispatch_layout has reported an
 // error it may be anything: groups that overlap could make 2^34 of them).
@@ -282,7 +277,7 @@ __device__ __forceinline__ void block_few_part(const BlockGemm& a, int g, int ro
             if constexpr (kGlu) {
                 const floatx4 u = joined(kNF + f);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = blk_swiglu(v[x], u[x]);
+                for (int x = 0; x < 4; ++x) v[x] = swiglu(v[x], u[x]);
             }
             if (r >= count || col >= a.n) continue;  // n is a multiple of 8: four columns are inside or not
             const int64_t at = (int64_t)(row0 + r) * a.n + col;
@@ -743,7 +738,7 @@ __device__ __forceinline__ void block_gemm_tiles(const BlockGemm& p) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float g = acc[i][j][c];
-                        const float h = blk_swiglu(g, acc[i][kJ + j][c]);  // (past column n: of zeros)
+                        const float h = swiglu(g, acc[i][kJ + j][c]);  // (past column n: of zeros)
                         acc[i][j][c] = h;
                         m[i] = fmaxf(m[i], fabsf(h));
                     }
