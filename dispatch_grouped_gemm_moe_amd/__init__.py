@@ -489,8 +489,8 @@ def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None):
 def moe_query_block_swiglu(rows, n, k, groups) -> int:
     """Bytes of moe_block_gemm_swiglu's workspace for so many rows or fewer."""
     fn, size = "moe_query_block_swiglu", ctypes.c_size_t()
-    if max(n, k, groups) >= 1 << 31 or rows >= 1 << 63:
-        raise MoeError(fn, MOE_E_UNSUPPORTED)
+    for v in n, k, groups:
+        _sizes(fn, rows, v)
     _check(fn, _load().moe_query_block_swiglu(rows, n, k, groups, ctypes.byref(size)))
     return size.value
 

@@ -71,6 +71,14 @@ def test_swiglu_workspace():
         assert e.value.status == want
 
 
+def test_swiglu_workspace_of_sizes_the_c_call_cannot_hold():
+    """Their low bits alone would be sizes that it takes."""
+    for sizes in ((4, 64 - (1 << 32), 64, 2), (4, 64, 64 - (1 << 32), 2), (4, 64, 64, 2 - (1 << 32)), (4 - (1 << 64), 64, 64, 2)):
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_query_block_swiglu(*sizes)
+        assert e.value.status == moe.MOE_E_UNSUPPORTED
+
+
 @pytest.mark.parametrize("n,k,groups", [(1024, 2048, 64), (2048, 7168, 32), (16, 13296, 26), (32, 3264, 1), (128, 128, 5),
                                         (144, 272, 256), (2048, 512, 600), (4096, 4096, 1), (528, 1040, 512)])
 def test_a_swiglu_workspace_serves_fewer_rows(n, k, groups):
