@@ -3,7 +3,9 @@
 //   norm = sqrt(sum over all tensors of g^2),  g' = g min(1, max_norm / (norm + 1e-6))
 //
 // Bound by memory: every value is read for the norm, and read and written again once
-// the norm is known.  The tensors' addresses travel in the kernel's arguments, so a
+// the norm is known.  Tensors that are not 16-byte aligned go element by element, for one
+// of 4.7e8 values: norm of fp32 276 -> 918 us, of bf16 232 -> 852, clip 637 -> 799 and 300
+// -> 698.  The tensors' addresses travel in the kernel's arguments, so a
 // call copies no table and a captured graph holds its own.
 #include "block8.hpp"
 #include "common.hpp"

@@ -71,7 +71,9 @@ __device__ __forceinline__ T ld_uniform(const T* p) {
 // ---------------------------------------------------------------------------
 
 // Measured: 16384 tokens of 7168 to 8 rows each 405 us (5.2 TB/s, mostly writes), as codes
-// 299 us (3.9 TB/s: scales of neighbouring rows are written by different XCDs).
+// 299 us (3.9 TB/s: scales of neighbouring rows are written by different XCDs), as both 1061
+// us (2.9 TB/s: a thread's two stores of bf16 each skip every other 16 bytes, past the caches),
+// more than the two calls.
 //
 // A workgroup takes kRowThreads >> log tokens at a time.  A thread has eight
 // consecutive values, or with codes sixteen, which leave as 16 bytes; a block's eight
@@ -298,7 +300,8 @@ void launch_rows_combine(const RowsCombine& a, hipStream_t stream) {
 // A token per group of 1 << log lanes, its columns in one go or one piece after the other:
 // the k dot products stay in registers over them and are joined once, in a fixed order.
 // kWide: one wave's lanes share a token, and its table's entries are scalars.  16384 tokens
-// of 7168 from 8 rows each: 766 us (5.2 TB/s).
+// of 7168 from 8 rows each: 766 us (5.2 TB/s); as codes alone 319 (3.8 TB/s), as codes with dw
+// 653 (4.7), with all three 1031 (4.8).
 template <int kK, bool kDot, bool kWide, bool kStream, int kThreads>
 __global__ __launch_bounds__(kThreads) void rows_combine_bwd_kernel(RowsCombineBwd a, int log, int64_t units) {
     __shared__ float s_dot[kThreads / kWave][kK];
