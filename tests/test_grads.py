@@ -207,6 +207,36 @@ def test_captured_replayed_and_on_another_stream(gpu_lib):
 
 
 @pytest.mark.gpu
+def test_two_calls_at_once(gpu_lib):
+    """Norm and clipping of two lists on two streams, a workspace each, while the other's run: as alone."""
+    g = torch.Generator().manual_seed(7)
+    jobs = []
+    for shapes in ([(3_000_001, F, 0), (70_000, B, 1)], [(5000, F, 0)] * 120):
+        grads = _grads(g, shapes)
+        out = [torch.empty_like(t) for t in grads]
+        norm, ws = torch.empty(1, device="cuda"), _ws(len(grads))
+
+        def run(stream, grads=grads, out=out, norm=norm, ws=ws):
+            moe.moe_grad_norm(grads, norm, ws, stream=stream)
+            moe.moe_clip_grads(grads, norm, 1.0, out=out, stream=stream)
+
+        run(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        jobs.append((run, (norm, *out), [t.clone() for t in (norm, *out)], torch.cuda.Stream(), ws))
+    for _, outs, *_ in jobs:
+        for t in outs:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for run, _, _, stream, _ in jobs:
+            run(stream)
+    torch.cuda.synchronize()
+    for _, outs, alone, _, ws in jobs:
+        assert all(torch.equal(x, y) for x, y in zip(outs, alone))
+        assert not ws[:moe.MOE_GRAD_COUNTER_BYTES].any()
+
+
+@pytest.mark.gpu
 def test_after_the_layers_backward(gpu_lib):
     """The gradients of moe_layer_bwd, clipped together in place, as a training step does."""
     T, H, I, E, k = 64, 128, 64, 8, 2

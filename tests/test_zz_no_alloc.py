@@ -70,6 +70,17 @@ def test_static_forward_clears_a_stale_status_word(gpu_lib):
     assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
 
 
+@pytest.mark.gpu
+def test_static_forward_reports_the_wait_site(gpu_lib):
+    """The caller's copy of the status word holds the code and the site (3: down tiles waited for gate|up), as
+    moe_read_device_status gives them."""
+    w = Workload("static_site", T=1500, H=256, I=128, E=8, k=2, minibatch=256, stream=8210)
+    cfg, bufs, x, Wr, bias, _ = _layer(make_inputs(w), w.T, flags=moe.MOE_F_DEBUG_DROP_SIGNAL)
+    assert moe.moe_read_device_status(bufs.ws) == (moe.MOE_E_DEVICE, moe.MOE_DEV_WAIT_TIMEOUT, 3)
+    _, status = _static(cfg, bufs, x, Wr, bias)
+    assert status == [moe.MOE_DEV_WAIT_TIMEOUT, 3]
+
+
 def test_static_forward_rejects_configs_beyond_the_static_workspace():
     """Checked on the host before any device call (runs without a GPU)."""
     cfg = moe.make_cfg(16384, 7168, 2048, 32, 8, minibatch=2560)
